@@ -57,6 +57,10 @@ typedef enum {
 
 typedef enum { W4A8_OUT_BF16 = 0, W4A8_OUT_F32 = 1 } w4a8_out_dtype;
 
+/* Element types of the router and of the unquantized (W16A16) products; the first two values are
+ * those of w4a8_out_dtype. */
+typedef enum { W4A8_BF16 = 0, W4A8_F32 = 1, W4A8_F16 = 2 } w4a8_dtype;
+
 /* Weight format description (P3 "Four independent dimensions": object, format,
  * granularity, execution types must each be stated).
  *   K, N        weight matrix W[K, N]
@@ -438,6 +442,89 @@ int w4a8_moe_forward_static(const void* X_bf16, const int32_t* topk_ids, const f
                             const w4a8_wdesc* gu_desc, const void* d_blobs, size_t d_stride,
                             const w4a8_wdesc* d_desc, const float* s_gu, const float* s_dn,
                             void* workspace, size_t workspace_bytes, void* out_bf16, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Router, and the expert-grouped products of the two formats beside W4A8
+ * ------------------------------------------------------------------------------------ */
+
+typedef enum { W4A8_ROUTE_SOFTMAX = 0, W4A8_ROUTE_SIGMOID = 1 } w4a8_route_score;
+
+/* How a router chooses experts.
+ *   E, k         experts (1..1024) and experts per token (1..min(E, 64))
+ *   score        p_i = softmax(x)_i over all E logits, or p_i = 1 / (1 + exp(-x_i))
+ *   renormalize  0 or 1: divide the k chosen scores by their sum (weights 0 if the sum is 0)
+ *   n_group, topk_group
+ *                experts in n_group groups of E / n_group neighbours, of which only the topk_group
+ *                best may be chosen from; n_group = 1 (or 0) turns groups off
+ *   scale        factor on every weight, applied last */
+typedef struct {
+    int32_t E;
+    int32_t k;
+    int32_t score;
+    int32_t renormalize;
+    int32_t n_group;
+    int32_t topk_group;
+    float scale;
+} w4a8_route_desc;
+
+/* Top-k routing of T tokens (P1 section 4.1 keeps the router in 16 bits, outside the quantized
+ * path): the topk_ids and topk_w that w4a8_moe_align, w4a8_moe_combine and the MoE layers take.
+ *   logits    device float32, bfloat16 or float16 (dtype) [T, E], row stride ldl >= E elements,
+ *             aligned to its element
+ *   bias      device float32 [E] or NULL: an offset used for the choice only, not for the weights
+ *   topk_ids  device int32 [T, k], best first; topk_w device float32 [T, k]
+ * Experts are ranked by their logit, or by p_i + bias_i in float64 if a bias is given; a group by
+ * its best expert, or with a bias by the sum of its two best.  Equal ranks go to the lower index.
+ * An expert whose logit (or bias) is -Inf is masked: never chosen; a -Inf logit also has p_i = 0.
+ * Where fewer than k
+ * can be chosen, the remaining entries are id -1 with weight 0, which w4a8_moe_align leaves out and
+ * w4a8_moe_combine skips (a padded token: all logits -Inf).  A row with a NaN logit or rank, or
+ * with a +Inf logit under softmax, has no order: it gets the ids 0..k-1 with NaN weights.
+ * Softmax and sigmoid are computed in float64 if a bias is given and in float32 otherwise.
+ * T == 0 is a no-op.  EINVAL: E, k or score out of range, n_group not dividing E, topk_group
+ * outside 1..n_group or leaving fewer than k experts, ldl < E, NULL or misaligned pointers;
+ * EUNSUPPORTED: E > 1024, k > 64, T > 2^24. */
+int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, const float* bias,
+                   const w4a8_route_desc* d, int32_t* topk_ids, float* topk_w, void* stream);
+
+/* Expert-grouped W8A8 GEMM (P1 section 5.3: W8A8 beside W4A8; P5 section 8.3: one scale per token
+ * and one per output channel): w4a8_moe_gemm for blobs of 8-bit codes with group_size = K,
+ *   Y[r, n] = sx[src] sw[e, n] sum_k Xq[src, k] q_e[k, n],
+ * the sum exact in int32, then float32, then rounded to nearest even for bfloat16.
+ *   d   weight_bits = 8, group_size = K, float32 scales, K < 133144; other formats EUNSUPPORTED
+ * Rows at or past expert_offsets[E] are not written.  Other arguments, bounds and errors as
+ * w4a8_moe_gemm; additionally EUNSUPPORTED for N > 2^20 or rows > 2^24. */
+int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather, int k,
+                       const int32_t* expert_offsets, int E, int rows, int src_rows,
+                       const void* blobs_dev, size_t expert_stride, const w4a8_wdesc* d, void* Y,
+                       int out_dtype, void* stream);
+
+/* Expert-grouped unquantized GEMM (P1 section 8: sensitive experts kept in a finer format):
+ *   Y[r, n] = sum_k X[src, k] W[e, n, k],
+ * the products exact and summed in float32, then rounded to nearest even if Y has 16 bits.
+ *   X         device bfloat16 or float16 (dtype) [src_rows, K], row stride ldx elements
+ *   W         device, same type, [E, N, K]: output channels by inputs, K contiguous, row stride ldw
+ *             and expert stride expert_stride, both in elements
+ *   Y         device [rows, N], row stride ldy; out_dtype is dtype or W4A8_F32
+ *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm
+ * K, ldx, ldw and expert_stride are multiples of 8, X and W 16-byte aligned (EINVAL); any N.  Rows
+ * at or past expert_offsets[E] are not written, nor is Y past column N.  A gather entry that
+ * names no row of X gives a row of zeros.  EUNSUPPORTED: N > 2^20, ldw > 2^23, rows > 2^24. */
+int w4a8_moe_gemm_w16a16(const void* X, int dtype, int ldx, const int32_t* gather, int k,
+                         const int32_t* expert_offsets, int E, int rows, int src_rows, const void* W,
+                         size_t expert_stride, int ldw, int K, int N, void* Y, int ldy, int out_dtype,
+                         void* stream);
+
+/* Expert-grouped unquantized gate/up GEMM with the gated activation in its epilogue (P1 section 1):
+ *   H[r, c] = silu(g) u,  g = sum_k X[src, k] W[e, c, k],  u = sum_k X[src, k] W[e, I + c, k],
+ * formed from the float32 sums and rounded once, so no [rows, 2I] intermediate is stored.
+ *   W   device [E, 2I, K]: the I gate rows, then the I up rows; any I
+ *   H   device [rows, I], row stride ldh, of type dtype
+ * Other arguments and errors as w4a8_moe_gemm_w16a16. */
+int w4a8_moe_gemm_silu_w16a16(const void* X, int dtype, int ldx, const int32_t* gather, int k,
+                              const int32_t* expert_offsets, int E, int rows, int src_rows,
+                              const void* W, size_t expert_stride, int ldw, int K, int I, void* H,
+                              int ldh, void* stream);
 
 /* Name of the kernel variant w4a8_gemm resolves to for (d, M), or "unsupported"
  * (P4: record target and resolved backend so a silent fallback is visible):

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_PKG, "libw4a8.so")
 
 W4A8_OK, W4A8_EINVAL, W4A8_ESIZE, W4A8_EUNSUPPORTED, W4A8_EHIP = 0, -1, -2, -3, -4
 W4A8_OUT_BF16, W4A8_OUT_F32 = 0, 1
+W4A8_BF16, W4A8_F32, W4A8_F16 = 0, 1, 2
+W4A8_ROUTE_SOFTMAX, W4A8_ROUTE_SIGMOID = 0, 1
 HEADER_BYTES = 256
 
 EXPORTED = [
@@ -29,6 +31,7 @@ EXPORTED = [
     "w4a8_quant_act_static", "w4a8_moe_quant_static", "w4a8_silu_mul_quant_static",
     "w4a8_moe_static_workspace_size", "w4a8_moe_forward_static", "w4a8_moe_forward_sets", "w4a8_moe_forward_noalloc",
     "w4a16_gemm", "w4a16_kernel_name",
+    "w4a8_moe_route", "w4a8_moe_gemm_w8a8", "w4a8_moe_gemm_w16a16", "w4a8_moe_gemm_silu_w16a16",
     "w4a8_kernel_name", "w4a8_status_string", "w4a8_version",
 ]
 
@@ -52,6 +55,11 @@ class ExpertSet(ctypes.Structure):
     _fields_ = [("n_experts", ctypes.c_int32), ("gu_blobs", ctypes.c_void_p), ("gu_stride", ctypes.c_size_t),
                 ("gu_desc", ctypes.POINTER(WDesc)), ("d_blobs", ctypes.c_void_p), ("d_stride", ctypes.c_size_t),
                 ("d_desc", ctypes.POINTER(WDesc))]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -91,6 +99,10 @@ def lib() -> ctypes.CDLL:
             "w4a8_moe_forward_static": (I, [P, P, P, I, I, I, P, SZ, DP, P, SZ, DP, P, P, P, SZ, P, VP]),
             "w4a8_moe_forward_sets": (I, [P, P, P, I, I, ctypes.POINTER(ExpertSet), I, P, SZ, P, VP]),
             "w4a8_moe_forward_noalloc": (I, [P, P, P, I, I, I, P, SZ, DP, P, SZ, DP, P, VP]),
+            "w4a8_moe_route": (I, [P, I, I, I, P, ctypes.POINTER(RouteDesc), P, P, VP]),
+            "w4a8_moe_gemm_w8a8": (I, [P, P, P, I, P, I, I, I, P, SZ, DP, P, I, VP]),
+            "w4a8_moe_gemm_w16a16": (I, [P, I, I, P, I, P, I, I, I, P, SZ, I, I, I, P, I, I, VP]),
+            "w4a8_moe_gemm_silu_w16a16": (I, [P, I, I, P, I, P, I, I, I, P, SZ, I, I, I, P, I, VP]),
             "w4a8_kernel_name": (ctypes.c_char_p, [DP, I]),
             "w4a16_gemm": (I, [P, I, I, P, DP, P, I, I, VP]),
             "w4a16_kernel_name": (ctypes.c_char_p, [DP, I]),
@@ -118,6 +130,21 @@ def desc(K: int, N: int, group_size: int, asymmetric: bool, bits: int = 4, scale
     """Weight descriptor; bits = 8 selects the symmetric INT8-weight (W8A8) form, scale_bits = 16
     binary16 group scales."""
     return WDesc(int(K), int(N), int(group_size), int(bool(asymmetric)), int(bits), int(scale_bits))
+
+
+def route_desc(E: int, k: int, score: int = W4A8_ROUTE_SOFTMAX, renormalize: bool = False, scale: float = 1.0,
+               n_group: int = 1, topk_group: int = 1) -> RouteDesc:
+    """How a router chooses: see w4a8_route_desc."""
+    return RouteDesc(int(E), int(k), int(score), int(bool(renormalize)), int(n_group), int(topk_group), float(scale))
+
+
+def _dtype(t) -> int:
+    """w4a8_dtype of a tensor."""
+    import torch
+    try:
+        return {torch.bfloat16: W4A8_BF16, torch.float32: W4A8_F32, torch.float16: W4A8_F16}[t.dtype]
+    except KeyError:
+        raise ValueError(f"{t.dtype} is not an element type of this call") from None
 
 
 def _ptr(x) -> int | None:
@@ -384,6 +411,73 @@ def w4a8_moe_forward_sets(X, topk_ids, topk_w, sets, workspace, out, stream=None
     _check(lib().w4a8_moe_forward_sets(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, arr, len(sets), _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
            "w4a8_moe_forward_sets")
+
+
+def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=None) -> None:
+    """Top-k routing: logits [T, E] (float32, bfloat16 or float16; rows may be strided) -> topk_ids int32 [T, k],
+    topk_w float32 [T, k]; bias: float32 [E] for the choice only."""
+    _require_cuda(logits, topk_ids, topk_w, bias)
+    T, E = logits.shape
+    if E != d.E or logits.stride(1) != 1:
+        raise ValueError("logits must be [T, E] with contiguous rows")
+    for t in (topk_ids, topk_w):
+        if t.shape != (T, d.k) or not t.is_contiguous():
+            raise ValueError("topk_ids and topk_w must be contiguous [T, k]")
+    if bias is not None and (bias.numel() != E or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous [E]")
+    _check_types(int32=(topk_ids,), float32=(topk_w, bias))
+    _check(lib().w4a8_moe_route(_ptr(logits), _dtype(logits), T, max(logits.stride(0), E), _ptr(bias), ctypes.byref(d),
+                                _ptr(topk_ids), _ptr(topk_w), _stream(stream)), "w4a8_moe_route")
+
+
+def _check_types(**kinds) -> None:
+    """Each keyword names a torch dtype; its tensors must have it (None is skipped)."""
+    for kind, tensors in kinds.items():
+        for t in tensors:
+            if t is not None and str(t.dtype) != "torch." + kind:
+                raise ValueError(f"expected torch.{kind}, got {t.dtype}")
+
+
+def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int, blobs_dev, expert_stride: int,
+                       d: WDesc, Y, out_dtype: int = W4A8_OUT_BF16, stream=None) -> None:
+    """Grouped W8A8 GEMM: w4a8_moe_gemm for 8-bit blobs with one scale per output channel (group_size = K)."""
+    _require_cuda(Xq, sx, gather, expert_offsets, blobs_dev, Y)
+    src_rows = int(Xq.shape[0])
+    if sx.numel() < src_rows:
+        raise ValueError("sx must hold one scale per row of Xq")
+    _check(lib().w4a8_moe_gemm_w8a8(_ptr(Xq), _ptr(sx), _ptr(gather), int(k), _ptr(expert_offsets), int(E), int(rows),
+                                    src_rows, _ptr(blobs_dev), int(expert_stride), ctypes.byref(d), _ptr(Y),
+                                    int(out_dtype), _stream(stream)), "w4a8_moe_gemm_w8a8")
+
+
+def _w16_args(X, gather, k, expert_offsets, W, Y, width: int):
+    """Checked arguments of the unquantized grouped products, up to and including the row stride of Y."""
+    _require_cuda(X, gather, expert_offsets, W, Y)
+    E, N, K = W.shape
+    if X.dtype != W.dtype or X.shape[1] != K or N != width * Y.shape[1]:
+        raise ValueError("X [src_rows, K], W [E, N, K] and Y do not match")
+    if X.stride(1) != 1 or W.stride(2) != 1 or Y.stride(1) != 1:
+        raise ValueError("the last dimension of X, W and Y must be contiguous")
+    if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < Y.shape[0]):
+        raise ValueError("expert_offsets must hold E + 1 entries and gather one per row of Y")
+    _check_types(int32=(expert_offsets, gather))
+    return (_ptr(X), _dtype(X), X.stride(0), _ptr(gather), int(k), _ptr(expert_offsets), E, Y.shape[0], X.shape[0], _ptr(W),
+            W.stride(0), W.stride(1), K, Y.shape[1], _ptr(Y), Y.stride(0))
+
+
+def w4a8_moe_gemm_w16a16(X, gather, k: int, expert_offsets, W, Y, stream=None) -> None:
+    """Grouped unquantized GEMM: X [src_rows, K] and W [E, N, K] in bfloat16 or float16, Y [rows, N] in the same type
+    or float32; rows may be strided."""
+    args = _w16_args(X, gather, k, expert_offsets, W, Y, 1)
+    _check(lib().w4a8_moe_gemm_w16a16(*args, _dtype(Y), _stream(stream)), "w4a8_moe_gemm_w16a16")
+
+
+def w4a8_moe_gemm_silu_w16a16(X, gather, k: int, expert_offsets, W, H, stream=None) -> None:
+    """Grouped unquantized gate/up GEMM with silu(gate) * up in its epilogue: W [E, 2I, K], H [rows, I] of X's type."""
+    args = _w16_args(X, gather, k, expert_offsets, W, H, 2)
+    if H.dtype != X.dtype:
+        raise ValueError("H must have the type of X")
+    _check(lib().w4a8_moe_gemm_silu_w16a16(*args, _stream(stream)), "w4a8_moe_gemm_silu_w16a16")
 
 
 # ------------------------------------------------------------------------------ helpers

@@ -1,0 +1,116 @@
+// Expert-grouped GEMMs on 8-bit per-channel blobs and on 16-bit row-major weights: arguments, formats and the
+// row-tile lookup shared by their kernels (gfx950).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "w4a8_device.h"
+
+namespace w4a8 {
+
+// Operand formats.  Every kernel works in bytes along K: an MFMA step takes 64 bytes of a row whatever the format
+// (64 int8 values on v_mfma_i32_16x16x64_i8, 32 values of 16 bits on v_mfma_f32_16x16x32_{bf16,f16}), 16 bytes a lane, so
+// the tile shapes, the staging and the waits are the same and only the instruction and the epilogue differ.
+enum GroupedFormat { GF_I8 = 0, GF_BF16 = 1, GF_F16 = 2 };
+
+struct GroupedArgs {
+    const uint8_t* X;         // activation rows
+    long long ldx;            // bytes between them
+    const float* sx;          // GF_I8: scale of each activation row
+    const int32_t* gather;    // source row of routed row r: gather[r] / topk (NULL: r)
+    int topk;
+    int src_rows;
+    const int32_t* offsets;   // [E + 1]
+    int E;
+    int rows;
+    const uint8_t* W;         // expert 0: blob (GF_I8) or rows [N, K] (16 bit)
+    size_t expert_stride;     // bytes between experts
+    unsigned ldw;             // 16 bit: bytes between rows of W
+    size_t codes_off, scales_off;   // GF_I8: blob sections
+    int kb;                   // bytes of K in a row
+    int N;                    // columns of Y (paired form: of h; W then holds 2 N rows, gate rows first)
+    void* Y;
+    size_t ldy;               // elements
+    int out;                  // w4a8_dtype of Y
+    int lo, hi;               // this launch serves the experts with lo <= rows < hi
+};
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+template <int FMT>
+struct GroupedAcc {
+    using type = v4f;
+};
+template <>
+struct GroupedAcc<GF_I8> {
+    using type = v4i;
+};
+
+// One 64-byte MFMA step of a 16 x 16 tile.  w holds 16 bytes of weight column lane % 16, x 16 bytes of token row
+// lane % 16; lane / 16 selects which 16 of the step's 64 bytes, the same ones in both.  The weights are the first
+// operand, so a lane's four sums are the columns 4 (lane / 16) .. + 3 of token row lane % 16: neighbours in Y.
+template <int FMT>
+__device__ __forceinline__ typename GroupedAcc<FMT>::type grouped_mfma(const v4i w, const v4i x,
+                                                                      const typename GroupedAcc<FMT>::type c) {
+    if constexpr (FMT == GF_I8) return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0);
+    else if constexpr (FMT == GF_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
+}
+
+// Round to nearest even; float16 results past 65504 become infinities, as the conversion does.
+__device__ __forceinline__ uint32_t f32_to_f16_rne(float f) {
+    return uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(f)));
+}
+
+// Four neighbouring outputs of one row.  `n` (1..4) of them exist; whole quads go out in one store where the row
+// pitch keeps them aligned (`wide`, uniform over the launch).
+__device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t at, const int n, const bool wide,
+                                              const float y0, const float y1, const float y2, const float y3) {
+    const float y[4] = {y0, y1, y2, y3};
+    if (a.out == W4A8_F32) {
+        float* p = static_cast<float*>(a.Y) + at;
+        if (n == 4 && wide) {
+            *reinterpret_cast<float4*>(p) = make_float4(y0, y1, y2, y3);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) p[i] = y[i];
+        }
+        return;
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = a.out == W4A8_F16 ? f32_to_f16_rne(y[i]) : f32_to_bf16_rne(y[i]);
+    uint16_t* p = static_cast<uint16_t*>(a.Y) + at;
+    if (n == 4 && wide) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = uint16_t(h[i]);
+    }
+}
+
+// Whether every quad of a row starts on a multiple of its size: 4 columns of 2 or 4 bytes.
+__device__ __forceinline__ bool grouped_wide(const GroupedArgs& a) {
+    const uintptr_t mask = a.out == W4A8_F32 ? 15u : 7u;
+    return a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.Y) & mask) == 0;
+}
+
+// Source row of routed row r, or -1 (a gather entry that names no row of X: its output is zero).
+__device__ __forceinline__ int grouped_src(const GroupedArgs& a, int r) {
+    if (!a.gather) return r;
+    const int g = a.gather[r];
+    if (g < 0) return -1;
+    const int t = g / a.topk;
+    return t < a.src_rows ? t : -1;
+}
+
+}  // namespace w4a8
