@@ -113,4 +113,7 @@ __device__ __forceinline__ int grouped_src(const GroupedArgs& a, int r) {
     return t < a.src_rows ? t : -1;
 }
 
+// 256 x 256 MFMA tiles (w4a8_moe_grouped_tile_kernels.hip) over the experts with a.lo <= rows < a.hi.
+void launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s);
+
 }  // namespace w4a8

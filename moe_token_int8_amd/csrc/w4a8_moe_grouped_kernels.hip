@@ -219,9 +219,15 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
         a.lo = 17, a.hi = 33;
         launch_stream_t<FMT, PAIR, 2, 2>(a, std::min(E, rows / 17), s);
     }
+    // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
+    const bool near = a.ldx <= (1 << 24) && (!a.gather || (long long)a.src_rows * a.ldx < (1ll << 32));
     if (rows > 32) {
-        a.lo = 33, a.hi = 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 2>(a, rows / 64 + std::min(E, rows / 33), s);
+        a.lo = 33, a.hi = near ? 65 : 0x7fffffff;
+        launch_stream_t<FMT, PAIR, 4, 2>(a, near ? std::min(E, rows / 33) : rows / 64 + std::min(E, rows / 33), s);
+    }
+    if (rows > 64 && near) {
+        a.lo = 65, a.hi = 0x7fffffff;
+        launch_grouped_tile(a, FMT, PAIR, s);
     }
 }
 
@@ -250,7 +256,7 @@ static int check_w8_call(const int8_t* Xq, const float* sx, const int32_t* gathe
                          int out_dtype) {
     const int st = check_w8(d);
     if (st) return st;
-    if (rows < 0 || src_rows < 0 || E <= 0 || (out_dtype != W4A8_BF16 && out_dtype != W4A8_F32)) return W4A8_EINVAL;
+    if (rows < 0 || src_rows < 0 || E <= 0 || E > 1024 || (out_dtype != W4A8_BF16 && out_dtype != W4A8_F32)) return W4A8_EINVAL;
     if (rows == 0) return W4A8_OK;
     if (rows > GROUPED_MAX_ROWS) return W4A8_EUNSUPPORTED;
     if (!Xq || !sx || !offsets || !blobs || !Y) return W4A8_EINVAL;
@@ -266,7 +272,7 @@ static int check_w16_call(const void* X, int dtype, int ldx, const int32_t* gath
                           const void* Y, int ldy, int out_dtype) {
     if (dtype != W4A8_BF16 && dtype != W4A8_F16) return W4A8_EINVAL;
     if (out_dtype != dtype && (pair || out_dtype != W4A8_F32)) return W4A8_EINVAL;
-    if (rows < 0 || src_rows < 0 || E <= 0 || K <= 0 || N <= 0) return W4A8_EINVAL;
+    if (rows < 0 || src_rows < 0 || E <= 0 || E > 1024 || K <= 0 || N <= 0) return W4A8_EINVAL;
     if (K % 8 || ldx % 8 || ldw % 8 || stride % 8 || ldx < K || ldw < K || ldy < N) return W4A8_EINVAL;
     if (E > 1 && stride < (size_t(N) * (pair ? 2 : 1) - 1) * size_t(ldw) + size_t(K)) return W4A8_EINVAL;
     if (N > GROUPED_MAX_N || ldw > (1 << 23) || rows > GROUPED_MAX_ROWS) return W4A8_EUNSUPPORTED;
