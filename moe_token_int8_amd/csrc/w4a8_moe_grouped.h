@@ -69,6 +69,16 @@ __device__ __forceinline__ uint32_t f32_to_f16_rne(float f) {
     return uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(f)));
 }
 
+// Two values rounded to nearest even and packed (v_cvt_pk_bf16_f32; NaN stays NaN).
+__device__ __forceinline__ uint32_t f32_to_bf16_pair(float lo, float hi) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{lo, hi}, v2bf));
+}
+__device__ __forceinline__ uint32_t f32_to_f16_pair(float lo, float hi) {
+    return f32_to_f16_rne(lo) | (f32_to_f16_rne(hi) << 16);
+}
+
 // Four neighbouring outputs of one row.  `n` (1..4) of them exist; whole quads go out in one store where the row
 // pitch keeps them aligned (`wide`, uniform over the launch).
 __device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t at, const int n, const bool wide,
@@ -85,16 +95,17 @@ __device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t
         }
         return;
     }
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = a.out == W4A8_F16 ? f32_to_f16_rne(y[i]) : f32_to_bf16_rne(y[i]);
+    const bool f16 = a.out == W4A8_F16;
+    const uint32_t lo = f16 ? f32_to_f16_pair(y0, y1) : f32_to_bf16_pair(y0, y1);
+    const uint32_t hi = f16 ? f32_to_f16_pair(y2, y3) : f32_to_bf16_pair(y2, y3);
     uint16_t* p = static_cast<uint16_t*>(a.Y) + at;
     if (n == 4 && wide) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) p[i] = uint16_t(h[i]);
+        p[0] = uint16_t(lo);
+        if (n > 1) p[1] = uint16_t(lo >> 16);
+        if (n > 2) p[2] = uint16_t(hi);
+        if (n > 3) p[3] = uint16_t(hi >> 16);
     }
 }
 
