@@ -191,7 +191,7 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
         } else if constexpr (PAIR) {
             const acc_t up = total(item + ITEMS / 2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = src < 0 ? 0.0f : silu_mul(s[i], up[i]);
+            for (int i = 0; i < 4; ++i) y[i] = src < 0 ? 0.0f : silu_gate(s[i]) * up[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = src < 0 ? 0.0f : s[i];
@@ -220,7 +220,7 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
         launch_stream_t<FMT, PAIR, 2, 2>(a, std::min(E, rows / 17), s);
     }
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
-    const bool near = a.ldx <= (1 << 24) && (!a.gather || (long long)a.src_rows * a.ldx < (1ll << 32));
+    const bool near = a.ldx <= (1 << 24) && (!a.gather || (long long)a.src_rows * a.ldx < (1ll << 32) - 256);
     if (rows > 32) {
         a.lo = 33, a.hi = near ? 65 : 0x7fffffff;
         launch_stream_t<FMT, PAIR, 4, 2>(a, near ? std::min(E, rows / 33) : rows / 64 + std::min(E, rows / 33), s);

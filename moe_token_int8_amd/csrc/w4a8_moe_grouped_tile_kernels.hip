@@ -12,32 +12,32 @@
 namespace w4a8 {
 
 // A persistent workgroup of 8 waves per compute unit walks over 256-row x 256-column tiles (paired form: 128 gate and the
-// matching 128 up columns).  Per step of 128 bytes of K the 256 activation rows and the 256 weight rows are copied
-// straight from memory to LDS (global_load_lds, 16 bytes a lane, no registers in between), one step ahead of the MFMAs:
-// two 64 KiB stages.  Wave (wm, wn) owns rows 128 wm .. + 127 and 64 columns: 8 x 4 MFMA tiles, 128 accumulators a lane.
+// matching 128 up columns).  A step is 64 bytes of K: the 256 activation rows and 256 weight rows are copied straight
+// from memory to LDS (16 bytes a lane, no registers in between) into a ring of four 32 KiB stages, three steps ahead of
+// the MFMAs.  Wave (wm, wn) owns rows 128 wm .. + 127 and 64 columns: 8 x 4 MFMA tiles, 128 accumulators a lane.
 constexpr int GT_M = 256, GT_N = 256;
-constexpr int GT_STAGE = (GT_M + GT_N) * 128;
+constexpr int GT_STEP = 64;                                     // bytes of K in a step
+constexpr int GT_STAGE = (GT_M + GT_N) * GT_STEP;
+constexpr int GT_WOFF = GT_M * GT_STEP;                         // weights within a stage
 constexpr int GT_PANEL = 4;                                     // row tiles of a panel of consecutive tiles
 constexpr int GT_MAX_E = 1024;
+constexpr int GT_LIST = 512;                                    // tiles looked up at a time, one a thread
 
-// LDS image of a stage: the activation rows, then the weight rows, 128 bytes each, in 16-byte chunks.  Chunk c of row r
-// sits at position c ^ ((r >> 1) & 7): the 16 rows that an operand read takes at one chunk then lie in distinct banks.  A
-// copy of 64 lanes fills 8 rows in order, so lane l supplies row l / 8, position l % 8.  Packed codes keep their
-// superblocks of 2 KiB (16 columns) with neighbouring chunks swapped in the upper 8 columns, for the same reason.
-__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
-
-// Chunk that lane group q takes of half h: the packed layout's order, for the 16-bit rows too.  (With the streaming
-// kernel's order 2 q + h two lane groups that are served together meet in the same banks.)
-__device__ __forceinline__ int operand_chunk(int q, int h) { return 4 * h + q; }
+// LDS image of a stage: rows of 64 bytes in four 16-byte chunks, the activations' 256, then the weights'.  Chunk c of row
+// r sits at position c ^ row_swizzle(r): 16 rows read at one chunk, and the halves of two neighbouring chunks that the
+// LDS serves together, then lie in distinct banks.  (Weights in 8-bit codes keep the MFMA operand's own order, 1 KiB a
+// 16-column tile, which is read in a row.)
+__device__ __forceinline__ int row_swizzle(int r) { return -(r >> 2) & 3; }
 
 // Stages are addressed as LDS objects, not through generic pointers, and copied into through buffer descriptors: the
-// compiler then sees that a read of one stage does not touch the other, and waits neither for the copies in flight into
-// it nor (as it does after a global_load_lds) for every LDS read before an MFMA.
+// compiler then sees that a read of one stage does not touch the others, and waits neither for the copies in flight into
+// them nor (as it does after a global_load_lds) for every LDS read before an MFMA.
 #define LDS __attribute__((address_space(3)))
 using lds_ptr = LDS uint8_t*;
 
-__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t src, unsigned off, unsigned step, lds_ptr dst) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LDS void*)dst, 16, off, step, 0, 0);
+// (The whole offset is in the register operand: a scalar offset is not part of the descriptor's range check.)
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t src, unsigned off, lds_ptr dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LDS void*)dst, 16, off, 0, 0, 0);
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, size_t bytes) {
@@ -45,11 +45,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base,
                                              0x00020000);
 }
 
-// Every copy of this wave has landed and every wave is here: the stage that was being filled is whole and the one that
-// was being read is free.
+// Waits until at most NEWER memory operations of this wave are in flight (the counter goes down in the order of issue)
+// and its LDS reads are done, then for every wave.
+template <int NEWER>
 __device__ __forceinline__ void stage_barrier() {
+    static_assert(NEWER < 64, "the counter has 6 bits");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((7 << 4) | (0 << 8));           // vmcnt 0, lgkmcnt 0, expcnt not waited for
+    __builtin_amdgcn_s_waitcnt((NEWER & 15) | ((NEWER >> 4) << 14) | (7 << 4) | (0 << 8));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -61,10 +63,13 @@ __device__ __forceinline__ int opaque(int v) {
     return v;
 }
 
-// A tile: rows rbeg .. rbeg + nrows of expert e, column block cb.  Uniform over the workgroup.
-struct GroupedTile {
-    int e, rbeg, nrows, cb;
-};
+// Weight column, within a wave's block of 64 (paired form: 32), that MFMA tile n has in its row c.  A lane's sums are the
+// rows 4 (lane / 16) .. + 3 of its tiles: with 16-bit outputs the columns are dealt out so that two tiles together give
+// it 8 neighbouring ones, a 16-byte store and 64 contiguous bytes a row (8-byte stores in 32-byte pieces cost the
+// 8192-token down product 0.04 of 0.68 ms); with float32 a tile's 16 columns are 64 bytes as they stand.
+__device__ __forceinline__ int tile_column(bool f32, int n, int c) {
+    return f32 ? n * 16 + c : (n >> 1) * 32 + (c >> 2) * 8 + (n & 1) * 4 + (c & 3);
+}
 
 template <int FMT, bool PAIR>
 __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a) {
@@ -72,15 +77,23 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     constexpr int COLS = PAIR ? GT_N / 2 : GT_N;                // columns of Y
     __shared__ __align__(1024) uint8_t stage0[GT_STAGE];
     __shared__ __align__(1024) uint8_t stage1[GT_STAGE];
+    __shared__ __align__(1024) uint8_t stage2[GT_STAGE];
+    __shared__ __align__(1024) uint8_t stage3[GT_STAGE];
+    __shared__ int4 list[GT_LIST];                              // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[GT_MAX_E + 1];                         // row tiles before expert e
     __shared__ float rowscale[2][GT_M];                         // of this tile's rows and the next one's
     __shared__ int wsum[8];
-    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1, st2 = (lds_ptr)stage2, st3 = (lds_ptr)stage3;
+    const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int q = lane >> 4, c16 = lane & 15;
+    const int ncb = (a.N + COLS - 1) / COLS;
+    const int steps = (a.kb + GT_STEP - 1) / GT_STEP;
+    const bool wide = grouped_wide(a);
+    const bool f32 = !PAIR && a.out == W4A8_F32;
 
     // row tiles of every expert of this launch, as a prefix sum (two experts a thread)
     {
+        const int tid = threadIdx.x;
         int t[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -103,254 +116,311 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         if (a.E == GT_MAX_E && tid == 511) first[GT_MAX_E] = incl;
         __syncthreads();
     }
-    const int ncb = (a.N + COLS - 1) / COLS;
     const long long total = (long long)first[a.E] * ncb;
-    const int steps = (a.kb + 127) / 128;
-    // Where K ends inside the last step the chunks behind it receive other bytes of the tile's rows, or what a read past
-    // the end of a descriptor gives: they are set to zero in LDS once that step's copies have landed, in both operands,
-    // so that an infinity or a NaN there meets nothing.
-    const bool ragged = FMT != GF_I8 && (a.kb & 127) != 0;
-    auto clear_tail = [&](lds_ptr st) __attribute__((always_inline)) {
-        const int row = opaque(int(threadIdx.x));
-#pragma unroll 1
-        for (int c = (a.kb & 127) >> 4; c < 8; ++c) *(LDS v4i*)(st + row * 128 + (c ^ row_swizzle(row)) * 16) = v4i{0, 0, 0, 0};
-        lds_barrier();
-    };
-    const bool wide = grouped_wide(a);
     // blocks go to the 8 XCDs in turn: the blocks of one XCD take neighbouring tiles, which share rows or columns in its L2
     const int nblk = int(gridDim.x), per = nblk / 8;
     const int rank = nblk % 8 ? int(blockIdx.x) : (int(blockIdx.x) % 8) * per + int(blockIdx.x) / 8;
+    const int mine = rank < total ? int((total - rank + nblk - 1) / nblk) : 0;      // tiles of this workgroup
+    if (mine == 0) return;
 
-    auto find = [&](const long long t) __attribute__((always_inline)) {
-        const int trow = int(t / ncb);
-        int e = 0;                                              // experts that end at or before row tile trow
-        for (int c = 0; c < a.E; c += 64)
-            e += __popcll(__ballot(c + lane < a.E && first[min(c + lane, a.E - 1) + 1] <= trow));
-        e = __builtin_amdgcn_readfirstlane(e);
-        const int f0 = __builtin_amdgcn_readfirstlane(first[e]), rt = __builtin_amdgcn_readfirstlane(first[e + 1]) - f0;
-        const int in_e = int(t - (long long)f0 * ncb);
-        const int panel = in_e / (GT_PANEL * ncb), j = in_e - panel * GT_PANEL * ncb;
-        const int rp = min(GT_PANEL, rt - panel * GT_PANEL);
-        const int cb = j / rp, rtile = panel * GT_PANEL + j - cb * rp;
-        const int r0 = min(max(a.offsets[e], 0), a.rows) + rtile * GT_M;
-        return GroupedTile{e, r0, min(GT_M, min(a.offsets[e + 1], a.rows) - r0), cb};
+    // tiles k0 .. k0 + 511 of this workgroup; all threads, between barriers
+    auto look_up = [&](const int k0) __attribute__((always_inline)) {
+        const int tid = opaque(int(threadIdx.x));
+        if (k0 + tid < mine) {
+            const long long t = rank + (long long)(k0 + tid) * nblk;
+            const int trow = int(t / ncb);
+            int lo = 0, hi = a.E;                               // expert: the last one whose first tile is not after trow
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= trow) lo = mid;
+                else hi = mid;
+            }
+            const int f0 = first[lo], rt = first[lo + 1] - f0, in_e = int(t - (long long)f0 * ncb);
+            const int panel = in_e / (GT_PANEL * ncb), j = in_e - panel * GT_PANEL * ncb;
+            const int rp = min(GT_PANEL, rt - panel * GT_PANEL);
+            const int cb = j / rp, r0 = min(max(a.offsets[lo], 0), a.rows) + (panel * GT_PANEL + j - cb * rp) * GT_M;
+            list[tid] = make_int4(lo, r0, min(GT_M, min(a.offsets[lo + 1], a.rows) - r0), cb);
+        }
+        __syncthreads();
     };
 
-    // Sources of this thread's copies: 4 of the 32 groups of 8 activation rows and 4 of the weights' 32 KiB, as byte
-    // offsets from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.
-    unsigned xoff[4], woff[4];
-    constexpr unsigned WSTEP = FMT == GF_I8 ? 2048 : 128;       // bytes from one step to the next
+    // Where K ends inside the last step the chunks behind it receive other bytes of the tile's rows, or what a read past
+    // the end of a descriptor gives: they are set to zero in LDS once that step's copies have landed, in both operands,
+    // so that an infinity or a NaN there meets nothing.
+    const bool ragged = FMT != GF_I8 && a.kb % GT_STEP != 0;
+    auto clear_tail = [&](lds_ptr st) __attribute__((always_inline)) {
+        const int row = opaque(int(threadIdx.x));
+#pragma unroll 1
+        for (int c = (a.kb % GT_STEP) >> 4; c < 4; ++c)
+            *(LDS v4i*)(st + row * GT_STEP + (c ^ row_swizzle(row)) * 16) = v4i{0, 0, 0, 0};
+        lds_barrier();
+    };
+
+    // Sources of this thread's copies, 2 of the 16 groups of 16 activation rows and 2 of the weights' 16 KiB, as byte
+    // offsets from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.  Weight
+    // rows past the last column and bytes past the last row's K lie outside it and load nothing.
+    unsigned xoff[2], woff;
     __amdgpu_buffer_rsrc_t xr, wr[PAIR ? 2 : 1];                // paired form: gate rows, up rows
+    const unsigned tile_bytes = unsigned(steps / 2) * 2048u;    // GF_I8: 16 columns of codes
+    const unsigned wgroup = FMT == GF_I8 ? 8u * tile_bytes : PAIR ? 0u : 128u * a.ldw;     // between the two copies
     auto fill = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
+        const unsigned wstep = FMT == GF_I8 ? unsigned(s >> 1) * 2048u + unsigned(s & 1) * 16u : unsigned(s) * GT_STEP;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            copy_to_lds(xr, xoff[i], unsigned(s) * 128u, st + (i * 8 + wave) * 1024);
-            copy_to_lds(wr[PAIR ? i >> 1 : 0], woff[i], unsigned(s) * WSTEP, st + GT_M * 128 + (i * 8 + wave) * 1024);
+        for (int i = 0; i < 2; ++i) {
+            copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * 8 + wave) * 1024);
+            copy_to_lds(wr[PAIR ? i : 0], woff + (wstep + i * wgroup), st + GT_WOFF + (i * 8 + wave) * 1024);
         }
     };
-    // descriptors, offsets and row scales of a tile, and the copies of its first two steps
-    auto begin = [&](const GroupedTile& g, const int buf) __attribute__((always_inline)) {
-        const int tid = opaque(int(threadIdx.x)), lane = tid & 63;
-        const uint8_t* wexp = a.W + size_t(g.e) * a.expert_stride;
-        const int last_col = min(COLS, a.N - g.cb * COLS) - 1;
+    constexpr int FILL = 4;                                     // copies of a wave in one fill
+
+    // The MFMA loop is four steps long and has no other exit, so that the accumulators stay where they are: K is rounded up
+    // to whole turns of the ring with steps of zeros (none where a row is a multiple of 256 bytes).
+    const int turns = (steps + 3) / 4;
+    auto supply = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
+        if (s < steps) {
+            fill(st, s);
+        } else if (s < 4 * turns) {
+            const int tid = opaque(int(threadIdx.x));
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) *(LDS v4i*)(st + (c * 512 + tid) * 16) = v4i{0, 0, 0, 0};
+        }
+    };
+
+    // Gather entries of a tile's rows: those of this thread's copies, and row threadIdx.x for its scale.
+    struct Rows {
+        int copy[2], own;
+    };
+    auto fetch_rows = [&](const int rbeg, const int nrows) __attribute__((always_inline)) {
+        const int tid = opaque(int(threadIdx.x));
+        Rows r;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = (i * 8 + (tid >> 6)) * 16 + ((tid & 63) >> 2);
+            r.copy[i] = row < nrows ? row : 0;                  // rows past the tile repeat its first row
+            if (a.gather) r.copy[i] = a.gather[rbeg + r.copy[i]];
+        }
+        r.own = tid < nrows ? rbeg + tid : -1;
+        if (a.gather && tid < nrows) r.own = a.gather[r.own];
+        return r;
+    };
+    auto source = [&](const int g) __attribute__((always_inline)) {    // row of X, or -1
+        if (!a.gather) return g;
+        const int t = g < 0 ? -1 : int(unsigned(g) / unsigned(a.topk));
+        return t < a.src_rows ? t : -1;
+    };
+    // scale of row threadIdx.x; 16 bit: 0 marks a gather entry that names no row
+    float own_scale = 0.0f;
+    // descriptors, offsets and row scales of a tile, and the copies of its first steps
+    auto begin = [&](const int4 g, const Rows r) __attribute__((always_inline)) {
+        const int tid = opaque(int(threadIdx.x)), lane = tid & 63, wave = tid >> 6;
+        const uint8_t* wexp = a.W + size_t(g.x) * a.expert_stride;
+        const int last_col = min(COLS, a.N - g.w * COLS) - 1;
         xr = a.gather ? buffer_of(a.X, size_t(a.src_rows - 1) * size_t(a.ldx) + size_t(a.kb))
-                      : buffer_of(a.X + size_t(g.rbeg) * size_t(a.ldx), size_t(g.nrows - 1) * size_t(a.ldx) + size_t(a.kb));
+                      : buffer_of(a.X + size_t(g.y) * size_t(a.ldx), size_t(g.z - 1) * size_t(a.ldx) + size_t(a.kb));
         if constexpr (FMT == GF_I8) {
-            wr[0] = buffer_of(wexp + a.codes_off + size_t(g.cb) * 16 * size_t(steps) * 2048,
-                              size_t(last_col / 16 + 1) * size_t(steps) * 2048);
+            wr[0] = buffer_of(wexp + a.codes_off + size_t(g.w) * 16 * tile_bytes, size_t(last_col / 16 + 1) * tile_bytes);
         } else {
 #pragma unroll
             for (int p = 0; p < (PAIR ? 2 : 1); ++p)
-                wr[p] = buffer_of(wexp + (size_t(g.cb) * COLS + size_t(p) * size_t(a.N)) * a.ldw,
+                wr[p] = buffer_of(wexp + (size_t(g.w) * COLS + size_t(p) * size_t(a.N)) * a.ldw,
                                   size_t(last_col) * a.ldw + size_t(a.kb));
         }
-        int src[4];
+        const int own = source(r.own);
+        own_scale = own < 0 ? 0.0f : 1.0f;
+        if (FMT == GF_I8 && own >= 0) own_scale = a.sx[own];
+        const int chunk = (lane & 3) ^ row_swizzle(lane >> 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = (i * 8 + wave) * 8 + (lane >> 3);
-            const int local = row < g.nrows ? row : 0;
-            src[i] = a.gather ? max(grouped_src(a, g.rbeg + local), 0) : local;
+        for (int i = 0; i < 2; ++i)                             // (opaque: a fused multiply-add would leave 64-bit results)
+            xoff[i] = unsigned(opaque(int(unsigned(max(source(r.copy[i]), 0)) * unsigned(a.ldx)))) + unsigned(chunk) * 16u;
+        if constexpr (FMT == GF_I8) {
+            const int col = (wave >> 2) * 64 + tile_column(f32, wave & 3, lane & 15);
+            woff = unsigned(opaque(int(unsigned(col >> 4) * tile_bytes))) + unsigned((lane >> 4) * 16 + (col & 15)) * 32u;
+        } else {
+            const int col = PAIR ? (wave >> 1) * 32 + tile_column(false, wave & 1, lane >> 2)
+                                 : (wave >> 2) * 64 + tile_column(f32, wave & 3, lane >> 2);
+            woff = unsigned(opaque(int(unsigned(col) * a.ldw))) + unsigned(chunk) * 16u;
         }
-        // scale of the tile's row tid; 16 bit: 0 marks a gather entry that names no row
-        float rs = 1.0f;
-        if (tid < g.nrows && (FMT == GF_I8 || a.gather)) {
-            const int r = grouped_src(a, g.rbeg + tid);
-            rs = r < 0 ? 0.0f : FMT == GF_I8 ? a.sx[r] : 1.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = (i * 8 + wave) * 8 + (lane >> 3);
-            const int chunk = (lane & 7) ^ row_swizzle(row);
-            // (opaque products: a fused multiply-add would leave a 64-bit result, two registers for each offset)
-            xoff[i] = unsigned(opaque(int(unsigned(src[i]) * unsigned(a.ldx)))) + unsigned(chunk) * 16u;
-            if constexpr (FMT == GF_I8) {                       // half a superblock
-                const int unit = ((i * 8 + wave) & 1) * 64 + (lane ^ ((lane >> 4) & 1));
-                woff[i] = unsigned(min((i * 8 + wave) >> 1, last_col / 16)) * unsigned(steps) * 2048u + unsigned(unit) * 16u;
-            } else {
-                woff[i] = unsigned(opaque(int(unsigned(min(PAIR ? row & 127 : row, last_col)) * a.ldw))) + unsigned(chunk) * 16u;
-            }
-        }
-        fill(st0, 0);
-        if (steps > 1) fill(st1, 1);
-        if (tid < GT_M) rowscale[buf][tid] = rs;
+        supply(st0, 0);
+        supply(st1, 1);
+        supply(st2, 2);
+        supply(st3, 3);
     };
 
-    // Operands of half h (64 bytes of K) of a stage: the 4 weight tiles, and 4 of the 8 row tiles.  The compiler may not
-    // see into the byte offsets: it would rebuild each address from its terms and lose which stage it belongs to.
+    // Operands of a stage: the 4 weight tiles, and 4 of the 8 row tiles.  The compiler may not see into the byte offsets: it
+    // would rebuild each address from its terms and lose which stage it belongs to.
     const int wm = wave >> 2, wn = wave & 3;
-    int xat[2], wat[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int pos = (operand_chunk(q, h) ^ row_swizzle(c16)) * 16;
-        xat[h] = (wm * 128 + c16) * 128 + pos;
-        if constexpr (FMT == GF_I8) wat[h] = GT_M * 128 + wn * 4 * 2048 + (2 * lane + (h ^ (c16 >> 3))) * 16;
-        else wat[h] = GT_M * 128 + ((PAIR ? wn * 32 : wn * 64) + c16) * 128 + pos;
-        asm volatile("" : "+v"(xat[h]), "+v"(wat[h]));
-    }
-    auto read_w = [&](const lds_ptr st, const int h, v4i (&w)[4]) __attribute__((always_inline)) {
+    const int pos = (q ^ row_swizzle(c16)) * 16;
+    const int xat = opaque((wm * 128 + c16) * GT_STEP + pos);
+    const int wat = opaque(GT_WOFF + (FMT == GF_I8 ? wn * 4096 + lane * 16 : ((PAIR ? wn * 32 : wn * 64) + c16) * GT_STEP + pos));
+    auto read_w = [&](const lds_ptr st, v4i (&w)[4]) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-            w[n] = *(const LDS v4i*)(st + wat[h] + (PAIR ? (n >> 1) * 128 * 128 + (n & 1) * 2048 : n * 2048));
+            w[n] = *(const LDS v4i*)(st + wat + (PAIR ? (n >> 1) * 128 * GT_STEP + (n & 1) * 1024 : n * 1024));
     };
-    auto read_x = [&](const lds_ptr st, const int h, const int mh, v4i (&x)[4]) __attribute__((always_inline)) {
+    auto read_x = [&](const lds_ptr st, const int mh, v4i (&x)[4]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = *(const LDS v4i*)(st + xat[h] + (mh * 4 + m) * 2048);
+        for (int m = 0; m < 4; ++m) x[m] = *(const LDS v4i*)(st + xat + (mh * 4 + m) * 1024);
     };
 
-    if (rank >= total) return;
-    GroupedTile g = find(rank);
-    begin(g, 0);
-    int buf = 0;
-    for (long long t = rank;; buf ^= 1) {
-        acc_t acc[4][8];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int m = 0; m < 8; ++m) acc[n][m] = acc_t{};
-        auto mfma = [&](const v4i (&w)[4], const v4i (&x)[4], const int mh) __attribute__((always_inline)) {
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) acc[n][mh * 4 + m] = grouped_mfma<FMT>(w[n], x[m], acc[n][mh * 4 + m]);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        const bool busy = wm * 128 < g.nrows;
-        stage_barrier();
+    // With whole aligned 16-byte stores and row offsets that fit 32 bits, every wave that computed ends a tile with at least
+    // STORES of them, which the next tile's first barriers leave in flight.
+    constexpr int STORES = PAIR ? 8 : 16;
+    const int quantum = f32 ? 3 : 7;
+    const bool regular = (a.N & quantum) == 0 && (a.ldy & quantum) == 0 && a.ldy < (size_t(1) << 21) &&
+                         (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0;
+    const bool behind_stores = regular && steps >= 8;
+
+    look_up(0);
+    int4 g = list[0];
+    auto uniform = [&](int4 v) __attribute__((always_inline)) {
+        return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                         __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+    };
+    g = uniform(g);
+    begin(g, fetch_rows(g.y, g.z));
+    __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);               // vmcnt 0: no stores stand behind the first copies
+    for (int k = 0;;) {
+        const int4 cur = g;
+        const int buf = k & 1;
+        if (behind_stores) stage_barrier<3 * FILL + STORES>();
+        else stage_barrier<0>();
+        if (threadIdx.x < GT_M) rowscale[buf][threadIdx.x] = own_scale;
         if (ragged && steps == 1) clear_tail(st0);
-        if (busy) {
-            v4i w0[4], w1[4], xa[4], xb[4];
-            // One step: four groups of 16 MFMAs, the operands of each read from LDS during the group before it.  The
-            // barrier stands before the last group, when this step's last operands are in registers: behind it the next
-            // stage is whole and this one is free for the copies of the step after.
-            auto step = [&](const lds_ptr cur, const lds_ptr next, const int s) __attribute__((always_inline)) {
-                read_x(cur, 0, 1, xb);
-                mfma(w0, xa, 0);
-                read_w(cur, 1, w1);
-                read_x(cur, 1, 0, xa);
-                mfma(w0, xb, 1);
-                read_x(cur, 1, 1, xb);
-                mfma(w1, xa, 0);
-                stage_barrier();
-                if (ragged && s + 2 == steps) clear_tail(next);
-                read_w(next, 0, w0);
-                read_x(next, 0, 0, xa);
-                if (s + 2 < steps) fill(cur, s + 2);
-                mfma(w1, xb, 1);
+        // the next tile, and its gather entries: requested here, first needed at the end of this tile
+        Rows rows;
+        if (++k < mine) {
+            if (k % GT_LIST == 0) look_up(k);
+            g = uniform(list[k % GT_LIST]);
+            rows = fetch_rows(g.y, g.z);
+        }
+        if (wm * 128 < cur.z) {
+            acc_t acc[4][8];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int m = 0; m < 8; ++m) acc[n][m] = acc_t{};
+            auto mfma = [&](const v4i (&w)[4], const v4i (&x)[4], const int mh) __attribute__((always_inline)) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) acc[n][mh * 4 + m] = grouped_mfma<FMT>(w[n], x[m], acc[n][mh * 4 + m]);
+                __builtin_amdgcn_sched_barrier(0);
             };
-            read_w(st0, 0, w0);
-            read_x(st0, 0, 0, xa);
-            int s = 0;
-            for (; s + 2 < steps; s += 2) {
-                step(st0, st1, s);
-                step(st1, st0, s + 1);
+            v4i wa[4], wb[4], xa[4], xb[4];
+            // One step: two groups of 16 MFMAs, the operands of each read from LDS during the group before it.  The barrier
+            // stands before the second group, when this stage's last operands are in registers: behind it the next stage
+            // is whole, with the copies of the two after it in flight, and this one is free for the fourth.
+            auto step = [&](const lds_ptr st, const lds_ptr next, v4i (&w)[4], v4i (&wnext)[4], const int s,
+                            const bool early) __attribute__((always_inline)) {
+                read_x(st, 1, xb);
+                mfma(w, xa, 0);
+                if (early) stage_barrier<2 * FILL + STORES>();
+                else if (s + 3 < steps) stage_barrier<2 * FILL>();
+                else if (s + 2 < steps) stage_barrier<FILL>();
+                else stage_barrier<0>();
+                if (ragged && s + 2 == steps) clear_tail(next);
+                read_w(next, wnext);
+                read_x(next, 0, xa);
+                supply(st, s + 4);
+                mfma(w, xb, 1);
+            };
+            read_w(st0, wa);
+            read_x(st0, 0, xa);
+            for (int s = 0; s < steps; s += 4) {
+                const bool early = behind_stores && s == 0;
+                step(st0, st1, wa, wb, s, early);
+                step(st1, st2, wb, wa, s + 1, early);
+                step(st2, st3, wa, wb, s + 2, early);
+                step(st3, st0, wb, wa, s + 3, false);
             }
-            if (s + 1 < steps) step(st0, st1, s++);
-            // last step
-            const lds_ptr last = s & 1 ? st1 : st0;
-            read_x(last, 0, 1, xb);
-            mfma(w0, xa, 0);
-            read_w(last, 1, w1);
-            read_x(last, 1, 0, xa);
-            mfma(w0, xb, 1);
-            read_x(last, 1, 1, xb);
-            mfma(w1, xa, 0);
-            mfma(w1, xb, 1);
-        } else {                                                // a wave below the last row only copies
-            for (int s = 0; s + 1 < steps; ++s) {
-                stage_barrier();
-                if (ragged && s + 2 == steps) clear_tail(s & 1 ? st0 : st1);
-                if (s + 2 < steps) {
-                    if (s & 1) fill(st1, s + 2);
-                    else fill(st0, s + 2);
-                }
-            }
-        }
-        stage_barrier();
 
-        // the next tile's copies start before this one's outputs are stored
-        const GroupedTile cur = g;
-        t += nblk;
-        const bool more = t < total;
-        if (more) {
-            g = find(t);
-            begin(g, buf ^ 1);
-        }
-        if (busy) {
-            const uint8_t* wexp = a.W + size_t(cur.e) * a.expert_stride;
             const int l = opaque(lane), c16 = l & 15;
-            const int col0 = cur.cb * COLS + (PAIR ? wn * 32 : wn * 64) + 4 * (l >> 4);   // this lane in tile n: + 16 n
             constexpr int NT = PAIR ? 2 : 4;
+            int col[NT];                                        // of this lane's four sums in tile n
+#pragma unroll
+            for (int n = 0; n < NT; ++n) col[n] = cur.w * COLS + (PAIR ? wn * 32 : wn * 64) + tile_column(f32, n, 4 * (l >> 4));
             float4 sw[NT];
             if constexpr (FMT == GF_I8) {
+                const uint8_t* scales = a.W + size_t(cur.x) * a.expert_stride + a.scales_off;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)                    // padded to whole column tiles: any col < N is inside
-                    sw[n] = *reinterpret_cast<const float4*>(wexp + a.scales_off + size_t(min(col0 + n * 16, (a.N - 1) & ~3)) * 4);
+                    sw[n] = *reinterpret_cast<const float4*>(scales + size_t(min(col[n], (a.N - 1) & ~3)) * 4);
             }
-            const bool whole = wide && (cur.cb + 1) * COLS <= a.N;      // no column checks
-            auto emit = [&](auto store) __attribute__((always_inline)) {
+            // every stage has been read: the next tile's copies start before this one's outputs are stored
+            lds_barrier();
+            if (k < mine) begin(g, rows);
+            auto value = [&](const int n, const int m, const float rs, float* y) __attribute__((always_inline)) {
+                if constexpr (FMT == GF_I8) {
+                    y[0] = (float(acc[n][m][0]) * sw[n].x) * rs;
+                    y[1] = (float(acc[n][m][1]) * sw[n].y) * rs;
+                    y[2] = (float(acc[n][m][2]) * sw[n].z) * rs;
+                    y[3] = (float(acc[n][m][3]) * sw[n].w) * rs;
+                } else {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    const int row = wm * 128 + m * 16 + c16;
-                    if (row >= cur.nrows) continue;
-                    const float rs = rowscale[buf][row];
-                    const size_t at = size_t(cur.rbeg + row) * a.ldy + col0;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float y[4];
-                        if constexpr (FMT == GF_I8) {
-                            y[0] = (float(acc[n][m][0]) * sw[n].x) * rs;
-                            y[1] = (float(acc[n][m][1]) * sw[n].y) * rs;
-                            y[2] = (float(acc[n][m][2]) * sw[n].z) * rs;
-                            y[3] = (float(acc[n][m][3]) * sw[n].w) * rs;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float v = PAIR ? silu_mul(acc[n][m][i], acc[n + (PAIR ? 2 : 0)][m][i]) : acc[n][m][i];
-                                y[i] = rs == 0.0f ? 0.0f : v;
-                            }
-                        }
-                        store(at + n * 16, col0 + n * 16, y);
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = PAIR ? silu_gate(acc[n][m][i]) * acc[n + (PAIR ? 2 : 0)][m][i] : acc[n][m][i];
+                        y[i] = rs == 0.0f ? 0.0f : v;
                     }
                 }
             };
-            if (!whole) {
-                emit([&](size_t at, int col, const float* y) __attribute__((always_inline)) {
-                    if (col < a.N) grouped_store(a, at, min(4, a.N - col), wide, y[0], y[1], y[2], y[3]);
-                });
-            } else if (!PAIR && a.out == W4A8_F32) {
-                emit([&](size_t at, int, const float* y) __attribute__((always_inline)) {
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at) = make_float4(y[0], y[1], y[2], y[3]);
-                });
-            } else {
-                emit([&](size_t at, int, const float* y) __attribute__((always_inline)) {
-                    const uint2 h = FMT == GF_F16 ? make_uint2(f32_to_f16_pair(y[0], y[1]), f32_to_f16_pair(y[2], y[3]))
-                                                  : make_uint2(f32_to_bf16_pair(y[0], y[1]), f32_to_bf16_pair(y[2], y[3]));
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.Y) + at) = h;
-                });
+            // stores of 16 bytes exist whole or not at all: one each, dropped by the descriptor where they do not
+            const unsigned es = f32 ? 4u : 2u, pitch = unsigned(a.ldy) * es;
+            const __amdgpu_buffer_rsrc_t yr = buffer_of(static_cast<const uint8_t*>(a.Y) + size_t(cur.y) * a.ldy * es,
+                                                        size_t(cur.z - 1) * pitch + size_t(a.N) * es);
+            unsigned coff[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) coff[n] = col[n] < a.N ? unsigned(col[n]) * es : 0x80000000u;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                const int row = wm * 128 + m * 16 + c16;
+                const float rs = rowscale[buf][row];
+                float y[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) value(n, m, rs, y[n]);
+                if (!regular) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (row < cur.z && col[n] < a.N)
+                            grouped_store(a, size_t(cur.y + row) * a.ldy + col[n], min(4, a.N - col[n]), wide, y[n][0], y[n][1],
+                                          y[n][2], y[n][3]);
+                } else if (f32) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v4f{y[n][0], y[n][1], y[n][2], y[n][3]}), yr,
+                                                               unsigned(row) * pitch + coff[n], 0, 0);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        v4i h;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = y[n + (i >> 1)][2 * (i & 1)], hi = y[n + (i >> 1)][2 * (i & 1) + 1];
+                            h[i] = int(FMT == GF_F16 ? f32_to_f16_pair(lo, hi) : f32_to_bf16_pair(lo, hi));
+                        }
+                        __builtin_amdgcn_raw_buffer_store_b128(h, yr, unsigned(row) * pitch + coff[n], 0, 0);
+                    }
+                }
             }
+            if (k == mine) break;
+        } else {                                                // a wave below the last row only copies
+            for (int s = 0; s < 4 * turns; ++s) {
+                if (s < 3 && behind_stores) stage_barrier<2 * FILL + STORES>();
+                else if (s + 3 < steps) stage_barrier<2 * FILL>();
+                else if (s + 2 < steps) stage_barrier<FILL>();
+                else stage_barrier<0>();
+                const int at = s & 3;
+                if (ragged && s + 2 == steps) clear_tail(at == 0 ? st1 : at == 1 ? st2 : at == 2 ? st3 : st0);
+                if (at == 0) supply(st0, s + 4);
+                else if (at == 1) supply(st1, s + 4);
+                else if (at == 2) supply(st2, s + 4);
+                else supply(st3, s + 4);
+            }
+            lds_barrier();
+            if (k == mine) break;
+            begin(g, rows);
+            __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);       // no stores behind its copies: they have to land
         }
-        if (!more) break;
     }
 }
 
