@@ -28,184 +28,252 @@ namespace w4a8 {
 constexpr int GS_WAVES = 8;
 constexpr int GS_CT = 4;                                        // column tiles of a workgroup
 
-// Byte within a 128-byte unit of the 16 bytes that lane group q holds in half h.  Packed codes: the layout's
-// k = 64 h + 16 q.  Row-major: 32 q + 16 h, so that a lane reads 32 neighbouring bytes; the order of k within a unit is
-// free as long as both operands have the same.
+// Byte within a 128-byte unit of the 16 bytes that lane group q takes in load h.  The order of k within a unit is free as
+// long as both operands have the same; it is chosen so that one load of the weights covers whole pieces of memory.
+// Row-major: 64 contiguous bytes of each row.  Packed codes (byte 64 h' + 16 q' of column c at (16 q' + c) * 32 + 16 h'):
+// the q' = 2 h, 2 h + 1 quarters with both their halves, a contiguous KiB.  (With 16 of every 32 bytes in a load, the
+// 256-expert steps read GS_OLD TB/s instead of GS_NEW.)
 template <int FMT>
 __device__ __forceinline__ unsigned unit_byte(int q, int h) {
-    return FMT == GF_I8 ? unsigned(64 * h + 16 * q) : unsigned(32 * q + 16 * h);
+    return FMT == GF_I8 ? unsigned(64 * (q & 1) + 32 * h + 16 * (q >> 1)) : unsigned(64 * h + 16 * q);
 }
 
-template <int FMT, bool PAIR, int MS, int D>
+// The slot-th tile of MT rows over the experts served by this launch, in expert order; every wave finds it alone.  expert is
+// -1 past the last tile.  The offsets of 256 experts are requested together, and the row range comes from the lane that
+// loaded it: one trip to memory for up to 256 experts.
+template <int MT>
+__device__ __forceinline__ TileRows grouped_find(const GroupedArgs& a, int slot, int lane) {
+    TileRows tr{0, 0, -1};
+    int base = 0;
+    for (int c0 = 0; c0 < a.E; c0 += 256) {
+        int b[4], e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int x = c0 + j * 64 + lane;
+            b[j] = x < a.E ? a.offsets[x] : 0;
+            e[j] = x < a.E ? a.offsets[x + 1] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // malformed offsets cannot move a tile outside the rows of the call
+            const int e0 = min(max(b[j], 0), a.rows), e1 = min(max(e[j], e0), a.rows), cnt = e1 - e0;
+            const int t = cnt >= a.lo && cnt < a.hi ? (cnt + MT - 1) / MT : 0;
+            int incl = t;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(incl, o, 64);
+                if (lane >= o) incl += y;
+            }
+            const unsigned long long hit = __ballot(slot >= base + incl - t && slot < base + incl);
+            if (hit) {
+                const int src = __ffsll((long long)hit) - 1;
+                tr.expert = c0 + j * 64 + src;
+                tr.rbeg = __builtin_amdgcn_readlane(e0 + (slot - base - (incl - t)) * MT, src);
+                tr.rend = min(__builtin_amdgcn_readlane(e1, src), tr.rbeg + MT);
+                return tr;
+            }
+            base += __builtin_amdgcn_readlane(incl, 63);
+        }
+    }
+    return tr;
+}
+
+template <int FMT, bool PAIR, int MS, int D, bool NT>
 __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kernel(GroupedArgs a, int ncb) {
     using acc_t = typename GroupedAcc<FMT>::type;
     constexpr int CT = GS_CT, COLS = PAIR ? 32 : 64;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slot = int(blockIdx.x) / ncb, cb = int(blockIdx.x) - slot * ncb;
-    TileRows tr;
-    {
-        GemmArgs g;                                             // moe_tile reads these members only
-        g.offsets = a.offsets;
-        g.E = a.E;
-        g.M = a.rows;
-        g.moe_lo = a.lo;
-        g.moe_hi = a.hi;
-        tr = moe_tile<16 * MS>(g, slot, lane);
-    }
-    const int expert = __builtin_amdgcn_readfirstlane(tr.expert);
-    if (expert < 0) return;                                     // uniform over the workgroup
-    const int rbeg = __builtin_amdgcn_readfirstlane(tr.rbeg), nrows = __builtin_amdgcn_readfirstlane(tr.rend) - rbeg;
     const int q = lane >> 4, c16 = lane & 15;
     const int units = (a.kb + 127) / 128;
+    const bool wide = grouped_wide(a);
+    for (unsigned item = blockIdx.x;; item += gridDim.x) {
+        const int slot = int(item / unsigned(ncb)), cb = int(item - unsigned(slot) * unsigned(ncb));
+        const TileRows tr = grouped_find<16 * MS>(a, slot, lane);
+        const int expert = __builtin_amdgcn_readfirstlane(tr.expert);
+        if (expert < 0) return;                                 // uniform over the workgroup; no later slot has a tile
+        const int rbeg = __builtin_amdgcn_readfirstlane(tr.rbeg), nrows = __builtin_amdgcn_readfirstlane(tr.rend) - rbeg;
 
-    // activation rows of this lane; rows past the tile repeat its first row (their sums are not stored)
-    const uint8_t* xrow[MS];
+        // weights: one buffer descriptor that ends with the last byte this workgroup may read (paired form: one for the
+        // gate and one for the up rows); offsets past it load zeros
+        const uint8_t* wexp = a.W + size_t(expert) * a.expert_stride;
+        __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1];
+        unsigned woff[CT];                                      // of this lane in each tile
+        constexpr unsigned NONE = 0x7ffffff0u;
+        if constexpr (FMT == GF_I8) {
+            const int tile0 = cb * CT, ntiles = (a.N + 15) / 16;
+            const unsigned tile_bytes = unsigned(units) * 2048u;
+            wr[0] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wexp + a.codes_off + size_t(tile0) * tile_bytes), 0,
+                                                      int(unsigned(min(CT, ntiles - tile0)) * tile_bytes), 0x00020000);
 #pragma unroll
-    for (int ms = 0; ms < MS; ++ms) {
-        const int row = ms * 16 + c16;
-        const int src = grouped_src(a, rbeg + (row < nrows ? row : 0));
-        xrow[ms] = a.X + size_t(src < 0 ? 0 : src) * size_t(a.ldx);
-    }
-
-    // weights: one buffer descriptor that ends with the last byte this workgroup may read (paired form: one for the
-    // gate and one for the up rows); offsets past it load zeros
-    const uint8_t* wexp = a.W + size_t(expert) * a.expert_stride;
-    __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1];
-    unsigned woff[CT];                                          // of this lane in each tile
-    constexpr unsigned NONE = 0x7ffffff0u;
-    if constexpr (FMT == GF_I8) {
-        const int tile0 = cb * CT, ntiles = (a.N + 15) / 16;
-        const unsigned tile_bytes = unsigned(units) * 2048u;
-        wr[0] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wexp + a.codes_off + size_t(tile0) * tile_bytes), 0,
-                                                  int(unsigned(min(CT, ntiles - tile0)) * tile_bytes), 0x00020000);
+            for (int t = 0; t < CT; ++t)
+                woff[t] = tile0 + t < ntiles ? t * tile_bytes + unsigned((q >> 1) * 16 + c16) * 32u + (q & 1) * 16u : NONE;
+        } else {
+            const int n0 = cb * COLS, nvalid = min(COLS, a.N - n0);
+            const unsigned extent = unsigned(nvalid - 1) * a.ldw + unsigned(a.kb);
 #pragma unroll
-        for (int t = 0; t < CT; ++t) woff[t] = tile0 + t < ntiles ? t * tile_bytes + lane * 32u : NONE;
-    } else {
-        const int n0 = cb * COLS, nvalid = min(COLS, a.N - n0);
-        const unsigned extent = unsigned(nvalid - 1) * a.ldw + unsigned(a.kb);
-#pragma unroll
-        for (int p = 0; p < (PAIR ? 2 : 1); ++p)
-            wr[p] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wexp + (size_t(n0) + (p ? a.N : 0)) * a.ldw), 0,
-                                                      int(extent), 0x00020000);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int col = (PAIR ? t & 1 : t) * 16 + c16;
-            woff[t] = col < nvalid ? unsigned(col) * a.ldw : NONE;
-        }
-    }
-
-    v4i wv[D][CT][2], xv[D][MS][2];
-    auto load = [&](const int d, const int u) __attribute__((always_inline)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const unsigned b = unsigned(u) * 128u + unit_byte<FMT>(q, h);
-            const bool in = b < unsigned(a.kb);
+            for (int p = 0; p < (PAIR ? 2 : 1); ++p)
+                wr[p] = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<uint8_t*>(wexp + (size_t(n0) + (p ? size_t(a.N) : 0)) * a.ldw), 0, int(extent), 0x00020000);
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
-                unsigned off;
-                if constexpr (FMT == GF_I8) off = in && woff[t] != NONE ? woff[t] + unsigned(u) * 2048u + 16u * h : NONE;
-                else off = in && woff[t] != NONE ? woff[t] + b : NONE;
-                wv[d][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wr[PAIR ? t >> 1 : 0], off, 0, 2);
+                const int col = (PAIR ? t & 1 : t) * 16 + c16;
+                woff[t] = col < nvalid ? unsigned(col) * a.ldw : NONE;
             }
-#pragma unroll
-            for (int ms = 0; ms < MS; ++ms) xv[d][ms][h] = *reinterpret_cast<const v4i*>(xrow[ms] + (in ? b : 0u));
         }
-    };
-    acc_t acc[CT][MS];
+        const uint8_t* xrow[MS];
+        v4i wv[D][CT][2], xv[D][MS][2];
+        // Both loads of a weight tile stand next to each other: they share its 128-byte lines.  The non-temporal hint (NT) is
+        // for calls that read more weights than the Infinity Cache holds, and for packed codes only: a load of row-major
+        // weights takes half a line of each row, and the hint lets the other half go before it is asked for.
+        auto load_w = [&](const int d, const int u) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
+            for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int ms = 0; ms < MS; ++ms) acc[t][ms] = acc_t{};
-
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(d, wave + d * GS_WAVES);
-    for (int u = wave; u < units; u += D * GS_WAVES) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int ud = u + d * GS_WAVES;
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned b = unsigned(u) * 128u + unit_byte<FMT>(q, h);
+                    const bool in = b < unsigned(a.kb) && woff[t] != NONE;
+                    const unsigned off = in ? woff[t] + (FMT == GF_I8 ? unsigned(u) * 2048u + 1024u * h : b) : NONE;
+                    wv[d][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wr[PAIR ? t >> 1 : 0], off, 0, NT ? 2 : 0);
+                }
+        };
+        auto load_x = [&](const int d, const int u) __attribute__((always_inline)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                // 16-bit values past the end of K: the weights are zero, and the activations have to be, since
-                // the bytes loaded in their place may hold an infinity or a NaN
-                const bool in = FMT == GF_I8 || unsigned(ud) * 128u + unit_byte<FMT>(q, h) < unsigned(a.kb);
+                const unsigned b = unsigned(u) * 128u + unit_byte<FMT>(q, h);
 #pragma unroll
-                for (int ms = 0; ms < MS; ++ms) {
-                    v4i x = xv[d][ms][h];
-                    if constexpr (FMT != GF_I8) x = in ? x : v4i{0, 0, 0, 0};
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) acc[t][ms] = grouped_mfma<FMT>(wv[d][t][h], x, acc[t][ms]);
-                }
+                for (int ms = 0; ms < MS; ++ms)
+                    xv[d][ms][h] = *reinterpret_cast<const v4i*>(xrow[ms] + (b < unsigned(a.kb) ? b : 0u));
             }
-            load(d, ud + D * GS_WAVES);
+        };
+        // activation rows of this lane; rows past the tile repeat its first row (their sums are not stored)
+        int src[MS];
+#pragma unroll
+        for (int ms = 0; ms < MS; ++ms) {
+            const int row = ms * 16 + c16;
+            src[ms] = grouped_src(a, rbeg + (row < nrows ? row : 0));
         }
-    }
+#pragma unroll
+        for (int d = 0; d < D; ++d) load_w(d, wave + d * GS_WAVES);
+#pragma unroll
+        for (int ms = 0; ms < MS; ++ms) xrow[ms] = a.X + size_t(src[ms] < 0 ? 0 : src[ms]) * size_t(a.ldx);
+#pragma unroll
+        for (int d = 0; d < D; ++d) load_x(d, wave + d * GS_WAVES);
 
-    // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
-    acc_t* red = reinterpret_cast<acc_t*>(smem);
-    constexpr int ITEMS = CT * MS * 64;
-    constexpr int KEPT = MS == 4 ? 4 : GS_WAVES;                // planes held at a time
-    if constexpr (KEPT < GS_WAVES) {
-        if (wave >= KEPT) {
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int ms = 0; ms < MS; ++ms) red[(wave - KEPT) * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
-        }
-        lds_barrier();
-        if (wave < KEPT) {
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int ms = 0; ms < MS; ++ms) acc[t][ms] += red[wave * ITEMS + (t * MS + ms) * 64 + lane];
-        }
-    }
-    if (wave < KEPT) {                                          // own plane: nobody else reads it before the barrier
+        acc_t acc[CT][MS];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
 #pragma unroll
-            for (int ms = 0; ms < MS; ++ms) red[wave * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
-    }
-    lds_barrier();
-    auto total = [&](const int item) __attribute__((always_inline)) {
-        acc_t s = red[item];
+            for (int ms = 0; ms < MS; ++ms) acc[t][ms] = acc_t{};
+        for (int u = wave; u < units; u += D * GS_WAVES) {
 #pragma unroll
-        for (int w = 1; w < KEPT; ++w) s += red[w * ITEMS + item];
-        return s;
-    };
-    const bool wide = grouped_wide(a);
-    for (int item = tid; item < (PAIR ? ITEMS / 2 : ITEMS); item += 512) {
-        const int l = item & 63, ms = (item >> 6) % MS, t = (item >> 6) / MS;
-        const int row = ms * 16 + (l & 15), col = cb * COLS + t * 16 + 4 * (l >> 4);
-        if (row >= nrows || col >= a.N) continue;
-        const acc_t s = total(item);
-        const int src = grouped_src(a, rbeg + row);
-        float y[4];
-        if constexpr (FMT == GF_I8) {
-            const float sxr = src < 0 ? 0.0f : a.sx[src];
-            const float4 sw = *reinterpret_cast<const float4*>(wexp + a.scales_off + size_t(col) * 4);
-            y[0] = (float(s[0]) * sw.x) * sxr;
-            y[1] = (float(s[1]) * sw.y) * sxr;
-            y[2] = (float(s[2]) * sw.z) * sxr;
-            y[3] = (float(s[3]) * sw.w) * sxr;
-        } else if constexpr (PAIR) {
-            const acc_t up = total(item + ITEMS / 2);
+            for (int d = 0; d < D; ++d) {
+                const int ud = u + d * GS_WAVES;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = src < 0 ? 0.0f : silu_gate(s[i]) * up[i];
-        } else {
+                for (int h = 0; h < 2; ++h) {
+                    // 16-bit values past the end of K: the weights are zero, and the activations have to be, since
+                    // the bytes loaded in their place may hold an infinity or a NaN
+                    const bool in = FMT == GF_I8 || unsigned(ud) * 128u + unit_byte<FMT>(q, h) < unsigned(a.kb);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = src < 0 ? 0.0f : s[i];
+                    for (int ms = 0; ms < MS; ++ms) {
+                        v4i x = xv[d][ms][h];
+                        if constexpr (FMT != GF_I8) x = in ? x : v4i{0, 0, 0, 0};
+#pragma unroll
+                        for (int t = 0; t < CT; ++t) acc[t][ms] = grouped_mfma<FMT>(wv[d][t][h], x, acc[t][ms]);
+                    }
+                }
+                load_w(d, ud + D * GS_WAVES);
+                load_x(d, ud + D * GS_WAVES);
+            }
         }
-        grouped_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), wide, y[0], y[1], y[2], y[3]);
+
+        // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
+        acc_t* red = reinterpret_cast<acc_t*>(smem);
+        constexpr int ITEMS = CT * MS * 64, OUT = PAIR ? ITEMS / 2 : ITEMS;
+        constexpr int KEPT = MS == 4 ? 4 : GS_WAVES;            // planes held at a time
+        if constexpr (KEPT < GS_WAVES) {
+            if (wave >= KEPT) {
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+#pragma unroll
+                    for (int ms = 0; ms < MS; ++ms) red[(wave - KEPT) * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
+            }
+            lds_barrier();
+            if (wave < KEPT) {
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+#pragma unroll
+                    for (int ms = 0; ms < MS; ++ms) acc[t][ms] += red[wave * ITEMS + (t * MS + ms) * 64 + lane];
+            }
+        }
+        if (wave < KEPT) {                                      // own plane: nobody else reads it before the barrier
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int ms = 0; ms < MS; ++ms) red[wave * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
+        }
+        // source rows and scales of this thread's outputs, in flight across the barrier
+        constexpr int PER = (OUT + 511) / 512;
+        int osrc[PER];
+        float osx[PER];
+        float4 osw[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int o = tid + i * 512, l = o & 63, row = ((o >> 6) % MS) * 16 + (l & 15);
+            const int col = cb * COLS + ((o >> 6) / MS) * 16 + 4 * (l >> 4);
+            osrc[i] = grouped_src(a, rbeg + (row < nrows ? row : 0));
+            if constexpr (FMT == GF_I8) {
+                osx[i] = osrc[i] < 0 ? 0.0f : a.sx[osrc[i]];
+                osw[i] = *reinterpret_cast<const float4*>(wexp + a.scales_off + size_t(min(col, (a.N - 1) & ~3)) * 4);
+            }
+        }
+        lds_barrier();
+        auto total = [&](const int o) __attribute__((always_inline)) {
+            acc_t s = red[o];
+#pragma unroll
+            for (int w = 1; w < KEPT; ++w) s += red[w * ITEMS + o];
+            return s;
+        };
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int o = tid + i * 512, l = o & 63, row = ((o >> 6) % MS) * 16 + (l & 15);
+            const int col = cb * COLS + ((o >> 6) / MS) * 16 + 4 * (l >> 4);
+            if (o >= OUT || row >= nrows || col >= a.N) continue;
+            const acc_t s = total(o);
+            float y[4];
+            if constexpr (FMT == GF_I8) {
+                y[0] = (float(s[0]) * osw[i].x) * osx[i];
+                y[1] = (float(s[1]) * osw[i].y) * osx[i];
+                y[2] = (float(s[2]) * osw[i].z) * osx[i];
+                y[3] = (float(s[3]) * osw[i].w) * osx[i];
+            } else if constexpr (PAIR) {
+                const acc_t up = total(o + ITEMS / 2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = osrc[i] < 0 ? 0.0f : silu_gate(s[k]) * up[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = osrc[i] < 0 ? 0.0f : s[k];
+            }
+            grouped_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), wide, y[0], y[1], y[2], y[3]);
+        }
+
+        if constexpr (MS == 1) return;                          // one tile a workgroup
+        lds_barrier();                                          // the planes are written again by the next tile
     }
 }
 
-template <int FMT, bool PAIR, int MS, int D>
+// Workgroups of a launch over `slots` row tiles: all tiles of the 16-row class; the other classes, which often have few
+// experts or none, go round in a grid that costs a few microseconds when it finds nothing (256 experts of 7168 columns:
+// 29 and 16 us with a workgroup for each possible tile).
+constexpr long long GS_GRID = 512;
+
+template <int FMT, bool PAIR, int MS, int D, bool NT>
 static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s) {
     constexpr size_t lds = size_t(MS == 4 ? 4 : GS_WAVES) * GS_CT * MS * 64 * 16;
     static_assert(lds <= 65536, "two workgroups of 16-row tiles share a compute unit");
     const int ncb = (a.N + (PAIR ? 31 : 63)) / (PAIR ? 32 : 64);
-    moe_grouped_stream_kernel<FMT, PAIR, MS, D><<<dim3(unsigned(slots * ncb)), dim3(512), lds, s>>>(a, ncb);
+    const long long blocks = MS == 1 ? slots * ncb : std::min(slots * ncb, GS_GRID);
+    moe_grouped_stream_kernel<FMT, PAIR, MS, D, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
 // Row classes of the streaming kernel, one launch each: an expert of up to 16 rows costs nothing for rows it does not
@@ -214,16 +282,23 @@ template <int FMT, bool PAIR>
 static void launch_grouped(GroupedArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
     a.lo = 1, a.hi = 17;
-    launch_stream_t<FMT, PAIR, 1, 2>(a, std::min(E, rows), s);
+    if constexpr (FMT == GF_I8) {
+        // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one:
+        // 6.4 GB of them 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
+        if (std::min(E, rows) * (long long)a.N * a.kb > (256ll << 20)) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
+        else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
+    } else {
+        launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
+    }
     if (rows > 16) {
         a.lo = 17, a.hi = 33;
-        launch_stream_t<FMT, PAIR, 2, 2>(a, std::min(E, rows / 17), s);
+        launch_stream_t<FMT, PAIR, 2, 2, false>(a, std::min(E, rows / 17), s);
     }
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     const bool near = a.ldx <= (1 << 24) && (!a.gather || (long long)a.src_rows * a.ldx < (1ll << 32) - 256);
     if (rows > 32) {
         a.lo = 33, a.hi = near ? 65 : 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 2>(a, near ? std::min(E, rows / 33) : rows / 64 + std::min(E, rows / 33), s);
+        launch_stream_t<FMT, PAIR, 4, 2, false>(a, near ? std::min(E, rows / 33) : rows / 64 + std::min(E, rows / 33), s);
     }
     if (rows > 64 && near) {
         a.lo = 65, a.hi = 0x7fffffff;
