@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t f32_to_f16_rne(float f) {
 // (one unit each) the result is good to about 4 units of float32, well inside the half step of the 16-bit types it is
 // rounded to.  (The library expf and an IEEE division took 6 us of every 125 us tile of the gate/up product.)
 __device__ __forceinline__ float silu_gate(float g) {
-    const float a = -fabsf(g), t = a * 1.44269502f;
+    const float a = fmaxf(-fabsf(g), -200.0f), t = a * 1.44269502f;    // exp(-200) is 0 in float32
     const float r = fmaf(a, 1.44269502f, -t) + a * 1.92596303e-8f;     // log2(e) = 1.44269502 + 1.926e-8
     float e = __builtin_amdgcn_exp2f(t);
     e = fmaf(e, r * 0.693147182f, e);

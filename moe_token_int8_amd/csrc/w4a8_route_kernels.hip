@@ -24,7 +24,8 @@ struct RouteArgs {
     float* w;
 };
 
-constexpr int ROUTE_WAVES = 4;      // tokens of a workgroup, one wave each
+constexpr int ROUTE_WAVES = 4;      // waves of a workgroup
+constexpr int ROUTE_SPREAD = 4096;  // tokens up to which each gets a wave
 
 __device__ __forceinline__ float route_logit(const RouteArgs& a, size_t i) {
     if (a.dtype == W4A8_F32) return static_cast<const float*>(a.logits)[i];
@@ -32,10 +33,229 @@ __device__ __forceinline__ float route_logit(const RouteArgs& a, size_t i) {
     return a.dtype == W4A8_F16 ? f16_to_f32(b) : bf16_to_f32(b);
 }
 
-// One wave per token; lane l holds the experts l, l + 64, ... (EPL of them).  Ranks are float64 throughout: a logit is
-// exact in it, and p + bias is compared where its last float32 digit would already decide between two experts.
+// exp(-a) for a >= 0 to about 2^-50: a = n ln 2 + r with |r| <= 0.35, the Taylor series of exp(-r) to the 12th power (the
+// next term is below 2^-52), scaled by 2^-n.
+__device__ __forceinline__ double exp_neg(double a) {
+    a = fmin(a, 750.0);                                         // exp(-750) is 0 in float64
+    const double n = rint(a * 1.4426950408889634);
+    double r = fma(n, -0.69314718036912382, a);                 // ln 2 in two parts, the first with 21 zero bits
+    r = -fma(n, -1.9082149292705877e-10, r);
+    double e = 1.0 / 479001600.0;
+    e = fma(e, r, 1.0 / 39916800.0);
+    e = fma(e, r, 1.0 / 3628800.0);
+    e = fma(e, r, 1.0 / 362880.0);
+    e = fma(e, r, 1.0 / 40320.0);
+    e = fma(e, r, 1.0 / 5040.0);
+    e = fma(e, r, 1.0 / 720.0);
+    e = fma(e, r, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return ldexp(e, -int(n));
+}
+
+// 1 / d for 1 <= d: the hardware's estimate (2^-23) and two Newton steps.
+__device__ __forceinline__ double reciprocal(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.0), r, r);
+    return fma(fma(-d, r, 1.0), r, r);
+}
+
+__device__ __forceinline__ double sigmoid64(float x) {
+    const double e = exp_neg(fabs(double(x))), d = reciprocal(1.0 + e);
+    return x >= 0.0f ? d : e * d;
+}
+
+// exp(-a) for a >= 0 in float32, good to about 2 units: v_exp_f32 of the product in two parts.
+__device__ __forceinline__ float exp_neg32(float a) {
+    a = fminf(a, 200.0f);                                       // exp(-200) is 0 in float32
+    const float t = -a * 1.44269502f, r = fmaf(-a, 1.44269502f, -t) - a * 1.92596303e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0.693147182f, e);
+}
+
+// A rank as a sorting key: the float64 value with its last 10 mantissa bits replaced by the index, turned so that of two
+// equal values the lower index is the larger key (of a negative value the larger mantissa is the smaller number).  One
+// v_max_f64 then compares value and index.  Logits are float32 and lose nothing; p + bias keeps 42 bits.
+constexpr double ROUTE_NONE = -1.7e308;                         // a masked or taken expert; ranks are above -1e39
+
+__device__ __forceinline__ double route_key(double v, int index) {
+    v = fmin(v + 0.0, 1e300);                                   // -0 equals 0; an infinite rank stays a number
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t low = (b >> 63) ? uint64_t(index) : uint64_t(1023 - index);
+    return __builtin_bit_cast(double, (b & ~uint64_t(1023)) | low);
+}
+__device__ __forceinline__ int route_index(double key) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, key);
+    return (b >> 63) ? int(b & 1023) : 1023 - int(b & 1023);
+}
+__device__ __forceinline__ double route_value(double key) {
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~uint64_t(1023));
+}
+
+// What the lane across from this one holds: STEP 0..3 exchange neighbours, pairs, quads and halves of 16 lanes (the last two
+// by mirroring, which is the same thing once the smaller groups agree), STEP 4 the 16s of 32 and STEP 5 the halves of 64.
+template <int STEP>
+__device__ __forceinline__ uint32_t route_across(uint32_t v) {
+    if constexpr (STEP == 0) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, true));
+    else if constexpr (STEP == 1) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, true));
+    else if constexpr (STEP == 2) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, true));
+    else if constexpr (STEP == 3) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, true));
+    else return uint32_t(__shfl_xor(int(v), STEP == 4 ? 16 : 32, 64));
+}
+template <int STEP>
+__device__ __forceinline__ double route_across(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = route_across<STEP>(uint32_t(b)), hi = route_across<STEP>(uint32_t(b >> 32));
+    return __builtin_bit_cast(double, hi << 32 | lo);
+}
+template <int STEP>
+__device__ __forceinline__ float route_across(float v) {
+    return __uint_as_float(route_across<STEP>(__float_as_uint(v)));
+}
+// v combined over the LANES lanes of a token, the same in all of them and in a fixed order
+template <int LANES, typename T, typename F>
+__device__ __forceinline__ T route_all(T v, F f) {
+    v = f(v, route_across<0>(v));
+    v = f(v, route_across<1>(v));
+    v = f(v, route_across<2>(v));
+    v = f(v, route_across<3>(v));
+    if constexpr (LANES > 16) v = f(v, route_across<4>(v));
+    if constexpr (LANES > 32) v = f(v, route_across<5>(v));
+    return v;
+}
+
+// LANES lanes per token, EPL neighbouring experts in each; k <= LANES rounds of an argmax over the keys.  With 16 lanes a
+// wave serves 4 tokens and most of a round is the 16 keys of a lane (for many tokens: the vector unit is the bound); with
+// 64 lanes a round is shortest (for few tokens: the latency is).  A group of experts is `glanes` (1, 2, 4, .. 16)
+// whole lanes.
+template <int LANES, int EPL>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a, int glanes) {
+    constexpr int TOKENS = 64 / LANES * ROUTE_WAVES;
+    const int lane = threadIdx.x % LANES, e0 = lane * EPL;
+    const int t0 = int(blockIdx.x) * TOKENS + int(threadIdx.x) / LANES;
+    const int t = min(t0, a.T - 1);                             // every lane takes part in the exchanges
+    const size_t row = size_t(t) * size_t(a.ldl);
+    const auto max64 = [](double x, double y) { return fmax(x, y); };
+
+    float x[EPL];
+    const bool full = e0 + EPL <= a.E;
+    if (EPL % 4 == 0 && a.dtype == W4A8_F32 && full && a.ldl % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < EPL; j += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0 + j);
+            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) x[j] = e0 + j < a.E ? route_logit(a, row + e0 + j) : -__builtin_huge_valf();
+    }
+    bool bad = false;
+    float top = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        bad |= x[j] != x[j] || (!a.sigmoid && x[j] == __builtin_huge_valf());
+        top = fmaxf(top, x[j]);
+    }
+    const auto max32 = [](float u, float v) { return fmaxf(u, v); };
+    double key[EPL], sum = 1.0;                                 // sum: softmax denominator
+    if (!a.sigmoid) top = route_all<LANES>(top, max32);
+    const float ref = top > -__builtin_huge_valf() ? top : 0.0f;
+    if (a.bias) {
+        double p[EPL];
+        if (a.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) p[j] = sigmoid64(x[j]);
+        } else {
+            sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                p[j] = exp_neg(double(ref) - double(x[j]));
+                sum += p[j];
+            }
+            sum = route_all<LANES>(sum, [](double u, double v) { return u + v; });
+            const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) p[j] *= inv;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const double r = p[j] + double(e0 + j < a.E ? a.bias[e0 + j] : 0.0f);
+            const bool masked = x[j] == -__builtin_huge_valf() || r < -1e39;
+            bad |= r != r;
+            key[j] = masked ? ROUTE_NONE : route_key(r, e0 + j);
+        }
+    } else {
+        if (!a.sigmoid) {
+            float part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) part += exp_neg32(ref - x[j]);
+            sum = double(route_all<LANES>(part, [](float u, float v) { return u + v; }));
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = x[j] == -__builtin_huge_valf() ? ROUTE_NONE : route_key(double(x[j]), e0 + j);
+    }
+    bad = route_all<LANES>(uint32_t(bad), [](uint32_t u, uint32_t v) { return u | v; }) != 0;
+
+    if (a.groups > 1) {
+        double b1 = ROUTE_NONE, b2 = ROUTE_NONE;                // the group's two best
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            b2 = fmax(b2, fmin(b1, key[j]));
+            b1 = fmax(b1, key[j]);
+        }
+        auto merge = [&](double c1, double c2) __attribute__((always_inline)) {
+            b2 = fmax(fmax(b2, c2), fmin(b1, c1));
+            b1 = fmax(b1, c1);
+        };
+        if (glanes > 1) merge(route_across<0>(b1), route_across<0>(b2));
+        if (glanes > 2) merge(route_across<1>(b1), route_across<1>(b2));
+        if (glanes > 4) merge(route_across<2>(b1), route_across<2>(b2));
+        if (glanes > 8) merge(route_across<3>(b1), route_across<3>(b2));
+        const int group = lane / glanes;
+        double score = ROUTE_NONE;
+        if (b1 > -1e300 && group < a.groups)
+            score = route_key(a.bias && b2 > -1e300 ? route_value(b1) + route_value(b2) : route_value(b1), group);
+        bool kept = false;
+        for (int r = 0; r < a.keep; ++r) {
+            const double best = route_all<LANES>(score, max64);
+            if (best > -1e300 && score == best) kept = true, score = ROUTE_NONE;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : ROUTE_NONE;
+    }
+
+    int id = -1;                                                // of round `lane`
+    for (int r = 0; r < a.k; ++r) {
+        double best = key[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) best = fmax(best, key[j]);
+        best = route_all<LANES>(best, max64);
+        if (lane == r && best > -1e300) id = route_index(best);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = key[j] == best ? ROUTE_NONE : key[j];
+    }
+    double w = 0.0;
+    if (id >= 0) {
+        const float v = route_logit(a, row + id);
+        w = a.sigmoid ? sigmoid64(v) : exp_neg(double(ref) - double(v)) / sum;
+    }
+    if (a.renorm) {
+        const double s = route_all<LANES>(w, [](double u, double v) { return u + v; });
+        w = s > 0.0 ? w / s : 0.0;
+    }
+    if (lane < a.k && t0 < a.T) {
+        a.ids[size_t(t) * a.k + lane] = bad ? lane : id;
+        a.w[size_t(t) * a.k + lane] = bad ? __builtin_nanf("") : float(w * double(a.scale));
+    }
+}
+
+// Groups that do not fall on whole lanes of the kernel above: one wave per token, the ranks in LDS for the group scores.
+// Lane l holds the experts l, l + 64, ... (EPL of them); ranks as above.
 template <int EPL>
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_any_groups_kernel(RouteArgs a) {
     extern __shared__ double route_lds[];                       // per wave: ranks [E], scores [E]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int t = blockIdx.x * ROUTE_WAVES + wave;
@@ -61,7 +281,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const bool masked = x[j] == -__builtin_huge_valf();
-        p[j] = masked ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-double(x[j]))) : exp(double(x[j]) - double(top));
+        p[j] = masked ? 0.0 : a.sigmoid ? sigmoid64(x[j]) : exp_neg(double(top) - double(x[j]));
         sum += p[j];
     }
     if (!a.sigmoid) {
@@ -74,8 +294,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
     for (int j = 0; j < EPL; ++j) {
         const int e = j * 64 + lane;
         const bool masked = x[j] == -__builtin_huge_valf();
-        rank[j] = masked ? NEG : a.bias ? p[j] + double(a.bias[e]) : double(x[j]);
+        rank[j] = masked ? NEG : a.bias ? (e < a.E ? p[j] + double(a.bias[e]) : 0.0) : double(x[j]);
         bad |= rank[j] != rank[j];
+        if (!masked && a.bias) rank[j] = rank[j] < -1e39 ? NEG : route_value(rank[j]);
         if (e < a.E) {
             lrank[e] = rank[j];
             lp[e] = p[j];
@@ -178,13 +399,25 @@ extern "C" int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, con
         return W4A8_EINVAL;
     const RouteArgs a{logits, dtype, T, ldl, bias, d->E, d->k, d->score == W4A8_ROUTE_SIGMOID, d->renormalize, groups, keep,
                       d->scale, ids, w};
-    const dim3 grid((T + ROUTE_WAVES - 1) / ROUTE_WAVES), block(64 * ROUTE_WAVES);
-    const size_t lds = size_t(ROUTE_WAVES) * 2 * d->E * sizeof(double);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (d->E <= 64) moe_route_kernel<1><<<grid, block, lds, s>>>(a);
-    else if (d->E <= 128) moe_route_kernel<2><<<grid, block, lds, s>>>(a);
-    else if (d->E <= 256) moe_route_kernel<4><<<grid, block, lds, s>>>(a);
-    else if (d->E <= 512) moe_route_kernel<8><<<grid, block, lds, s>>>(a);
-    else moe_route_kernel<16><<<grid, block, lds, s>>>(a);
+    // 64 lanes a token where the waves of all tokens fit the chip at once, or where the rounds need more than 16 lanes
+    const bool spread = T <= ROUTE_SPREAD || d->k > 16 || d->E > 256;
+    const int epl = spread ? (d->E <= 256 ? 4 : 16) : d->E <= 64 ? 4 : d->E <= 128 ? 8 : 16;
+    const int size = d->E / groups, glanes = size / epl;
+    if (groups > 1 && (size % epl || glanes > 16 || (glanes & (glanes - 1)))) {
+        const dim3 grid((T + ROUTE_WAVES - 1) / ROUTE_WAVES), block(64 * ROUTE_WAVES);
+        const size_t lds = size_t(ROUTE_WAVES) * 2 * d->E * sizeof(double);
+        if (d->E <= 64) moe_route_any_groups_kernel<1><<<grid, block, lds, s>>>(a);
+        else if (d->E <= 256) moe_route_any_groups_kernel<4><<<grid, block, lds, s>>>(a);
+        else moe_route_any_groups_kernel<16><<<grid, block, lds, s>>>(a);
+    } else {
+        const int tokens = ROUTE_WAVES * (spread ? 1 : 4);
+        const dim3 grid((T + tokens - 1) / tokens), block(64 * ROUTE_WAVES);
+        if (spread && epl == 4) moe_route_kernel<64, 4><<<grid, block, 0, s>>>(a, glanes);
+        else if (spread) moe_route_kernel<64, 16><<<grid, block, 0, s>>>(a, glanes);
+        else if (epl == 4) moe_route_kernel<16, 4><<<grid, block, 0, s>>>(a, glanes);
+        else if (epl == 8) moe_route_kernel<16, 8><<<grid, block, 0, s>>>(a, glanes);
+        else moe_route_kernel<16, 16><<<grid, block, 0, s>>>(a, glanes);
+    }
     return hipGetLastError() == hipSuccess ? W4A8_OK : W4A8_EHIP;
 }
