@@ -278,27 +278,33 @@ static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s
 
 // Row classes of the streaming kernel, one launch each: an expert of up to 16 rows costs nothing for rows it does not
 // have, and the launches of classes that no expert can be in are left out.  `slots` bounds the row tiles of the class.
+// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles, since each
+// launch that finds nothing costs 5 us (8192-token prompts: GS_PROMPT us).
 template <int FMT, bool PAIR>
 static void launch_grouped(GroupedArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
-    a.lo = 1, a.hi = 17;
-    if constexpr (FMT == GF_I8) {
-        // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one:
-        // 6.4 GB of them 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
-        if (std::min(E, rows) * (long long)a.N * a.kb > (256ll << 20)) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
-        else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
-    } else {
-        launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
-    }
-    if (rows > 16) {
-        a.lo = 17, a.hi = 33;
-        launch_stream_t<FMT, PAIR, 2, 2, false>(a, std::min(E, rows / 17), s);
-    }
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
-    const bool near = a.ldx <= (1 << 24) && (!a.gather || (long long)a.src_rows * a.ldx < (1ll << 32) - 256);
+    constexpr long long REACH = 0xe0000000ll;
+    const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
+    const bool few_small = near && rows >= 128 * E;
+    if (!few_small) {
+        a.lo = 1, a.hi = 17;
+        if constexpr (FMT == GF_I8) {
+            // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one:
+            // 6.4 GB of them 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
+            if (std::min(E, rows) * (long long)a.N * a.kb > (256ll << 20)) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
+            else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
+        } else {
+            launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
+        }
+        if (rows > 16) {
+            a.lo = 17, a.hi = 33;
+            launch_stream_t<FMT, PAIR, 2, 2, false>(a, std::min(E, rows / 17), s);
+        }
+    }
     if (rows > 32) {
-        a.lo = 33, a.hi = near ? 65 : 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 2, false>(a, near ? std::min(E, rows / 33) : rows / 64 + std::min(E, rows / 33), s);
+        a.lo = few_small ? 1 : 33, a.hi = near ? 65 : 0x7fffffff;
+        launch_stream_t<FMT, PAIR, 4, 2, false>(a, near ? std::min(E, rows / a.lo) : rows / 64 + std::min(E, rows / 33), s);
     }
     if (rows > 64 && near) {
         a.lo = 65, a.hi = 0x7fffffff;
