@@ -12,23 +12,24 @@
 namespace w4a8 {
 
 // A persistent workgroup of 8 waves per compute unit walks over 256-row x 256-column tiles (paired form: 128 gate and the
-// matching 128 up columns).  A step is 64 bytes of K: the 256 activation rows and 256 weight rows are copied straight
-// from memory to LDS (16 bytes a lane, no registers in between) into a ring of four 32 KiB stages, three steps ahead of
-// the MFMAs.  Wave (wm, wn) owns rows 128 wm .. + 127 and 64 columns: 8 x 4 MFMA tiles, 128 accumulators a lane.
+// matching 128 up columns).  A step is 128 bytes of K, a cache line of every row: the 256 activation rows and 256 weight
+// rows are copied straight from memory to LDS (16 bytes a lane, no registers in between), into two 64 KiB stages, one
+// step ahead of the MFMAs.  (Four stages of 64 bytes keep more copies in flight, but ask for every line twice: steps of
+// K = 4096 took 2.0 us against 1.75.)  Wave (wm, wn) owns rows 128 wm .. + 127 and 64 columns: 8 x 4 MFMA tiles, 128
+// accumulators a lane.
 constexpr int GT_M = 256, GT_N = 256;
-constexpr int GT_STEP = 64;                                     // bytes of K in a step
+constexpr int GT_STEP = 128;                                    // bytes of K in a step
 constexpr int GT_STAGE = (GT_M + GT_N) * GT_STEP;
 constexpr int GT_WOFF = GT_M * GT_STEP;                         // weights within a stage
 constexpr int GT_PANEL = 4;                                     // row tiles of a panel of consecutive tiles
 constexpr int GT_MAX_E = 1024;
-constexpr unsigned GT_NOWHERE = 0xf0000000u;                    // past every descriptor, with room for the offset along K
 constexpr int GT_LIST = 512;                                    // tiles looked up at a time, one a thread
 
-// LDS image of a stage: rows of 64 bytes in four 16-byte chunks, the activations' 256, then the weights'.  Chunk c of row
+// LDS image of a stage: rows of 128 bytes in eight 16-byte chunks, the activations' 256, then the weights'.  Chunk c of row
 // r sits at position c ^ row_swizzle(r): 16 rows read at one chunk, and the halves of two neighbouring chunks that the
-// LDS serves together, then lie in distinct banks.  (Weights in 8-bit codes keep the MFMA operand's own order, 1 KiB a
-// 16-column tile, which is read in a row.)
-__device__ __forceinline__ int row_swizzle(int r) { return -(r >> 2) & 3; }
+// LDS serves together, then lie in distinct banks.  Weights in 8-bit codes keep the packed layout's order within 16
+// columns, 2 KiB, with neighbouring chunks swapped in the upper 8 columns for the same reason.
+__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
 
 // Stages are addressed as LDS objects, not through generic pointers, and copied into through buffer descriptors: the
 // compiler then sees that a read of one stage does not touch the others, and waits neither for the copies in flight into
@@ -78,13 +79,12 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     constexpr int COLS = PAIR ? GT_N / 2 : GT_N;                // columns of Y
     __shared__ __align__(1024) uint8_t stage0[GT_STAGE];
     __shared__ __align__(1024) uint8_t stage1[GT_STAGE];
-    __shared__ __align__(1024) uint8_t stage2[GT_STAGE];
-    __shared__ __align__(1024) uint8_t stage3[GT_STAGE];
     __shared__ int4 list[GT_LIST];                              // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[GT_MAX_E + 1];                         // row tiles before expert e
     __shared__ float rowscale[2][GT_M];                         // of this tile's rows and the next one's
+    __shared__ int entries[GT_M];                               // gather entries of the next tile's rows
     __shared__ int wsum[8];
-    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1, st2 = (lds_ptr)stage2, st3 = (lds_ptr)stage3;
+    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1;
     const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int q = lane >> 4, c16 = lane & 15;
     const int ncb = (a.N + COLS - 1) / COLS;
@@ -152,64 +152,56 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     auto clear_tail = [&](lds_ptr st) __attribute__((always_inline)) {
         const int row = opaque(int(threadIdx.x));
 #pragma unroll 1
-        for (int c = (a.kb % GT_STEP) >> 4; c < 4; ++c)
+        for (int c = (a.kb % GT_STEP) >> 4; c < 8; ++c)
             *(LDS v4i*)(st + row * GT_STEP + (c ^ row_swizzle(row)) * 16) = v4i{0, 0, 0, 0};
         lds_barrier();
     };
 
-    // Sources of this thread's copies, 2 of the 16 groups of 16 activation rows and 2 of the weights' 16 KiB, as byte
-    // offsets from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.  Rows past
-    // the tile's last, weight rows past the last column and bytes past the last row's K lie outside it and load nothing.
-    unsigned xoff[2], woff;
+    // Sources of this thread's copies, 4 of the 32 groups of 8 activation rows and 4 of the weights' 32 KiB, as byte offsets
+    // from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.  Rows past the
+    // tile's last, weight rows past the last column and bytes past the last row's K lie outside it and load nothing.
+    unsigned xoff[4], woff;
     __amdgpu_buffer_rsrc_t xr, wr[PAIR ? 2 : 1];                // paired form: gate rows, up rows
-    const unsigned tile_bytes = unsigned(steps / 2) * 2048u;    // GF_I8: 16 columns of codes
-    const unsigned wgroup = FMT == GF_I8 ? 8u * tile_bytes : PAIR ? 0u : 128u * a.ldw;     // between the two copies
-    // Workgroups that share rows or columns take the 128-byte lines of every four in another order, each starting at its
-    // own: of what they all need, each fetches a part ahead of the others, and four neighbouring lines are wanted from
-    // memory at a time (8192-token down product 0.66 -> 0.64 ms; orders over two or eight lines gain half of that).
+    const unsigned tile_bytes = unsigned(steps) * 2048u;        // GF_I8: 16 columns of codes
+    const unsigned wgroup = FMT == GF_I8 ? 4u * tile_bytes : 64u * a.ldw;   // from one copy to the next
+    // Workgroups that share rows or columns take the steps of every four in another order, each starting at its own: of the
+    // lines that they all need, each then fetches a part ahead of the others, and a DRAM page is asked for four
+    // neighbouring lines at a time.
     int turn = 0;
-    const int fours = (a.kb / 128) & ~3;                        // whole lines, in fours
-    auto fill = [&](lds_ptr st, const int s0) __attribute__((always_inline)) {
-        const int line = s0 >> 1;
-        const int s = line < fours ? 2 * ((line & ~3) | ((line + turn) & 3)) + (s0 & 1) : s0;
-        const unsigned wstep = FMT == GF_I8 ? unsigned(s >> 1) * 2048u + unsigned(s & 1) * 16u : unsigned(s) * GT_STEP;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * 8 + wave) * 1024);
-            copy_to_lds(wr[PAIR ? i : 0], woff + (wstep + i * wgroup), st + GT_WOFF + (i * 8 + wave) * 1024);
-        }
+    const int whole_fours = (a.kb / GT_STEP) & ~3;
+    auto fill_part = [&](lds_ptr st, const int s0, const int part) __attribute__((always_inline)) {
+        const int s = s0 < whole_fours ? (s0 & ~3) | ((s0 + turn) & 3) : s0, i = part >> 1;
+        const unsigned wstep = unsigned(s) * (FMT == GF_I8 ? 2048u : GT_STEP);
+        if (part & 1) copy_to_lds(wr[PAIR ? i >> 1 : 0], woff + (wstep + (PAIR ? i & 1 : i) * wgroup), st + GT_WOFF + (i * 8 + wave) * 1024);
+        else copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * 8 + wave) * 1024);
     };
-    constexpr int FILL = 4;                                     // copies of a wave in one fill
+    constexpr int FILL = 8;                                     // copies of a wave in one fill
 
-    // The MFMA loop is four steps long and has no other exit, so that the accumulators stay where they are: K is rounded up
-    // to whole turns of the ring with steps of zeros (none where a row is a multiple of 256 bytes).
-    const int turns = (steps + 3) / 4;
-    auto supply = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
-        if (s < steps) {
-            fill(st, s);
-        } else if (s < 4 * turns) {
+    // The MFMA loop is two steps long and has no other exit, so that the accumulators stay where they are: an odd number
+    // of steps is rounded up with one of zeros.
+    const int turns = (steps + 1) / 2;
+    auto fill = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int part = 0; part < FILL; ++part) fill_part(st, s, part);
+    };
+    auto pad = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
+        if (s < 2 * turns) {
             const int tid = opaque(int(threadIdx.x));
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) *(LDS v4i*)(st + (c * 512 + tid) * 16) = v4i{0, 0, 0, 0};
+            for (int c = 0; c < GT_STAGE / 8192; ++c) *(LDS v4i*)(st + (c * 512 + tid) * 16) = v4i{0, 0, 0, 0};
         }
+    };
+    auto supply = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
+        if (s < steps) fill(st, s);
+        else pad(st, s);
     };
 
-    // Gather entries of a tile's rows: those of this thread's copies, and row threadIdx.x for its scale.
-    struct Rows {
-        int copy[2], own;
-    };
-    auto fetch_rows = [&](const int rbeg, const int nrows) __attribute__((always_inline)) {
-        const int tid = opaque(int(threadIdx.x));
-        Rows r;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = (i * 8 + (tid >> 6)) * 16 + ((tid & 63) >> 2);
-            r.copy[i] = row;
-            if (a.gather) r.copy[i] = a.gather[rbeg + min(row, nrows - 1)];
-        }
-        r.own = tid < nrows ? rbeg + tid : -1;
-        if (a.gather && tid < nrows) r.own = a.gather[r.own];
-        return r;
+    // Gather entries of a tile's rows, copied to LDS a tile ahead.
+    auto request_rows = [&](const int4 g) __attribute__((always_inline)) {
+        if (a.gather && wave < GT_M / 64)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(reinterpret_cast<const uint8_t*>(a.gather + g.y), size_t(g.z) * 4),
+                                                     (LDS void*)((LDS int*)entries + wave * 64), 4,
+                                                     unsigned(opaque(int(threadIdx.x))) * 4u, 0, 0, 0);
     };
     auto source = [&](const int g) __attribute__((always_inline)) {    // row of X, or -1
         if (!a.gather) return g;
@@ -219,7 +211,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     // scale of row threadIdx.x; 16 bit: 0 marks a gather entry that names no row
     float own_scale = 0.0f;
     // descriptors, offsets and row scales of a tile, and the copies of its first steps
-    auto begin = [&](const int4 g, const Rows r) __attribute__((always_inline)) {
+    auto begin = [&](const int4 g) __attribute__((always_inline)) {
         const int tid = opaque(int(threadIdx.x)), lane = tid & 63, wave = tid >> 6;
         const uint8_t* wexp = a.W + size_t(g.x) * a.expert_stride;
         const int last_col = min(COLS, a.N - g.w * COLS) - 1;
@@ -233,44 +225,46 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
                 wr[p] = buffer_of(wexp + (size_t(g.w) * COLS + size_t(p) * size_t(a.N)) * a.ldw,
                                   size_t(last_col) * a.ldw + size_t(a.kb));
         }
-        const int own = source(r.own);
+        const int own = tid < g.z ? source(a.gather ? entries[tid] : g.y + tid) : -1;
         own_scale = own < 0 ? 0.0f : 1.0f;
         if (FMT == GF_I8 && own >= 0) own_scale = a.sx[own];
-        const int chunk = (lane & 3) ^ row_swizzle(lane >> 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {                           // (opaque: a fused multiply-add would leave 64-bit results)
-            xoff[i] = unsigned(opaque(int(unsigned(max(source(r.copy[i]), 0)) * unsigned(a.ldx)))) + unsigned(chunk) * 16u;
-            if ((i * 8 + wave) * 16 + (lane >> 2) >= g.z) xoff[i] = GT_NOWHERE;
-        }
         turn = __builtin_amdgcn_readfirstlane(g.y / GT_M + g.w);
-        if constexpr (FMT == GF_I8) {
-            const int col = (wave >> 2) * 64 + tile_column(f32, wave & 3, lane & 15);
-            woff = unsigned(opaque(int(unsigned(col >> 4) * tile_bytes))) + unsigned((lane >> 4) * 16 + (col & 15)) * 32u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                           // (opaque: a fused multiply-add would leave 64-bit results)
+            const int row = (i * 8 + wave) * 8 + (lane >> 3), chunk = (lane & 7) ^ row_swizzle(row);
+            xoff[i] = unsigned(opaque(int(unsigned(max(source(a.gather ? entries[row] : row), 0)) * unsigned(a.ldx)))) + unsigned(chunk) * 16u;
+            if (row >= g.z) xoff[i] = 0xf0000000u;
+        }
+        if constexpr (FMT == GF_I8) {                           // tile wave / 2 of column block i, half its chunks
+            const int p = (wave & 1) * 64 + (lane ^ ((lane >> 4) & 1)), col = tile_column(f32, wave >> 1, (p >> 1) & 15);
+            woff = unsigned(opaque(int(unsigned(col >> 4) * tile_bytes))) + unsigned((p >> 5) * 16 + (col & 15)) * 32u +
+                   unsigned(p & 1) * 16u;
         } else {
-            const int col = PAIR ? (wave >> 1) * 32 + tile_column(false, wave & 1, lane >> 2)
-                                 : (wave >> 2) * 64 + tile_column(f32, wave & 3, lane >> 2);
-            woff = unsigned(opaque(int(unsigned(col) * a.ldw))) + unsigned(chunk) * 16u;
+            const int row = wave * 8 + (lane >> 3), n = (wave >> 1) & (PAIR ? 1 : 3);
+            const int col = (PAIR ? (wave >> 2) * 32 : 0) + tile_column(f32, n, row & 15);
+            woff = unsigned(opaque(int(unsigned(col) * a.ldw))) + unsigned((lane & 7) ^ row_swizzle(row)) * 16u;
         }
         supply(st0, 0);
         supply(st1, 1);
-        supply(st2, 2);
-        supply(st3, 3);
     };
 
-    // Operands of a stage: the 4 weight tiles, and 4 of the 8 row tiles.  The compiler may not see into the byte offsets: it
-    // would rebuild each address from its terms and lose which stage it belongs to.
+    // Operands of half h (64 bytes of K) of a stage: the 4 weight tiles, and 4 of the 8 row tiles.  Lane group q takes chunk
+    // 4 h + q, the packed layout's order.  The compiler may not see into the byte offsets: it would rebuild each address from
+    // its terms and lose which stage it belongs to.
     const int wm = wave >> 2, wn = wave & 3;
-    const int pos = (q ^ row_swizzle(c16)) * 16;
-    const int xat = opaque((wm * 128 + c16) * GT_STEP + pos);
-    const int wat = opaque(GT_WOFF + (FMT == GF_I8 ? wn * 4096 + lane * 16 : ((PAIR ? wn * 32 : wn * 64) + c16) * GT_STEP + pos));
-    auto read_w = [&](const lds_ptr st, v4i (&w)[4]) __attribute__((always_inline)) {
+    int xat[2], wat[2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            w[n] = *(const LDS v4i*)(st + wat + (PAIR ? (n >> 1) * 128 * GT_STEP + (n & 1) * 1024 : n * 1024));
+    for (int h = 0; h < 2; ++h) {
+        const int pos = ((4 * h + q) ^ row_swizzle(c16)) * 16;
+        xat[h] = opaque((wm * 128 + c16) * GT_STEP + pos);
+        wat[h] = opaque(GT_WOFF + (FMT == GF_I8 ? wn * 8192 + (2 * lane + (h ^ (c16 >> 3))) * 16
+                                                : ((PAIR ? wn * 32 : wn * 64) + c16) * GT_STEP + pos));
+    }
+    auto read_w = [&](const lds_ptr st, const int h, const int n) __attribute__((always_inline)) {
+        return *(const LDS v4i*)(st + wat[h] + (PAIR ? (n >> 1) * 128 * GT_STEP + (n & 1) * 2048 : n * 2048));
     };
-    auto read_x = [&](const lds_ptr st, const int mh, v4i (&x)[4]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = *(const LDS v4i*)(st + xat + (mh * 4 + m) * 1024);
+    auto read_x = [&](const lds_ptr st, const int h, const int m) __attribute__((always_inline)) {
+        return *(const LDS v4i*)(st + xat[h] + m * 2048);
     };
 
     // With whole aligned 16-byte stores and row offsets that fit 32 bits, every wave that computed ends a tile with at least
@@ -279,7 +273,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     const int quantum = f32 ? 3 : 7;
     const bool regular = (a.N & quantum) == 0 && (a.ldy & quantum) == 0 && a.ldy < (size_t(1) << 21) &&
                          (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0;
-    const bool behind_stores = regular && steps >= 8;
+    const bool behind_stores = regular && steps >= 2;
 
     look_up(0);
     int4 g = list[0];
@@ -288,21 +282,22 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
                          __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
     };
     g = uniform(g);
-    begin(g, fetch_rows(g.y, g.z));
+    request_rows(g);
+    stage_barrier<0>();
+    begin(g);
     __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);               // vmcnt 0: no stores stand behind the first copies
     for (int k = 0;;) {
         const int4 cur = g;
         const int buf = k & 1;
-        if (behind_stores) stage_barrier<3 * FILL + STORES>();
+        if (behind_stores) stage_barrier<FILL + STORES>();
         else stage_barrier<0>();
         if (threadIdx.x < GT_M) rowscale[buf][threadIdx.x] = own_scale;
         if (ragged && steps == 1) clear_tail(st0);
         // the next tile, and its gather entries: requested here, first needed at the end of this tile
-        Rows rows;
         if (++k < mine) {
             if (k % GT_LIST == 0) look_up(k);
             g = uniform(list[k % GT_LIST]);
-            rows = fetch_rows(g.y, g.z);
+            request_rows(g);
         }
         if (wm * 128 < cur.z) {
             acc_t acc[4][8];
@@ -310,40 +305,55 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 8; ++m) acc[n][m] = acc_t{};
-            auto mfma = [&](const v4i (&w)[4], const v4i (&x)[4], const int mh) __attribute__((always_inline)) {
+            // 4 of the 64 MFMAs of a step: row tile m against the 4 weight tiles
+            auto mfma4 = [&](const v4i (&w)[4], const v4i x, const int m) __attribute__((always_inline)) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) acc[n][mh * 4 + m] = grouped_mfma<FMT>(w[n], x[m], acc[n][mh * 4 + m]);
+                for (int n = 0; n < 4; ++n) acc[n][m] = grouped_mfma<FMT>(w[n], x, acc[n][m]);
                 __builtin_amdgcn_sched_barrier(0);
             };
             v4i wa[4], wb[4], xa[4], xb[4];
-            // One step: two groups of 16 MFMAs, the operands of each read from LDS during the group before it.  The barrier
-            // stands before the second group, when this stage's last operands are in registers: behind it the next stage
-            // is whole, with the copies of the two after it in flight, and this one is free for the fourth.
-            auto step = [&](const lds_ptr st, const lds_ptr next, v4i (&w)[4], v4i (&wnext)[4], const int s,
-                            const bool early) __attribute__((always_inline)) {
-                read_x(st, 1, xb);
-                mfma(w, xa, 0);
-                if (early) stage_barrier<2 * FILL + STORES>();
-                else if (s + 3 < steps) stage_barrier<2 * FILL>();
-                else if (s + 2 < steps) stage_barrier<FILL>();
+            // One step: four groups of 16 MFMAs, the operands of each read from LDS during the group before it.  The barrier
+            // stands before the last group, when this step's last operands are in registers: behind it the next stage is
+            // whole and this one is free for the copies of the step after.
+            auto step = [&](const lds_ptr st, const lds_ptr next, const int s, const bool early) __attribute__((always_inline)) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    xb[m] = read_x(st, 0, 4 + m);
+                    mfma4(wa, xa[m], m);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    wb[m] = read_w(st, 1, m);
+                    xa[m] = read_x(st, 1, m);
+                    mfma4(wa, xb[m], 4 + m);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    xb[m] = read_x(st, 1, 4 + m);
+                    mfma4(wb, xa[m], m);
+                }
+                if (early) stage_barrier<STORES>();
                 else stage_barrier<0>();
                 if (ragged && s + 2 == steps) clear_tail(next);
-                read_w(next, wnext);
-                read_x(next, 0, xa);
-                supply(st, s + 4);
-                mfma(w, xb, 1);
+                const bool more = s + 2 < steps;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    wa[m] = read_w(next, 0, m);
+                    xa[m] = read_x(next, 0, m);
+                    if (more) {
+                        fill_part(st, s + 2, 2 * m);
+                        fill_part(st, s + 2, 2 * m + 1);
+                    }
+                    mfma4(wb, xb[m], 4 + m);
+                }
+                if (!more) pad(st, s + 2);
             };
-            read_w(st0, wa);
-            read_x(st0, 0, xa);
-            for (int s = 0; s < steps; s += 4) {
-                const bool early = behind_stores && s == 0;
-                step(st0, st1, wa, wb, s, early);
-                step(st1, st2, wb, wa, s + 1, early);
-                step(st2, st3, wa, wb, s + 2, early);
-                step(st3, st0, wb, wa, s + 3, false);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) wa[m] = read_w(st0, 0, m), xa[m] = read_x(st0, 0, m);
+            for (int s = 0; s < steps; s += 2) {
+                step(st0, st1, s, behind_stores && s == 0);
+                step(st1, st0, s + 1, false);
             }
 
             const int l = opaque(lane), c16 = l & 15;
@@ -360,7 +370,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
             }
             // every stage has been read: the next tile's copies start before this one's outputs are stored
             lds_barrier();
-            if (k < mine) begin(g, rows);
+            if (k < mine) begin(g);
             auto value = [&](const int n, const int m, const float rs, float* y) __attribute__((always_inline)) {
                 if constexpr (FMT == GF_I8) {
                     y[0] = (float(acc[n][m][0]) * sw[n].x) * rs;
@@ -415,21 +425,16 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
             }
             if (k == mine) break;
         } else {                                                // a wave below the last row only copies
-            for (int s = 0; s < 4 * turns; ++s) {
-                if (s < 3 && behind_stores) stage_barrier<2 * FILL + STORES>();
-                else if (s + 3 < steps) stage_barrier<2 * FILL>();
-                else if (s + 2 < steps) stage_barrier<FILL>();
+            for (int s = 0; s < 2 * turns; ++s) {
+                if (s == 0 && behind_stores) stage_barrier<STORES>();
                 else stage_barrier<0>();
-                const int at = s & 3;
-                if (ragged && s + 2 == steps) clear_tail(at == 0 ? st1 : at == 1 ? st2 : at == 2 ? st3 : st0);
-                if (at == 0) supply(st0, s + 4);
-                else if (at == 1) supply(st1, s + 4);
-                else if (at == 2) supply(st2, s + 4);
-                else supply(st3, s + 4);
+                if (ragged && s + 2 == steps) clear_tail(s & 1 ? st0 : st1);
+                if (s & 1) supply(st1, s + 2);
+                else supply(st0, s + 2);
             }
             lds_barrier();
             if (k == mine) break;
-            begin(g, rows);
+            begin(g);
             __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);       // no stores behind its copies: they have to land
         }
     }
