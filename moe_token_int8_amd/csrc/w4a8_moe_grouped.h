@@ -91,19 +91,20 @@ __device__ __forceinline__ uint32_t f32_to_f16_pair(float lo, float hi) {
     return f32_to_f16_rne(lo) | (f32_to_f16_rne(hi) << 16);
 }
 
-// Four neighbouring outputs of one row.  `n` (1..4) of them exist; whole quads go out in one store where the row
-// pitch keeps them aligned (`wide`, uniform over the launch).
-__device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t at, const int n, const bool wide,
-                                              const float y0, const float y1, const float y2, const float y3) {
-    const float y[4] = {y0, y1, y2, y3};
+// Four neighbouring outputs of one row, of which n (1..4) exist.  A whole quad goes out in one store wherever it starts:
+// global memory takes wide stores at any element's address.
+__device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t at, const int n, const float y0,
+                                              const float y1, const float y2, const float y3) {
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
     if (a.out == W4A8_F32) {
         float* p = static_cast<float*>(a.Y) + at;
-        if (n == 4 && wide) {
-            *reinterpret_cast<float4*>(p) = make_float4(y0, y1, y2, y3);
+        if (n == 4) {
+            *reinterpret_cast<f4*>(p) = f4{y0, y1, y2, y3};
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) p[i] = y[i];
+            p[0] = y0;
+            if (n > 1) p[1] = y1;
+            if (n > 2) p[2] = y2;
         }
         return;
     }
@@ -111,20 +112,13 @@ __device__ __forceinline__ void grouped_store(const GroupedArgs& a, const size_t
     const uint32_t lo = f16 ? f32_to_f16_pair(y0, y1) : f32_to_bf16_pair(y0, y1);
     const uint32_t hi = f16 ? f32_to_f16_pair(y2, y3) : f32_to_bf16_pair(y2, y3);
     uint16_t* p = static_cast<uint16_t*>(a.Y) + at;
-    if (n == 4 && wide) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    if (n == 4) {
+        *reinterpret_cast<u2*>(p) = u2{lo, hi};
     } else {
         p[0] = uint16_t(lo);
         if (n > 1) p[1] = uint16_t(lo >> 16);
         if (n > 2) p[2] = uint16_t(hi);
-        if (n > 3) p[3] = uint16_t(hi >> 16);
     }
-}
-
-// Whether every quad of a row starts on a multiple of its size: 4 columns of 2 or 4 bytes.
-__device__ __forceinline__ bool grouped_wide(const GroupedArgs& a) {
-    const uintptr_t mask = a.out == W4A8_F32 ? 15u : 7u;
-    return a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.Y) & mask) == 0;
 }
 
 // Source row of routed row r, or -1 (a gather entry that names no row of X: its output is zero).

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -86,7 +87,6 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, c16 = lane & 15;
     const int units = (a.kb + 127) / 128;
-    const bool wide = grouped_wide(a);
     for (unsigned item = blockIdx.x;; item += gridDim.x) {
         const int slot = int(item / unsigned(ncb)), cb = int(item - unsigned(slot) * unsigned(ncb));
         const TileRows tr = grouped_find<16 * MS>(a, slot, lane);
@@ -254,9 +254,8 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] = osrc[i] < 0 ? 0.0f : s[k];
             }
-            grouped_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), wide, y[0], y[1], y[2], y[3]);
+            grouped_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), y[0], y[1], y[2], y[3]);
         }
-
         if constexpr (MS == 1) return;                          // one tile a workgroup
         lds_barrier();                                          // the planes are written again by the next tile
     }
@@ -276,17 +275,40 @@ static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s
     moe_grouped_stream_kernel<FMT, PAIR, MS, D, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
+// Whether one launch of 64-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
+// estimates, in us, use what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates
+// measured on this chip: a compute unit takes a 64 x 64 streaming tile in 3 us and 32 bytes of operands a nanosecond,
+// with all of them 4.5 TB/s of weights, and a 256 x 256 tile in 9 us and 1.5 us for 128 bytes of K; the streaming classes
+// read 6 TB/s; 4 launches that find little cost 35 us, 2 cost 25.  Examples (one launch / by class): 853 tokens x 2 of 41
+// experts, K = 264, I = 1356: 55 / 74 us; 254 x 6 of 12, K = 2048, N = 287: 16 / 53; 3782 x 4 of 64, K = 568, I = 799: 245 / 91;
+// 64 x 8 of 256, K = 7168, N = 4096 in 8 bits: 1365 / 960.
+static bool one_launch(const GroupedArgs& a, bool pair) {
+    const double rows = a.rows, E = a.E, avg = rows / E, kb = a.kb, width = pair ? 2.0 * a.N : a.N;
+    const double experts = std::min(E, rows);
+    auto rounds = [](double tiles) { return std::ceil(tiles / 256); };
+    const double weights = experts * width * kb;
+    const double items = (std::floor(rows / 64) + experts) * std::ceil(width / 64);
+    const double one = 6 + std::max(rounds(items) * (3 + (64 + std::min(64.0, avg)) * kb / 32e3), weights / 4.5e6);
+    const double tiles = (std::floor(rows / 256) + std::min(E, std::floor(rows / 65))) * std::ceil(width / 256);
+    const double split = (avg >= 128 ? 25 : 35) + rounds(tiles) * (9 + kb / 85) * std::min(1.0, avg / 32) + weights / 6e6;
+    return one < split;
+}
+
 // Row classes of the streaming kernel, one launch each: an expert of up to 16 rows costs nothing for rows it does not
 // have, and the launches of classes that no expert can be in are left out.  `slots` bounds the row tiles of the class.
-// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles, since each
-// launch that finds nothing costs 5 us (8192-token prompts: GS_PROMPT us).
+// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles.
 template <int FMT, bool PAIR>
 static void launch_grouped(GroupedArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     constexpr long long REACH = 0xe0000000ll;
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
-    const bool few_small = near && rows >= 128 * E;
+    if (rows > 16 && (!near || one_launch(a, PAIR))) {
+        a.lo = 1, a.hi = 0x7fffffff;
+        launch_stream_t<FMT, PAIR, 4, 2, false>(a, rows / 64 + std::min(E, rows), s);
+        return;
+    }
+    const bool few_small = rows >= 128 * E;
     if (!few_small) {
         a.lo = 1, a.hi = 17;
         if constexpr (FMT == GF_I8) {
@@ -303,10 +325,10 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
         }
     }
     if (rows > 32) {
-        a.lo = few_small ? 1 : 33, a.hi = near ? 65 : 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 2, false>(a, near ? std::min(E, rows / a.lo) : rows / 64 + std::min(E, rows / 33), s);
+        a.lo = few_small ? 1 : 33, a.hi = 65;
+        launch_stream_t<FMT, PAIR, 4, 2, false>(a, std::min(E, rows / a.lo), s);
     }
-    if (rows > 64 && near) {
+    if (rows > 64) {
         a.lo = 65, a.hi = 0x7fffffff;
         launch_grouped_tile(a, FMT, PAIR, s);
     }

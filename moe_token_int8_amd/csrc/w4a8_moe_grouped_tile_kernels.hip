@@ -89,7 +89,6 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     const int q = lane >> 4, c16 = lane & 15;
     const int ncb = (a.N + COLS - 1) / COLS;
     const int steps = (a.kb + GT_STEP - 1) / GT_STEP;
-    const bool wide = grouped_wide(a);
     const bool f32 = !PAIR && a.out == W4A8_F32;
 
     // row tiles of every expert of this launch, as a prefix sum (two experts a thread)
@@ -267,13 +266,12 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         return *(const LDS v4i*)(st + xat[h] + m * 2048);
     };
 
-    // With whole aligned 16-byte stores and row offsets that fit 32 bits, every wave that computed ends a tile with at least
+    // A tile whose columns come in whole 16-byte stores (of any address) ends, in every wave that computed, with at least
     // STORES of them, which the next tile's first barriers leave in flight.
     constexpr int STORES = PAIR ? 8 : 16;
+    const bool near_rows = a.ldy < (size_t(1) << 21);           // 32-bit offsets within a tile
     const int quantum = f32 ? 3 : 7;
-    const bool regular = (a.N & quantum) == 0 && (a.ldy & quantum) == 0 && a.ldy < (size_t(1) << 21) &&
-                         (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0;
-    const bool behind_stores = regular && steps >= 2;
+    bool behind_stores = false;
 
     look_up(0);
     int4 g = list[0];
@@ -285,7 +283,6 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     request_rows(g);
     stage_barrier<0>();
     begin(g);
-    __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);               // vmcnt 0: no stores stand behind the first copies
     for (int k = 0;;) {
         const int4 cur = g;
         const int buf = k & 1;
@@ -385,7 +382,8 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
                     }
                 }
             };
-            // stores of 16 bytes exist whole or not at all: one each, dropped by the descriptor where they do not
+            // stores of 16 bytes that exist whole or not at all: one each, dropped by the descriptor where they do not
+            const bool regular = near_rows && ((a.N & quantum) == 0 || (cur.w + 1) * COLS <= a.N);
             const unsigned es = f32 ? 4u : 2u, pitch = unsigned(a.ldy) * es;
             const __amdgpu_buffer_rsrc_t yr = buffer_of(static_cast<const uint8_t*>(a.Y) + size_t(cur.y) * a.ldy * es,
                                                         size_t(cur.z - 1) * pitch + size_t(a.N) * es);
@@ -403,8 +401,8 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         if (row < cur.z && col[n] < a.N)
-                            grouped_store(a, size_t(cur.y + row) * a.ldy + col[n], min(4, a.N - col[n]), wide, y[n][0], y[n][1],
-                                          y[n][2], y[n][3]);
+                            grouped_store(a, size_t(cur.y + row) * a.ldy + col[n], min(4, a.N - col[n]), y[n][0], y[n][1], y[n][2],
+                                          y[n][3]);
                 } else if (f32) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -424,6 +422,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
                 }
             }
             if (k == mine) break;
+            behind_stores = regular && steps >= 2;
         } else {                                                // a wave below the last row only copies
             for (int s = 0; s < 2 * turns; ++s) {
                 if (s == 0 && behind_stores) stage_barrier<STORES>();
@@ -435,7 +434,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
             lds_barrier();
             if (k == mine) break;
             begin(g);
-            __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);       // no stores behind its copies: they have to land
+            behind_stores = false;                              // no stores behind its copies
         }
     }
 }
