@@ -29,14 +29,31 @@ namespace w4a8 {
 constexpr int GS_WAVES = 8;
 constexpr int GS_CT = 4;                                        // column tiles of a workgroup
 
-// Byte within a 128-byte unit of the 16 bytes that lane group q takes in load h.  The order of k within a unit is free as
-// long as both operands have the same; it is chosen so that one load of the weights covers whole pieces of memory.
-// Row-major: 64 contiguous bytes of each row.  Packed codes (byte 64 h' + 16 q' of column c at (16 q' + c) * 32 + 16 h'):
-// the q' = 2 h, 2 h + 1 quarters with both their halves, a contiguous KiB.  (With 16 of every 32 bytes in a load, the
-// 256-expert steps read GS_OLD TB/s instead of GS_NEW.)
+// Loads of the weights.  A load of a wave is 64 pieces of 16 bytes, and an MFMA wants one of each of 16 columns at 4 places
+// along K; which places is free, as long as the activations have the same.  The loads are arranged to cover whole pieces of
+// memory (with 16 of every 32 bytes in a load, the 256-expert steps read 3.7 TB/s instead of 6.6):
+//  - packed codes (byte 64 h' + 16 q' of column c at (16 q' + c) * 32 + 16 h'): load h takes the quarters q' = 2 h, 2 h + 1
+//    with both their halves, a contiguous KiB;
+//  - row-major weights: load h takes the whole 128-byte lines of columns 8 h .. 8 h + 7, lane (q, i) the chunk 2 q + i / 8 of
+//    column 8 h + i % 8.  Exchanging 8 lanes of the two loads in every 16 (pair_up) then gives chunk 2 q of all 16 columns in
+//    one register set and chunk 2 q + 1 in the other.  (Loads of 64 bytes of 16 rows read 5.6 TB/s: they cannot carry
+//    the non-temporal hint, which lets the other half of each line go before it is asked for.)
+// unit_byte: the byte of a unit that lane group q then multiplies with in step h.
 template <int FMT>
 __device__ __forceinline__ unsigned unit_byte(int q, int h) {
-    return FMT == GF_I8 ? unsigned(64 * (q & 1) + 32 * h + 16 * (q >> 1)) : unsigned(64 * h + 16 * q);
+    return FMT == GF_I8 ? unsigned(64 * (q & 1) + 32 * h + 16 * (q >> 1)) : unsigned(32 * q + 16 * h);
+}
+
+template <int FMT>
+__device__ __forceinline__ void pair_up(v4i& a, v4i& b) {
+    if constexpr (FMT != GF_I8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int x = a[k], y = b[k];                       // row_ror:8 into the upper, into the lower 8 of every 16 lanes
+            a[k] = __builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);
+            b[k] = __builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);
+        }
+    }
 }
 
 // The slot-th tile of MT rows over the experts served by this launch, in expert order; every wave finds it alone.  expert is
@@ -98,7 +115,7 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
         // gate and one for the up rows); offsets past it load zeros
         const uint8_t* wexp = a.W + size_t(expert) * a.expert_stride;
         __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1];
-        unsigned woff[CT];                                      // of this lane in each tile
+        unsigned woff[CT][FMT == GF_I8 ? 1 : 2];                // of this lane in each tile (and load)
         constexpr unsigned NONE = 0x7ffffff0u;
         if constexpr (FMT == GF_I8) {
             const int tile0 = cb * CT, ntiles = (a.N + 15) / 16;
@@ -107,7 +124,7 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
                                                       int(unsigned(min(CT, ntiles - tile0)) * tile_bytes), 0x00020000);
 #pragma unroll
             for (int t = 0; t < CT; ++t)
-                woff[t] = tile0 + t < ntiles ? t * tile_bytes + unsigned((q >> 1) * 16 + c16) * 32u + (q & 1) * 16u : NONE;
+                woff[t][0] = tile0 + t < ntiles ? t * tile_bytes + unsigned((q >> 1) * 16 + c16) * 32u + (q & 1) * 16u : NONE;
         } else {
             const int n0 = cb * COLS, nvalid = min(COLS, a.N - n0);
             const unsigned extent = unsigned(nvalid - 1) * a.ldw + unsigned(a.kb);
@@ -116,24 +133,28 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
                 wr[p] = __builtin_amdgcn_make_buffer_rsrc(
                     const_cast<uint8_t*>(wexp + (size_t(n0) + (p ? size_t(a.N) : 0)) * a.ldw), 0, int(extent), 0x00020000);
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const int col = (PAIR ? t & 1 : t) * 16 + c16;
-                woff[t] = col < nvalid ? unsigned(col) * a.ldw : NONE;
-            }
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = (PAIR ? t & 1 : t) * 16 + 8 * h + (c16 & 7);
+                    woff[t][h] = col < nvalid ? unsigned(col) * a.ldw : NONE;
+                }
         }
         const uint8_t* xrow[MS];
         v4i wv[D][CT][2], xv[D][MS][2];
-        // Both loads of a weight tile stand next to each other: they share its 128-byte lines.  The non-temporal hint (NT) is
-        // for calls that read more weights than the Infinity Cache holds, and for packed codes only: a load of row-major
-        // weights takes half a line of each row, and the hint lets the other half go before it is asked for.
+        // NT: the non-temporal hint, for calls that read more weights than the Infinity Cache holds.
         auto load_w = [&](const int d, const int u) __attribute__((always_inline)) {
 #pragma unroll
             for (int t = 0; t < CT; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const unsigned b = unsigned(u) * 128u + unit_byte<FMT>(q, h);
-                    const bool in = b < unsigned(a.kb) && woff[t] != NONE;
-                    const unsigned off = in ? woff[t] + (FMT == GF_I8 ? unsigned(u) * 2048u + 1024u * h : b) : NONE;
+                    unsigned off = NONE;
+                    if constexpr (FMT == GF_I8) {
+                        if (u < units && woff[t][0] != NONE) off = woff[t][0] + unsigned(u) * 2048u + 1024u * h;
+                    } else {
+                        const unsigned b = unsigned(u) * 128u + unsigned(2 * q + (c16 >> 3)) * 16u;
+                        if (b < unsigned(a.kb) && woff[t][h] != NONE) off = woff[t][h] + b;
+                    }
                     wv[d][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wr[PAIR ? t >> 1 : 0], off, 0, NT ? 2 : 0);
                 }
         };
@@ -169,6 +190,8 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 const int ud = u + d * GS_WAVES;
+#pragma unroll
+                for (int t = 0; t < CT; ++t) pair_up<FMT>(wv[d][t][0], wv[d][t][1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // 16-bit values past the end of K: the weights are zero, and the activations have to be, since
@@ -311,14 +334,11 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
     const bool few_small = rows >= 128 * E;
     if (!few_small) {
         a.lo = 1, a.hi = 17;
-        if constexpr (FMT == GF_I8) {
-            // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one:
-            // 6.4 GB of them 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
-            if (std::min(E, rows) * (long long)a.N * a.kb > (256ll << 20)) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
-            else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
-        } else {
-            launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
-        }
+        // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one: 6.4 GB
+        // of codes 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
+        const bool nt = std::min(E, rows) * (long long)a.N * (PAIR ? 2 : 1) * a.kb > (256ll << 20);
+        if (nt) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
+        else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
         if (rows > 16) {
             a.lo = 17, a.hi = 33;
             launch_stream_t<FMT, PAIR, 2, 2, false>(a, std::min(E, rows / 17), s);
