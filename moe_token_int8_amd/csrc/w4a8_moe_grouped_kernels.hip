@@ -20,14 +20,14 @@ namespace w4a8 {
 
 // Streaming kernel: experts with few rows, bound by the read of their weights.
 //
-// A workgroup of 8 waves owns one tile of up to 16 * MS routed rows of one expert and 64 weight columns (4 MFMA tiles; the
-// paired form: 32 gate columns and the matching 32 up columns) over all of K.  The waves share K: wave w takes the
+// A workgroup of 8 waves owns one tile of up to 16 * MS routed rows of one expert and CT MFMA tiles of 16 weight columns (the
+// paired form: gate columns in half of them, the matching up columns in the others) over all of K.  The waves share K: wave w takes the
 // 128-byte units w, w + 8, w + 16, ... of every row, so that at any time the workgroup reads 1 KiB runs of each weight
 // row (16 KiB runs of a packed tile), and no operand is used by two waves: weights and activations go from memory to
-// registers in the layout of the MFMA operands, with no LDS and no barrier in the loop.  D units of 8 + 2 MS loads are in
-// flight per wave.  At the end the 8 partial sums are added in wave order through LDS (int32 sums exactly).
+// registers in the layout of the MFMA operands, with no LDS and no barrier in the loop.  One unit
+// of 2 CT + 2 MS loads is in flight per wave; the loads of the other waves cover its wait (two units a wave take the
+// registers of half of them: 64-token 256-expert 16-bit down product 1.05 against 1.01 ms).  At the end the 8 partial sums are added in wave order through LDS (int32 sums exactly).
 constexpr int GS_WAVES = 8;
-constexpr int GS_CT = 4;                                        // column tiles of a workgroup
 
 // Loads of the weights.  A load of a wave is 64 pieces of 16 bytes, and an MFMA wants one of each of 16 columns at 4 places
 // along K; which places is free, as long as the activations have the same.  The loads are arranged to cover whole pieces of
@@ -96,10 +96,10 @@ __device__ __forceinline__ TileRows grouped_find(const GroupedArgs& a, int slot,
     return tr;
 }
 
-template <int FMT, bool PAIR, int MS, int D, bool NT>
+template <int FMT, bool PAIR, int MS, int CT, bool NT>
 __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kernel(GroupedArgs a, int ncb) {
     using acc_t = typename GroupedAcc<FMT>::type;
-    constexpr int CT = GS_CT, COLS = PAIR ? 32 : 64;
+    constexpr int COLS = PAIR ? CT * 8 : CT * 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, c16 = lane & 15;
@@ -136,14 +136,14 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
             for (int t = 0; t < CT; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int col = (PAIR ? t & 1 : t) * 16 + 8 * h + (c16 & 7);
+                    const int col = (PAIR ? t % (CT / 2) : t) * 16 + 8 * h + (c16 & 7);
                     woff[t][h] = col < nvalid ? unsigned(col) * a.ldw : NONE;
                 }
         }
         const uint8_t* xrow[MS];
-        v4i wv[D][CT][2], xv[D][MS][2];
+        v4i wv[CT][2], xv[MS][2];
         // NT: the non-temporal hint, for calls that read more weights than the Infinity Cache holds.
-        auto load_w = [&](const int d, const int u) __attribute__((always_inline)) {
+        auto load_w = [&](const int u) __attribute__((always_inline)) {
 #pragma unroll
             for (int t = 0; t < CT; ++t)
 #pragma unroll
@@ -155,16 +155,16 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
                         const unsigned b = unsigned(u) * 128u + unsigned(2 * q + (c16 >> 3)) * 16u;
                         if (b < unsigned(a.kb) && woff[t][h] != NONE) off = woff[t][h] + b;
                     }
-                    wv[d][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wr[PAIR ? t >> 1 : 0], off, 0, NT ? 2 : 0);
+                    wv[t][h] = __builtin_amdgcn_raw_buffer_load_b128(wr[PAIR ? t / (CT / 2) : 0], off, 0, NT ? 2 : 0);
                 }
         };
-        auto load_x = [&](const int d, const int u) __attribute__((always_inline)) {
+        auto load_x = [&](const int u) __attribute__((always_inline)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const unsigned b = unsigned(u) * 128u + unit_byte<FMT>(q, h);
 #pragma unroll
                 for (int ms = 0; ms < MS; ++ms)
-                    xv[d][ms][h] = *reinterpret_cast<const v4i*>(xrow[ms] + (b < unsigned(a.kb) ? b : 0u));
+                    xv[ms][h] = *reinterpret_cast<const v4i*>(xrow[ms] + (b < unsigned(a.kb) ? b : 0u));
             }
         };
         // activation rows of this lane; rows past the tile repeat its first row (their sums are not stored)
@@ -174,40 +174,34 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
             const int row = ms * 16 + c16;
             src[ms] = grouped_src(a, rbeg + (row < nrows ? row : 0));
         }
-#pragma unroll
-        for (int d = 0; d < D; ++d) load_w(d, wave + d * GS_WAVES);
+        load_w(wave);
 #pragma unroll
         for (int ms = 0; ms < MS; ++ms) xrow[ms] = a.X + size_t(src[ms] < 0 ? 0 : src[ms]) * size_t(a.ldx);
-#pragma unroll
-        for (int d = 0; d < D; ++d) load_x(d, wave + d * GS_WAVES);
+        load_x(wave);
 
         acc_t acc[CT][MS];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
 #pragma unroll
             for (int ms = 0; ms < MS; ++ms) acc[t][ms] = acc_t{};
-        for (int u = wave; u < units; u += D * GS_WAVES) {
+        for (int u = wave; u < units; u += GS_WAVES) {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int ud = u + d * GS_WAVES;
+            for (int t = 0; t < CT; ++t) pair_up<FMT>(wv[t][0], wv[t][1]);
 #pragma unroll
-                for (int t = 0; t < CT; ++t) pair_up<FMT>(wv[d][t][0], wv[d][t][1]);
+            for (int h = 0; h < 2; ++h) {
+                // 16-bit values past the end of K: the weights are zero, and the activations have to be, since the bytes
+                // loaded in their place may hold an infinity or a NaN
+                const bool in = FMT == GF_I8 || unsigned(u) * 128u + unit_byte<FMT>(q, h) < unsigned(a.kb);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // 16-bit values past the end of K: the weights are zero, and the activations have to be, since
-                    // the bytes loaded in their place may hold an infinity or a NaN
-                    const bool in = FMT == GF_I8 || unsigned(ud) * 128u + unit_byte<FMT>(q, h) < unsigned(a.kb);
+                for (int ms = 0; ms < MS; ++ms) {
+                    v4i x = xv[ms][h];
+                    if constexpr (FMT != GF_I8) x = in ? x : v4i{0, 0, 0, 0};
 #pragma unroll
-                    for (int ms = 0; ms < MS; ++ms) {
-                        v4i x = xv[d][ms][h];
-                        if constexpr (FMT != GF_I8) x = in ? x : v4i{0, 0, 0, 0};
-#pragma unroll
-                        for (int t = 0; t < CT; ++t) acc[t][ms] = grouped_mfma<FMT>(wv[d][t][h], x, acc[t][ms]);
-                    }
+                    for (int t = 0; t < CT; ++t) acc[t][ms] = grouped_mfma<FMT>(wv[t][h], x, acc[t][ms]);
                 }
-                load_w(d, ud + D * GS_WAVES);
-                load_x(d, ud + D * GS_WAVES);
             }
+            load_w(u + GS_WAVES);
+            load_x(u + GS_WAVES);
         }
 
         // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
@@ -289,13 +283,14 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
 // 29 and 16 us with a workgroup for each possible tile).
 constexpr long long GS_GRID = 512;
 
-template <int FMT, bool PAIR, int MS, int D, bool NT>
+template <int FMT, bool PAIR, int MS, int CT, bool NT>
 static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s) {
-    constexpr size_t lds = size_t(MS == 4 ? 4 : GS_WAVES) * GS_CT * MS * 64 * 16;
+    constexpr size_t lds = size_t(MS == 4 ? 4 : GS_WAVES) * CT * MS * 64 * 16;
     static_assert(lds <= 65536, "two workgroups of 16-row tiles share a compute unit");
-    const int ncb = (a.N + (PAIR ? 31 : 63)) / (PAIR ? 32 : 64);
+    constexpr int cols = PAIR ? CT * 8 : CT * 16;
+    const int ncb = (a.N + cols - 1) / cols;
     const long long blocks = MS == 1 ? slots * ncb : std::min(slots * ncb, GS_GRID);
-    moe_grouped_stream_kernel<FMT, PAIR, MS, D, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
+    moe_grouped_stream_kernel<FMT, PAIR, MS, CT, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
 // Whether one launch of 64-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
@@ -328,7 +323,7 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
     if (rows > 16 && (!near || one_launch(a, PAIR))) {
         a.lo = 1, a.hi = 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 2, false>(a, rows / 64 + std::min(E, rows), s);
+        launch_stream_t<FMT, PAIR, 4, 4, false>(a, rows / 64 + std::min(E, rows), s);
         return;
     }
     const bool few_small = rows >= 128 * E;
@@ -337,16 +332,25 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
         // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one: 6.4 GB
         // of codes 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
         const bool nt = std::min(E, rows) * (long long)a.N * (PAIR ? 2 : 1) * a.kb > (256ll << 20);
-        if (nt) launch_stream_t<FMT, PAIR, 1, 2, true>(a, std::min(E, rows), s);
-        else launch_stream_t<FMT, PAIR, 1, 2, false>(a, std::min(E, rows), s);
+        // column tiles of a workgroup: 4, or 2 where there are few workgroups to spread over the chip (a single token's 69 MB:
+        // 17.5 -> 15.4 us; 64-token steps of 256 experts lose 4 %) and in the paired form (33 tokens: 240 -> 225 us)
+        const long long slots = std::min(E, rows), blocks = slots * ((a.N + 63) / 64);
+        if constexpr (PAIR) {
+            if (nt) launch_stream_t<FMT, PAIR, 1, 2, true>(a, slots, s);
+            else launch_stream_t<FMT, PAIR, 1, 2, false>(a, slots, s);
+        } else {
+            if (nt) launch_stream_t<FMT, PAIR, 1, 4, true>(a, slots, s);
+            else if (blocks < 1024) launch_stream_t<FMT, PAIR, 1, 2, false>(a, slots, s);
+            else launch_stream_t<FMT, PAIR, 1, 4, false>(a, slots, s);
+        }
         if (rows > 16) {
             a.lo = 17, a.hi = 33;
-            launch_stream_t<FMT, PAIR, 2, 2, false>(a, std::min(E, rows / 17), s);
+            launch_stream_t<FMT, PAIR, 2, 4, false>(a, std::min(E, rows / 17), s);
         }
     }
     if (rows > 32) {
         a.lo = few_small ? 1 : 33, a.hi = 65;
-        launch_stream_t<FMT, PAIR, 4, 2, false>(a, std::min(E, rows / a.lo), s);
+        launch_stream_t<FMT, PAIR, 4, 4, false>(a, std::min(E, rows / a.lo), s);
     }
     if (rows > 64) {
         a.lo = 65, a.hi = 0x7fffffff;
