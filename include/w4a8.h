@@ -473,16 +473,16 @@ typedef struct {
  *             aligned to its element
  *   bias      device float32 [E] or NULL: an offset used for the choice only, not for the weights
  *   topk_ids  device int32 [T, k], best first; topk_w device float32 [T, k]
- * Experts are ranked by their logit, or by p_i + bias_i in float64 if a bias is given; a group by
- * its best expert, or with a bias by the sum of its two best.  Equal ranks go to the lower index.
- * An expert whose logit (or bias) is -Inf is masked: never chosen; a -Inf logit also has p_i = 0.
- * Where fewer than k
- * can be chosen, the remaining entries are id -1 with weight 0, which w4a8_moe_align leaves out and
- * w4a8_moe_combine skips (a padded token: all logits -Inf).  A row with a NaN logit or rank, or
+ * Experts are ranked by their logit, or by p_i + bias_i in float64 if a bias is given, of which 42
+ * bits of the mantissa count; a group by its best expert, or with a bias by the sum of its two best.
+ * Equal ranks go to the lower index.  An expert whose logit (or bias) is -Inf is masked: never chosen;
+ * a -Inf logit also has p_i = 0.  Where fewer than k can be chosen, the remaining entries are id -1
+ * with weight 0, which w4a8_moe_align leaves out and w4a8_moe_combine skips (a padded token: all
+ * logits -Inf).  A row with a NaN logit or rank, or
  * with a +Inf logit under softmax, has no order: it gets the ids 0..k-1 with NaN weights.
- * Softmax and sigmoid are computed in float64 if a bias is given and in float32 otherwise.
+ * Scores are computed in float64, without a bias the denominator of the softmax in float32.
  * T == 0 is a no-op.  EINVAL: E, k or score out of range, n_group not dividing E, topk_group
- * outside 1..n_group or leaving fewer than k experts, ldl < E, NULL or misaligned pointers;
+ * outside 1..n_group or leaving fewer than k experts, ldl < E, scale not finite, NULL or misaligned pointers;
  * EUNSUPPORTED: E > 1024, k > 64, T > 2^24. */
 int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, const float* bias,
                    const w4a8_route_desc* d, int32_t* topk_ids, float* topk_w, void* stream);
@@ -493,7 +493,7 @@ int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, const float* b
  * the sum exact in int32, then float32, then rounded to nearest even for bfloat16.
  *   d   weight_bits = 8, group_size = K, float32 scales, K < 133144; other formats EUNSUPPORTED
  * Rows at or past expert_offsets[E] are not written.  Other arguments, bounds and errors as
- * w4a8_moe_gemm; additionally EUNSUPPORTED for N > 2^20 or rows > 2^24. */
+ * w4a8_moe_gemm; additionally E <= 1024 (EINVAL) and EUNSUPPORTED for N > 2^20 or rows > 2^24. */
 int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather, int k,
                        const int32_t* expert_offsets, int E, int rows, int src_rows,
                        const void* blobs_dev, size_t expert_stride, const w4a8_wdesc* d, void* Y,
@@ -509,7 +509,8 @@ int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather,
  *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm
  * K, ldx, ldw and expert_stride are multiples of 8, X and W 16-byte aligned (EINVAL); any N.  Rows
  * at or past expert_offsets[E] are not written, nor is Y past column N.  A gather entry that
- * names no row of X gives a row of zeros.  EUNSUPPORTED: N > 2^20, ldw > 2^23, rows > 2^24. */
+ * names no row of X gives a row of zeros.  E <= 1024 (EINVAL).  EUNSUPPORTED: N > 2^20, ldw > 2^23,
+ * rows > 2^24. */
 int w4a8_moe_gemm_w16a16(const void* X, int dtype, int ldx, const int32_t* gather, int k,
                          const int32_t* expert_offsets, int E, int rows, int src_rows, const void* W,
                          size_t expert_stride, int ldw, int K, int N, void* Y, int ldy, int out_dtype,
@@ -517,7 +518,8 @@ int w4a8_moe_gemm_w16a16(const void* X, int dtype, int ldx, const int32_t* gathe
 
 /* Expert-grouped unquantized gate/up GEMM with the gated activation in its epilogue (P1 section 1):
  *   H[r, c] = silu(g) u,  g = sum_k X[src, k] W[e, c, k],  u = sum_k X[src, k] W[e, I + c, k],
- * formed from the float32 sums and rounded once, so no [rows, 2I] intermediate is stored.
+ * formed from the float32 sums and rounded once, so no [rows, 2I] intermediate is stored.  For g < 0
+ * silu(g) is g exp(g) / (1 + exp(g)), where exp(g) may count as 0 below 2^-126.
  *   W   device [E, 2I, K]: the I gate rows, then the I up rows; any I
  *   H   device [rows, I], row stride ldh, of type dtype
  * Other arguments and errors as w4a8_moe_gemm_w16a16. */
@@ -525,6 +527,35 @@ int w4a8_moe_gemm_silu_w16a16(const void* X, int dtype, int ldx, const int32_t* 
                               const int32_t* expert_offsets, int E, int rows, int src_rows,
                               const void* W, size_t expert_stride, int ldw, int K, int I, void* H,
                               int ldh, void* stream);
+
+/* One MoE expert layer on 8-bit per-channel experts: the steps of w4a8_moe_forward with
+ * w4a8_moe_gemm_w8a8 for both products.
+ *   gu_desc, d_desc  as w4a8_moe_gemm_w8a8 (K = H, N = 2I; K = I, N = H)
+ *   workspace        device, >= w4a8_moe_workspace_size(T, k, H, I, E) bytes, 256-aligned
+ * Ids outside [0, E) (w4a8_moe_route gives -1 for padded tokens) add nothing to their token.  H <= 65536
+ * and I <= 16384 (EUNSUPPORTED).  Other arguments, limits and errors as w4a8_moe_forward. */
+int w4a8_moe_forward_w8a8(const void* X_bf16, const int32_t* topk_ids, const float* topk_w, int T,
+                          int k, int E, const void* gu_blobs, size_t gu_stride,
+                          const w4a8_wdesc* gu_desc, const void* d_blobs, size_t d_stride,
+                          const w4a8_wdesc* d_desc, void* workspace, size_t workspace_bytes,
+                          void* out_bf16, void* stream);
+
+/* Workspace bytes needed by w4a8_moe_forward_w16a16 (0 if invalid). */
+size_t w4a8_moe_w16a16_workspace_size(int T, int k, int H, int I, int E);
+
+/* One MoE expert layer on unquantized bfloat16 experts: w4a8_moe_align ->
+ * w4a8_moe_gemm_silu_w16a16 (gate/up, gathered) -> w4a8_moe_gemm_w16a16 (down) -> w4a8_moe_combine.
+ *   X_bf16     device bfloat16 [T, H]
+ *   Wgu        device bfloat16 [E, 2I, H], gate rows first; Wd [E, H, I]; rows dense, expert strides
+ *              gu_stride and d_stride in elements
+ *   workspace  device, >= w4a8_moe_w16a16_workspace_size(T, k, H, I, E) bytes, 256-aligned
+ *   out        device bfloat16 [T, H]
+ * H and I multiples of 8, all pointers 16-byte aligned (EINVAL); T*k <= 2^24 (EUNSUPPORTED).  Every
+ * check of the chained steps runs before the first launch. */
+int w4a8_moe_forward_w16a16(const void* X_bf16, const int32_t* topk_ids, const float* topk_w, int T,
+                            int k, int E, const void* Wgu, size_t gu_stride, const void* Wd,
+                            size_t d_stride, int H, int I, void* workspace, size_t workspace_bytes,
+                            void* out_bf16, void* stream);
 
 /* Name of the kernel variant w4a8_gemm resolves to for (d, M), or "unsupported"
  * (P4: record target and resolved backend so a silent fallback is visible):

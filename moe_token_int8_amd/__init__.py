@@ -32,6 +32,7 @@ EXPORTED = [
     "w4a8_moe_static_workspace_size", "w4a8_moe_forward_static", "w4a8_moe_forward_sets", "w4a8_moe_forward_noalloc",
     "w4a16_gemm", "w4a16_kernel_name",
     "w4a8_moe_route", "w4a8_moe_gemm_w8a8", "w4a8_moe_gemm_w16a16", "w4a8_moe_gemm_silu_w16a16",
+    "w4a8_moe_forward_w8a8", "w4a8_moe_w16a16_workspace_size", "w4a8_moe_forward_w16a16",
     "w4a8_kernel_name", "w4a8_status_string", "w4a8_version",
 ]
 
@@ -103,6 +104,9 @@ def lib() -> ctypes.CDLL:
             "w4a8_moe_gemm_w8a8": (I, [P, P, P, I, P, I, I, I, P, SZ, DP, P, I, VP]),
             "w4a8_moe_gemm_w16a16": (I, [P, I, I, P, I, P, I, I, I, P, SZ, I, I, I, P, I, I, VP]),
             "w4a8_moe_gemm_silu_w16a16": (I, [P, I, I, P, I, P, I, I, I, P, SZ, I, I, I, P, I, VP]),
+            "w4a8_moe_forward_w8a8": (I, [P, P, P, I, I, I, P, SZ, DP, P, SZ, DP, P, SZ, P, VP]),
+            "w4a8_moe_w16a16_workspace_size": (SZ, [I, I, I, I, I]),
+            "w4a8_moe_forward_w16a16": (I, [P, P, P, I, I, I, P, SZ, P, SZ, I, I, P, SZ, P, VP]),
             "w4a8_kernel_name": (ctypes.c_char_p, [DP, I]),
             "w4a16_gemm": (I, [P, I, I, P, DP, P, I, I, VP]),
             "w4a16_kernel_name": (ctypes.c_char_p, [DP, I]),
@@ -499,6 +503,49 @@ def w4a8_moe_gemm_silu_w16a16(X, gather, k: int, expert_offsets, W, H, stream=No
     if H.dtype != X.dtype:
         raise ValueError("H must have the type of X")
     _check(lib().w4a8_moe_gemm_silu_w16a16(*args, _stream(stream)), "w4a8_moe_gemm_silu_w16a16")
+
+
+def w4a8_moe_w16a16_workspace_size(T: int, k: int, H: int, I: int, E: int) -> int:
+    return int(lib().w4a8_moe_w16a16_workspace_size(T, k, H, I, E))
+
+
+def _check_layer(X, topk_ids, topk_w, workspace, out, *weights) -> None:
+    _require_current((X, workspace, out) + weights, int32=(topk_ids,), float32=(topk_w,))
+    if str(X.dtype) != "torch.bfloat16" or X.dtype != out.dtype or X.shape != out.shape:
+        raise ValueError("X and out must be bfloat16 [T, H]")
+    if topk_ids.shape != topk_w.shape or topk_ids.shape[0] != X.shape[0]:
+        raise ValueError("topk_ids and topk_w must be [T, k]")
+    if not all(t.is_contiguous() for t in (X, topk_ids, topk_w, workspace, out)):
+        raise ValueError("the layer's tensors must be contiguous")
+
+
+def w4a8_moe_forward_w8a8(X, topk_ids, topk_w, E: int, gu_blobs, gu_stride: int, gu_desc: WDesc, d_blobs, d_stride: int,
+                          d_desc: WDesc, workspace, out, stream=None) -> None:
+    """w4a8_moe_forward on 8-bit per-channel experts; workspace of w4a8_moe_workspace_size bytes."""
+    _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
+    if X.shape[1] != gu_desc.K:
+        raise ValueError("X must be [T, K of the gate/up weights]")
+    T, k = topk_ids.shape
+    _check(lib().w4a8_moe_forward_w8a8(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, int(E), _ptr(gu_blobs), int(gu_stride),
+                                       gu_desc, _ptr(d_blobs), int(d_stride), d_desc, _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
+           "w4a8_moe_forward_w8a8")
+
+
+def w4a8_moe_forward_w16a16(X, topk_ids, topk_w, Wgu, Wd, workspace, out, stream=None) -> None:
+    """One MoE layer on unquantized bfloat16 experts: Wgu [E, 2I, H], Wd [E, H, I]; workspace of
+    w4a8_moe_w16a16_workspace_size bytes."""
+    _check_layer(X, topk_ids, topk_w, workspace, out, Wgu, Wd)
+    E, I2, H = Wgu.shape
+    if Wd.shape != (E, H, I2 // 2) or X.shape[1] != H or I2 % 2 or Wgu.dtype != X.dtype or Wd.dtype != X.dtype:
+        raise ValueError("Wgu [E, 2I, H] and Wd [E, H, I] must be bfloat16 and match X")
+    if not Wgu[0].is_contiguous() or not Wd[0].is_contiguous():
+        raise ValueError("each expert's weights must be dense")
+    T, k = topk_ids.shape
+    _check(lib().w4a8_moe_forward_w16a16(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, E, _ptr(Wgu), Wgu.stride(0), _ptr(Wd),
+                                         Wd.stride(0), H, I2 // 2, _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
+           "w4a8_moe_forward_w16a16")
 
 
 # ------------------------------------------------------------------------------ helpers

@@ -20,13 +20,14 @@ namespace w4a8 {
 
 // Streaming kernel: experts with few rows, bound by the read of their weights.
 //
-// A workgroup of 8 waves owns one tile of up to 16 * MS routed rows of one expert and CT MFMA tiles of 16 weight columns (the
-// paired form: gate columns in half of them, the matching up columns in the others) over all of K.  The waves share K: wave w takes the
-// 128-byte units w, w + 8, w + 16, ... of every row, so that at any time the workgroup reads 1 KiB runs of each weight
-// row (16 KiB runs of a packed tile), and no operand is used by two waves: weights and activations go from memory to
-// registers in the layout of the MFMA operands, with no LDS and no barrier in the loop.  One unit
-// of 2 CT + 2 MS loads is in flight per wave; the loads of the other waves cover its wait (two units a wave take the
-// registers of half of them: 64-token 256-expert 16-bit down product 1.05 against 1.01 ms).  At the end the 8 partial sums are added in wave order through LDS (int32 sums exactly).
+// A workgroup of 8 waves owns one tile of up to 16 * MS routed rows of one expert and CT MFMA tiles of 16 weight columns
+// (the paired form: gate columns in half of them, the matching up columns in the others) over all of K.  The waves share K:
+// wave w takes the 128-byte units w, w + 8, w + 16, ... of every row, so that at any time the workgroup reads 1 KiB runs of
+// each weight row (16 KiB runs of a packed tile), and no operand is used by two waves: weights and activations go from
+// memory to registers in the layout of the MFMA operands, with no LDS and no barrier in the loop.  One unit of 2 CT + 2 MS
+// loads is in flight per wave; the loads of the other waves cover its wait (two units a wave take the registers of half of
+// them: 64-token 256-expert 16-bit down product 1.05 against 1.01 ms).  At the end the 8 partial sums are added in wave
+// order through LDS (int32 sums exactly).
 constexpr int GS_WAVES = 8;
 
 // Loads of the weights.  A load of a wave is 64 pieces of 16 bytes, and an MFMA wants one of each of 16 columns at 4 places
@@ -297,9 +298,10 @@ static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s
 // estimates, in us, use what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates
 // measured on this chip: a compute unit takes a 64 x 64 streaming tile in 3 us and 32 bytes of operands a nanosecond,
 // with all of them 4.5 TB/s of weights, and a 256 x 256 tile in 9 us and 1.5 us for 128 bytes of K; the streaming classes
-// read 6 TB/s; 4 launches that find little cost 35 us, 2 cost 25.  Examples (one launch / by class): 853 tokens x 2 of 41
-// experts, K = 264, I = 1356: 55 / 74 us; 254 x 6 of 12, K = 2048, N = 287: 16 / 53; 3782 x 4 of 64, K = 568, I = 799: 245 / 91;
-// 64 x 8 of 256, K = 7168, N = 4096 in 8 bits: 1365 / 960.
+// read 6 TB/s; all 4 launches cost 35 us beside that, 2 with many rows 25, those of up to 64 rows 12.  Examples (one launch /
+// by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 51 / 101 us; 205 x 4 of 6, K = 2432, N = 897 in 8 bits: 20 / 42;
+// 2062 x 3 of 8, K = 2104, N = 1410: 171 / 79; 792 x 8 of 50, K = 1928, N = 1952: 276 / 241; 25 x 2 of 138, K = 2160,
+// N = 756: 42 / 29; 64 x 8 of 256, K = 7168, N = 4096 in 8 bits: 1365 / 960.
 static bool one_launch(const GroupedArgs& a, bool pair) {
     const double rows = a.rows, E = a.E, avg = rows / E, kb = a.kb, width = pair ? 2.0 * a.N : a.N;
     const double experts = std::min(E, rows);
@@ -308,23 +310,26 @@ static bool one_launch(const GroupedArgs& a, bool pair) {
     const double items = (std::floor(rows / 64) + experts) * std::ceil(width / 64);
     const double one = 6 + std::max(rounds(items) * (3 + (64 + std::min(64.0, avg)) * kb / 32e3), weights / 4.5e6);
     const double tiles = (std::floor(rows / 256) + std::min(E, std::floor(rows / 65))) * std::ceil(width / 256);
-    const double split = (avg >= 128 ? 25 : 35) + rounds(tiles) * (9 + kb / 85) * std::min(1.0, avg / 32) + weights / 6e6;
+    const double split = (avg >= 128 ? 25 : rows <= 64 ? 12 : 35) + rounds(tiles) * (9 + kb / 85) * std::min(1.0, avg / 32) + weights / 6e6;
     return one < split;
 }
 
 // Row classes of the streaming kernel, one launch each: an expert of up to 16 rows costs nothing for rows it does not
 // have, and the launches of classes that no expert can be in are left out.  `slots` bounds the row tiles of the class.
-// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles.
+// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles.  Returns the
+// kernels' names for the log.
 template <int FMT, bool PAIR>
-static void launch_grouped(GroupedArgs a, hipStream_t s) {
+static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     constexpr long long REACH = 0xe0000000ll;
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
-    if (rows > 16 && (!near || one_launch(a, PAIR))) {
+    // a launch has less than 2^32 work-items; the 16-row class has a workgroup for each of its tiles, of 16 columns or more
+    const bool wide = std::min(E, rows) * (long long)a.N >= (1ll << 27);
+    if (rows > 16 && (!near || wide || one_launch(a, PAIR))) {
         a.lo = 1, a.hi = 0x7fffffff;
         launch_stream_t<FMT, PAIR, 4, 4, false>(a, rows / 64 + std::min(E, rows), s);
-        return;
+        return "moe_grouped_stream_kernel (64-row tiles)";
     }
     const bool few_small = rows >= 128 * E;
     if (!few_small) {
@@ -352,17 +357,17 @@ static void launch_grouped(GroupedArgs a, hipStream_t s) {
         a.lo = few_small ? 1 : 33, a.hi = 65;
         launch_stream_t<FMT, PAIR, 4, 4, false>(a, std::min(E, rows / a.lo), s);
     }
-    if (rows > 64) {
-        a.lo = 65, a.hi = 0x7fffffff;
-        launch_grouped_tile(a, FMT, PAIR, s);
-    }
+    if (rows <= 64) return "moe_grouped_stream_kernel (by rows)";
+    a.lo = 65, a.hi = 0x7fffffff;
+    launch_grouped_tile(a, FMT, PAIR, s);
+    return "moe_grouped_stream_kernel (by rows), moe_grouped_tile_kernel";
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static int launched() { return hipGetLastError() == hipSuccess ? W4A8_OK : W4A8_EHIP; }
 
-// Columns a launch may have: blocks = slots * column blocks stay below 2^31 for 2^24 rows.
+// Columns a launch may have: 16 rows of as many experts make 2^20 workgroups.
 constexpr int GROUPED_MAX_N = 1 << 20;
 constexpr int GROUPED_MAX_ROWS = 1 << 24;
 
@@ -415,9 +420,6 @@ static int run_w8(const int8_t* Xq, const float* sx, const int32_t* gather, int 
                   int src_rows, const void* blobs, size_t stride, const w4a8_wdesc* d, void* Y, int out_dtype,
                   hipStream_t s) {
     const Layout L = layout_of(d);
-    if (log_on())
-        std::fprintf(stderr, "w4a8: w4a8_moe_gemm_w8a8 E=%d rows=%d K=%d N=%d -> moe_grouped_stream_kernel\n", E, rows, L.K,
-                     L.N);
     GroupedArgs a;
     std::memset(&a, 0, sizeof(a));
     a.X = reinterpret_cast<const uint8_t*>(Xq);
@@ -438,16 +440,15 @@ static int run_w8(const int8_t* Xq, const float* sx, const int32_t* gather, int 
     a.Y = Y;
     a.ldy = size_t(L.N);
     a.out = out_dtype;
-    launch_grouped<GF_I8, false>(a, s);
+    const char* names = launch_grouped<GF_I8, false>(a, s);
+    if (log_on())
+        std::fprintf(stderr, "w4a8: w4a8_moe_gemm_w8a8 E=%d rows=%d K=%d N=%d -> %s\n", E, rows, L.K, L.N, names);
     return launched();
 }
 
 static int run_w16(const void* X, int dtype, int ldx, const int32_t* gather, int k, const int32_t* offsets, int E, int rows,
                    int src_rows, const void* W, size_t stride, int ldw, int K, int N, bool pair, void* Y, int ldy,
                    int out_dtype, hipStream_t s) {
-    if (log_on())
-        std::fprintf(stderr, "w4a8: w4a8_moe_gemm%s_w16a16 E=%d rows=%d K=%d N=%d %s -> moe_grouped_stream_kernel\n",
-                     pair ? "_silu" : "", E, rows, K, N, dtype == W4A8_F16 ? "float16" : "bfloat16");
     GroupedArgs a;
     std::memset(&a, 0, sizeof(a));
     a.X = static_cast<const uint8_t*>(X);
@@ -466,13 +467,11 @@ static int run_w16(const void* X, int dtype, int ldx, const int32_t* gather, int
     a.Y = Y;
     a.ldy = size_t(ldy);
     a.out = out_dtype;
-    if (dtype == W4A8_BF16) {
-        if (pair) launch_grouped<GF_BF16, true>(a, s);
-        else launch_grouped<GF_BF16, false>(a, s);
-    } else {
-        if (pair) launch_grouped<GF_F16, true>(a, s);
-        else launch_grouped<GF_F16, false>(a, s);
-    }
+    const char* names = dtype == W4A8_BF16 ? (pair ? launch_grouped<GF_BF16, true>(a, s) : launch_grouped<GF_BF16, false>(a, s))
+                                           : (pair ? launch_grouped<GF_F16, true>(a, s) : launch_grouped<GF_F16, false>(a, s));
+    if (log_on())
+        std::fprintf(stderr, "w4a8: w4a8_moe_gemm%s_w16a16 E=%d rows=%d K=%d N=%d %s -> %s\n", pair ? "_silu" : "", E, rows, K,
+                     N, dtype == W4A8_F16 ? "float16" : "bfloat16", names);
     return launched();
 }
 
@@ -509,6 +508,106 @@ int w4a8_moe_gemm_silu_w16a16(const void* X, int dtype, int ldx, const int32_t* 
     if (st || rows == 0) return st;
     return run_w16(X, dtype, ldx, gather, k, offsets, E, rows, src_rows, W, stride, ldw, K, I, true, H, ldh, dtype,
                    static_cast<hipStream_t>(stream));
+}
+
+// ------------------------------------------------------------------------------------
+// MoE layers
+// ------------------------------------------------------------------------------------
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace of a layer: pieces in order, each 256-byte aligned.  The W8A8 layer has the pieces and sizes of
+// w4a8_moe_workspace_size; the W16A16 layer the routing, h and the expert outputs.
+struct LayerWs {
+    size_t xq = 0, sx = 0, rows = 0, offs = 0, inv = 0, gu = 0, hq = 0, sh = 0, yd = 0, total = 0;
+};
+
+LayerWs layer_ws(int T, int k, int H, int I, int E, bool w8) {
+    const size_t R = size_t(T) * size_t(k);
+    LayerWs w;
+    size_t o = 0;
+    auto piece = [&](size_t bytes) {
+        const size_t at = o;
+        o = align256(o + bytes);
+        return at;
+    };
+    if (w8) w.xq = piece(size_t(T) * H), w.sx = piece(size_t(T) * 4);
+    w.rows = piece(R * 4);
+    w.offs = piece(size_t(E + 1) * 4);
+    w.inv = piece(R * 4);
+    w.gu = piece(R * size_t(I) * (w8 ? 4 : 2));                 // gate and up, or h
+    if (w8) w.hq = piece(R * size_t(I)), w.sh = piece(R * 4);
+    w.yd = piece(R * size_t(H) * 2);
+    w.total = o;
+    return w;
+}
+
+int layer_check(const void* X, const int32_t* ids, const float* w, int T, int k, int E, const void* ws, size_t ws_bytes,
+                size_t need, const void* out) {
+    if (T < 0 || k <= 0 || E <= 0 || E > 1024) return W4A8_EINVAL;
+    if ((long long)T * k > GROUPED_MAX_ROWS) return W4A8_EUNSUPPORTED;
+    if (T == 0) return W4A8_OK;
+    if (!X || !ids || !w || !ws || !out || !aligned16(X) || !aligned16(out)) return W4A8_EINVAL;
+    if (ws_bytes < need) return W4A8_ESIZE;
+    return (reinterpret_cast<uintptr_t>(ws) & 255u) ? W4A8_EINVAL : W4A8_OK;
+}
+
+}  // namespace
+
+size_t w4a8_moe_w16a16_workspace_size(int T, int k, int H, int I, int E) {
+    if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0) return 0;
+    return layer_ws(T, k, H, I, E, false).total;
+}
+
+int w4a8_moe_forward_w8a8(const void* X, const int32_t* ids, const float* w, int T, int k, int E, const void* gu_blobs,
+                          size_t gu_stride, const w4a8_wdesc* gu_desc, const void* d_blobs, size_t d_stride,
+                          const w4a8_wdesc* d_desc, void* ws, size_t ws_bytes, void* out, void* stream) {
+    int st = check_w8(gu_desc);
+    if (st || (st = check_w8(d_desc))) return st;
+    const int H = gu_desc->K, I = gu_desc->N / 2;
+    if (gu_desc->N % 2 || d_desc->K != I || d_desc->N != H) return W4A8_EINVAL;
+    if (T < 0 || k <= 0 || E <= 0) return W4A8_EINVAL;
+    if (H > 65536 || I > 16384) return W4A8_EUNSUPPORTED;       // rows of the two quantizations
+    const LayerWs L = layer_ws(T, k, H, I, E, true);
+    if ((st = layer_check(X, ids, w, T, k, E, ws, ws_bytes, L.total, out)) || T == 0) return st;
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    int8_t *xq = reinterpret_cast<int8_t*>(b + L.xq), *hq = reinterpret_cast<int8_t*>(b + L.hq);
+    float *sx = reinterpret_cast<float*>(b + L.sx), *sh = reinterpret_cast<float*>(b + L.sh);
+    int32_t *rows = reinterpret_cast<int32_t*>(b + L.rows), *offs = reinterpret_cast<int32_t*>(b + L.offs),
+            *inv = reinterpret_cast<int32_t*>(b + L.inv);
+    const int R = T * k;
+    if ((st = check_w8_call(xq, sx, rows, k, offs, E, R, T, gu_blobs, gu_stride, gu_desc, b + L.gu, W4A8_BF16))) return st;
+    if ((st = check_w8_call(hq, sh, nullptr, k, offs, E, R, R, d_blobs, d_stride, d_desc, b + L.yd, W4A8_BF16))) return st;
+    // every step's checks have passed: from here on only a launch error can stop the chain
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = w4a8_quant_act(X, T, H, H, xq, sx, stream))) return st;
+    if ((st = w4a8_moe_align(ids, T, k, E, rows, offs, inv, stream))) return st;
+    if ((st = run_w8(xq, sx, rows, k, offs, E, R, T, gu_blobs, gu_stride, gu_desc, b + L.gu, W4A8_BF16, s))) return st;
+    if ((st = w4a8_silu_mul_quant(b + L.gu, R, I, hq, sh, stream))) return st;
+    if ((st = run_w8(hq, sh, nullptr, k, offs, E, R, R, d_blobs, d_stride, d_desc, b + L.yd, W4A8_BF16, s))) return st;
+    return w4a8_moe_combine(b + L.yd, inv, w, T, k, H, out, stream);
+}
+
+int w4a8_moe_forward_w16a16(const void* X, const int32_t* ids, const float* w, int T, int k, int E, const void* Wgu,
+                            size_t gu_stride, const void* Wd, size_t d_stride, int H, int I, void* ws, size_t ws_bytes,
+                            void* out, void* stream) {
+    if (T < 0 || k <= 0 || E <= 0 || H <= 0 || I <= 0) return W4A8_EINVAL;
+    const LayerWs L = layer_ws(T, k, H, I, E, false);
+    int st = layer_check(X, ids, w, T, k, E, ws, ws_bytes, L.total, out);
+    if (st || T == 0) return st;
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    int32_t *rows = reinterpret_cast<int32_t*>(b + L.rows), *offs = reinterpret_cast<int32_t*>(b + L.offs),
+            *inv = reinterpret_cast<int32_t*>(b + L.inv);
+    const int R = T * k, dt = W4A8_BF16;
+    if ((st = check_w16_call(X, dt, H, rows, k, offs, E, R, T, Wgu, gu_stride, H, H, I, true, b + L.gu, I, dt))) return st;
+    if ((st = check_w16_call(b + L.gu, dt, I, nullptr, k, offs, E, R, R, Wd, d_stride, I, I, H, false, b + L.yd, H, dt)))
+        return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = w4a8_moe_align(ids, T, k, E, rows, offs, inv, stream))) return st;
+    if ((st = run_w16(X, dt, H, rows, k, offs, E, R, T, Wgu, gu_stride, H, H, I, true, b + L.gu, I, dt, s))) return st;
+    if ((st = run_w16(b + L.gu, dt, I, nullptr, k, offs, E, R, R, Wd, d_stride, I, I, H, false, b + L.yd, H, dt, s))) return st;
+    return w4a8_moe_combine(b + L.yd, inv, w, T, k, H, out, stream);
 }
 
 }  // extern "C"

@@ -99,3 +99,61 @@ def test_python_checks():
     x = torch.zeros(4, 64)
     with pytest.raises(ValueError):
         L.w4a8_moe_route(x, L.route_desc(64, 4), torch.zeros(4, 4, dtype=torch.int32), torch.zeros(4, 4))   # not on a GPU
+
+
+def test_experts_up_to_1024():
+    assert w8(E=1024, rows=0) == OK and w8(E=1025) == EI
+    assert w16(E=1024, rows=0) == OK and w16(E=1025) == EI
+    assert w16(True, E=1024, rows=0) == OK and w16(True, E=1025) == EI
+
+
+WS = ctypes.c_void_p(1 << 20)
+
+
+def layer8(gu=None, dn=None, X=P, ids=P, w=P, T=4, k=2, E=8, gub=P, gus=None, db=P, ds=None, ws=WS, nws=None, out=P, H=256, I=128):
+    gu = gu or L.desc(H, 2 * I, H, False, bits=8)
+    dn = dn or L.desc(I, H, I, False, bits=8)
+    gus = L.w4a8_packed_size(gu) if gus is None else gus
+    ds = L.w4a8_packed_size(dn) if ds is None else ds
+    nws = L.w4a8_moe_workspace_size(max(T, 0), max(k, 1), H, I, max(E, 1)) if nws is None else nws
+    return L.lib().w4a8_moe_forward_w8a8(X, ids, w, T, k, E, gub, gus, ctypes.byref(gu), db, ds, ctypes.byref(dn), ws, nws, out, None)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(T=-1), EI), (dict(k=0), EI), (dict(E=0), EI), (dict(E=1025), EI), (dict(X=None), EI), (dict(ids=None), EI),
+    (dict(w=None), EI), (dict(ws=None), EI), (dict(out=None), EI), (dict(gub=None), EI), (dict(db=None), EI),
+    (dict(X=ODD), EI), (dict(out=ODD), EI), (dict(gub=ODD), EI), (dict(ws=ctypes.c_void_p((1 << 20) + 16)), EI),
+    (dict(nws=1024), L.W4A8_ESIZE), (dict(gus=64), EI), (dict(ds=64), EI), (dict(T=1 << 23, k=4), EU),
+    (dict(gu=L.desc(256, 257, 256, False, bits=8)), EI), (dict(dn=L.desc(128, 128, 128, False, bits=8)), EI),
+    (dict(dn=L.desc(256, 256, 256, False, bits=8)), EI), (dict(gu=L.desc(256, 256, 128, False)), EU),
+    (dict(dn=L.desc(128, 256, 128, False)), EU), (dict(H=128, I=16512), EU), (dict(H=65664, I=128), EU),
+    (dict(T=0), OK), (dict(T=0, X=None, ids=None, w=None, ws=None, out=None), OK),
+])
+def test_w8_layer_refusals(over, want):
+    assert layer8(**over) == want
+
+
+def layer16(X=P, ids=P, w=P, T=4, k=2, E=8, gu=P, gus=None, dn=P, ds=None, H=256, I=72, ws=WS, nws=None, out=P):
+    nws = L.w4a8_moe_w16a16_workspace_size(max(T, 0), max(k, 1), H, I, max(E, 1)) if nws is None else nws
+    return L.lib().w4a8_moe_forward_w16a16(X, ids, w, T, k, E, gu, 2 * I * H if gus is None else gus, dn, H * I if ds is None else ds,
+                                           H, I, ws, nws, out, None)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(T=-1), EI), (dict(k=0), EI), (dict(E=0), EI), (dict(E=1025), EI), (dict(H=0), EI), (dict(I=0), EI), (dict(H=252), EI),
+    (dict(I=68), EI), (dict(X=None), EI), (dict(ids=None), EI), (dict(w=None), EI), (dict(ws=None), EI), (dict(out=None), EI),
+    (dict(gu=None), EI), (dict(dn=None), EI), (dict(X=ODD), EI), (dict(out=ODD), EI), (dict(gu=ODD), EI), (dict(dn=ODD), EI),
+    (dict(ws=ctypes.c_void_p((1 << 20) + 16)), EI), (dict(nws=1024), L.W4A8_ESIZE), (dict(gus=72 * 256), EI), (dict(ds=64), EI),
+    (dict(gus=2 * 72 * 256 + 4), EI), (dict(T=1 << 23, k=4), EU), (dict(T=0), OK),
+    (dict(T=0, X=None, ids=None, w=None, ws=None, out=None), OK),
+])
+def test_w16_layer_refusals(over, want):
+    assert layer16(**over) == want
+
+
+def test_w16_workspace_size():
+    """Routing (three integer arrays), h and the expert outputs, each piece 256-byte aligned."""
+    up = lambda n: (n + 255) // 256 * 256
+    assert L.w4a8_moe_w16a16_workspace_size(5, 3, 64, 24, 7) == 2 * up(60) + up(32) + up(15 * 24 * 2) + up(15 * 64 * 2)
+    for bad in ((-1, 1, 8, 8, 1), (1, 0, 8, 8, 1), (1, 1, 0, 8, 1), (1, 1, 8, 0, 1), (1, 1, 8, 8, 0)):
+        assert L.w4a8_moe_w16a16_workspace_size(*bad) == 0
