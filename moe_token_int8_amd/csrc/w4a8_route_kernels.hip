@@ -25,7 +25,6 @@ struct RouteArgs {
 };
 
 constexpr int ROUTE_WAVES = 4;      // waves of a workgroup
-constexpr int ROUTE_SPREAD = 4096;  // tokens up to which each gets a wave
 
 __device__ __forceinline__ float route_logit(const RouteArgs& a, size_t i) {
     if (a.dtype == W4A8_F32) return static_cast<const float*>(a.logits)[i];
@@ -33,39 +32,41 @@ __device__ __forceinline__ float route_logit(const RouteArgs& a, size_t i) {
     return a.dtype == W4A8_F16 ? f16_to_f32(b) : bf16_to_f32(b);
 }
 
-// exp(-a) for a >= 0 to about 2^-50: a = n ln 2 + r with |r| <= 0.35, the Taylor series of exp(-r) to the 12th power (the
-// next term is below 2^-52), scaled by 2^-n.
-__device__ __forceinline__ double exp_neg(double a) {
-    a = fmin(a, 750.0);                                         // exp(-750) is 0 in float64
-    const double n = rint(a * 1.4426950408889634);
-    double r = fma(n, -0.69314718036912382, a);                 // ln 2 in two parts, the first with 21 zero bits
-    r = -fma(n, -1.9082149292705877e-10, r);
-    double e = 1.0 / 479001600.0;
-    e = fma(e, r, 1.0 / 39916800.0);
-    e = fma(e, r, 1.0 / 3628800.0);
-    e = fma(e, r, 1.0 / 362880.0);
-    e = fma(e, r, 1.0 / 40320.0);
-    e = fma(e, r, 1.0 / 5040.0);
-    e = fma(e, r, 1.0 / 720.0);
-    e = fma(e, r, 1.0 / 120.0);
-    e = fma(e, r, 1.0 / 24.0);
-    e = fma(e, r, 1.0 / 6.0);
-    e = fma(e, r, 0.5);
+// exp(y) for |y| <= 750, relative error below 2^-50 near 0 and 2^-45 at the ends: y = n ln 2 + r with |r| <= 0.35, where
+// n is what adding 1.5 2^52 leaves in the low bits; exp(r) = 1 + r q(r) with q the polynomial that meets it at the 10
+// Chebyshev nodes of that range (the Taylor series needs two terms more); scaled by 2^n.
+__device__ __forceinline__ double route_exp(double y) {
+    const double t = fma(y, 1.4426950408889634, 6755399441055744.0), n = t - 6755399441055744.0;
+    const double r = fma(n, -0.6931471805599453, y);
+    double e = 0x1.289185613a3d6p-22;
+    e = fma(e, r, 0x1.72e1150d0c9b6p-19);
+    e = fma(e, r, 0x1.a019b90d2ae7ap-16);
+    e = fma(e, r, 0x1.a01994bd214e7p-13);
+    e = fma(e, r, 0x1.6c16c1788bd90p-10);
+    e = fma(e, r, 0x1.11111123c1f47p-7);
+    e = fma(e, r, 0x1.5555555553d63p-5);
+    e = fma(e, r, 0x1.5555555550d79p-3);
+    e = fma(e, r, 0x1.0000000000001p-1);
     e = fma(e, r, 1.0);
     e = fma(e, r, 1.0);
-    return ldexp(e, -int(n));
+    return ldexp(e, int(uint32_t(__builtin_bit_cast(uint64_t, t))));
 }
+__device__ __forceinline__ double exp_neg(double a) { return route_exp(-fmin(a, 750.0)); }   // a >= 0; exp(-750) is 0
 
-// 1 / d for 1 <= d: the hardware's estimate (2^-23) and two Newton steps.
+// 1 / d for 1 <= d <= 2^1022: the hardware's estimate (2^-23) and one step of third order.
 __device__ __forceinline__ double reciprocal(double d) {
-    double r = __builtin_amdgcn_rcp(d);
-    r = fma(fma(-d, r, 1.0), r, r);
-    return fma(fma(-d, r, 1.0), r, r);
+    const double r = __builtin_amdgcn_rcp(d), u = fma(-d, r, 1.0);
+    return fma(fma(u, u, u), r, r);
 }
 
 __device__ __forceinline__ double sigmoid64(float x) {
     const double e = exp_neg(fabs(double(x))), d = reciprocal(1.0 + e);
     return x >= 0.0f ? d : e * d;
+}
+
+// The same for a rank: one form for both signs, in which logits below -708 count as -708 (a score of 3e-308).
+__device__ __forceinline__ double sigmoid_rank(float x) {
+    return reciprocal(1.0 + route_exp(double(__builtin_amdgcn_fmed3f(-x, -745.0f, 708.0f))));
 }
 
 // exp(-a) for a >= 0 in float32, good to about 2 units: v_exp_f32 of the product in two parts.
@@ -82,14 +83,19 @@ __device__ __forceinline__ float exp_neg32(float a) {
 constexpr double ROUTE_NONE = -1.7e308;                         // a masked or taken expert; ranks are above -1e39
 
 __device__ __forceinline__ double route_key(double v, int index) {
-    v = fmin(v + 0.0, 1e300);                                   // -0 equals 0; an infinite rank stays a number
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint64_t low = (b >> 63) ? uint64_t(index) : uint64_t(1023 - index);
-    return __builtin_bit_cast(double, (b & ~uint64_t(1023)) | low);
+    const uint32_t sign = uint32_t(int32_t(b >> 32) >> 31), low = sign ^ uint32_t(index ^ 1023);
+    return __builtin_bit_cast(double, (b & ~uint64_t(1023)) | (low & 1023u));
 }
 __device__ __forceinline__ int route_index(double key) {
     const uint64_t b = __builtin_bit_cast(uint64_t, key);
-    return (b >> 63) ? int(b & 1023) : 1023 - int(b & 1023);
+    return int((uint32_t(b) ^ ~uint32_t(int32_t(b >> 32) >> 31)) & 1023u);
+}
+// the key of a masked expert: a number below all ranks, whatever its low half
+__device__ __forceinline__ double route_mask(double key, bool masked) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, key);
+    const uint32_t hi = masked ? uint32_t(__builtin_bit_cast(uint64_t, ROUTE_NONE) >> 32) : uint32_t(b >> 32);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | uint32_t(b));
 }
 __device__ __forceinline__ double route_value(double key) {
     return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~uint64_t(1023));
@@ -127,11 +133,38 @@ __device__ __forceinline__ T route_all(T v, F f) {
     return v;
 }
 
-// LANES lanes per token, EPL neighbouring experts in each; k <= LANES rounds of an argmax over the keys.  With 16 lanes a
-// wave serves 4 tokens and most of a round is the 16 keys of a lane (for many tokens: the vector unit is the bound); with
-// 64 lanes a round is shortest (for few tokens: the latency is).  A group of experts is `glanes` (1, 2, 4, .. 16)
-// whole lanes.
-template <int LANES, int EPL>
+// Descending order of key[LO .. LO + N): Batcher's odd-even merge sort, unrolled; what no one reads of its end is left out
+// by the compiler.
+template <int LO, int N, int STEP, int EPL>
+__device__ __forceinline__ void route_merge(double (&key)[EPL]) {
+    const auto swap = [&](int i, int j) __attribute__((always_inline)) {
+        const double u = key[i], v = key[j];
+        key[i] = fmax(u, v), key[j] = fmin(u, v);
+    };
+    if constexpr (2 * STEP < N) {
+        route_merge<LO, N, 2 * STEP>(key);
+        route_merge<LO + STEP, N, 2 * STEP>(key);
+#pragma unroll
+        for (int i = STEP; i + STEP < N; i += 2 * STEP) swap(LO + i, LO + i + STEP);
+    } else {
+        swap(LO, LO + STEP);
+    }
+}
+template <int LO, int N, int EPL>
+__device__ __forceinline__ void route_sort(double (&key)[EPL]) {
+    if constexpr (N > 1) {
+        route_sort<LO, N / 2>(key);
+        route_sort<LO + N / 2, N / 2>(key);
+        route_merge<LO, N, 1>(key);
+    }
+}
+
+// LANES lanes per token, EPL neighbouring experts in each, of which a lane keeps the DEPTH >= min(k, EPL) best in order;
+// k <= LANES rounds, each the best of the lanes' first keys, which its lane then drops.  A group of experts is `glanes`
+// (1, 2, 4, .. 16) whole lanes.  With 16 lanes a wave serves 4 tokens.  The vector unit is the bound of many tokens: 16384
+// of 256 experts with bias and groups take 1282 instructions a wave, 8.5 of the kernel's 12.4 us (a search of all keys in
+// each round and the Taylor series: 1949 and 18.0 us); half of them are the float64 scores and the keys.
+template <int LANES, int EPL, int DEPTH>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a, int glanes) {
     constexpr int TOKENS = 64 / LANES * ROUTE_WAVES;
     const int lane = threadIdx.x % LANES, e0 = lane * EPL;
@@ -142,11 +175,20 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
 
     float x[EPL];
     const bool full = e0 + EPL <= a.E;
-    if (EPL % 4 == 0 && a.dtype == W4A8_F32 && full && a.ldl % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0) {
+    const uintptr_t misfit = reinterpret_cast<uintptr_t>(a.logits) | uintptr_t(a.ldl & 3) << 2;
+    if (a.dtype == W4A8_F32 && full && !(misfit & 15)) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 4) {
             const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0 + j);
             x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        }
+    } else if (a.dtype != W4A8_F32 && full && !(misfit & 7) && !(a.ldl & 3)) {
+#pragma unroll
+        for (int j = 0; j < EPL; j += 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row + e0 + j);
+            const uint32_t h[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j + i] = a.dtype == W4A8_F16 ? f16_to_f32(uint16_t(h[i])) : bf16_to_f32(h[i]);
         }
     } else {
 #pragma unroll
@@ -165,9 +207,20 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
     const float ref = top > -__builtin_huge_valf() ? top : 0.0f;
     if (a.bias) {
         double p[EPL];
+        float bias[EPL];
+        if (full && !(reinterpret_cast<uintptr_t>(a.bias) & 15)) {
+#pragma unroll
+            for (int j = 0; j < EPL; j += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(a.bias + e0 + j);
+                bias[j] = v.x, bias[j + 1] = v.y, bias[j + 2] = v.z, bias[j + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) bias[j] = e0 + j < a.E ? a.bias[e0 + j] : 0.0f;
+        }
         if (a.sigmoid) {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) p[j] = sigmoid64(x[j]);
+            for (int j = 0; j < EPL; ++j) p[j] = sigmoid_rank(x[j]);
         } else {
             sum = 0.0;
 #pragma unroll
@@ -182,10 +235,10 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const double r = p[j] + double(e0 + j < a.E ? a.bias[e0 + j] : 0.0f);
-            const bool masked = x[j] == -__builtin_huge_valf() || r < -1e39;
+            const double r = p[j] + double(bias[j]);
             bad |= r != r;
-            key[j] = masked ? ROUTE_NONE : route_key(r, e0 + j);
+            // an infinite bias stays a number
+            key[j] = route_mask(route_key(fmin(r, 1e300), e0 + j), x[j] == -__builtin_huge_valf() || r < -1e39);
         }
     } else {
         if (!a.sigmoid) {
@@ -195,17 +248,29 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
             sum = double(route_all<LANES>(part, [](float u, float v) { return u + v; }));
         }
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) key[j] = x[j] == -__builtin_huge_valf() ? ROUTE_NONE : route_key(double(x[j]), e0 + j);
+        for (int j = 0; j < EPL; ++j)                           // -0 equals 0; an infinity stays a number
+            key[j] = route_mask(route_key(fmin(double(x[j]) + 0.0, 1e300), e0 + j), x[j] == -__builtin_huge_valf());
     }
     bad = route_all<LANES>(uint32_t(bad), [](uint32_t u, uint32_t v) { return u | v; }) != 0;
+    if constexpr (DEPTH == EPL) {
+        route_sort<0, EPL>(key);
+    } else {                                                    // the better half of two sorted halves, then sorted itself
+        route_sort<0, DEPTH>(key);
+        route_sort<DEPTH, DEPTH>(key);
+#pragma unroll
+        for (int j = 0; j < DEPTH; ++j) key[j] = fmax(key[j], key[EPL - 1 - j]);
+#pragma unroll
+        for (int d = DEPTH / 2; d; d /= 2)
+#pragma unroll
+            for (int j = 0; j < DEPTH; ++j)
+                if (!(j & d)) {
+                    const double u = key[j], v = key[j + d];
+                    key[j] = fmax(u, v), key[j + d] = fmin(u, v);
+                }
+    }
 
     if (a.groups > 1) {
-        double b1 = ROUTE_NONE, b2 = ROUTE_NONE;                // the group's two best
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            b2 = fmax(b2, fmin(b1, key[j]));
-            b1 = fmax(b1, key[j]);
-        }
+        double b1 = key[0], b2 = key[1];                        // the group's two best
         auto merge = [&](double c1, double c2) __attribute__((always_inline)) {
             b2 = fmax(fmax(b2, c2), fmin(b1, c1));
             b1 = fmax(b1, c1);
@@ -224,18 +289,17 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
             if (best > -1e300 && score == best) kept = true, score = ROUTE_NONE;
         }
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : ROUTE_NONE;
+        for (int j = 0; j < DEPTH; ++j) key[j] = route_mask(key[j], !kept);
     }
 
     int id = -1;                                                // of round `lane`
     for (int r = 0; r < a.k; ++r) {
-        double best = key[0];
-#pragma unroll
-        for (int j = 1; j < EPL; ++j) best = fmax(best, key[j]);
-        best = route_all<LANES>(best, max64);
+        const double best = route_all<LANES>(key[0], max64);
         if (lane == r && best > -1e300) id = route_index(best);
+        const bool mine = key[0] == best;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) key[j] = key[j] == best ? ROUTE_NONE : key[j];
+        for (int j = 0; j < DEPTH - 1; ++j) key[j] = mine ? key[j + 1] : key[j];
+        key[DEPTH - 1] = route_mask(key[DEPTH - 1], mine);
     }
     double w = 0.0;
     if (id >= 0) {
@@ -400,8 +464,9 @@ extern "C" int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, con
     const RouteArgs a{logits, dtype, T, ldl, bias, d->E, d->k, d->score == W4A8_ROUTE_SIGMOID, d->renormalize, groups, keep,
                       d->scale, ids, w};
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // 64 lanes a token where the waves of all tokens fit the chip at once, or where the rounds need more than 16 lanes
-    const bool spread = T <= ROUTE_SPREAD || d->k > 16 || d->E > 256;
+    // 64 lanes a token where the rounds or the experts need more than 16: those are no slower for few tokens either (64
+    // tokens of 256 experts 5.2 against 5.3 us, of 64 experts 2.8 against 4.1) and faster for many (4096: 5.6 against 8.1)
+    const bool spread = d->k > 16 || d->E > 256;
     const int epl = spread ? (d->E <= 256 ? 4 : 16) : d->E <= 64 ? 4 : d->E <= 128 ? 8 : 16;
     const int size = d->E / groups, glanes = size / epl;
     if (groups > 1 && (size % epl || glanes > 16 || (glanes & (glanes - 1)))) {
@@ -413,11 +478,12 @@ extern "C" int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, con
     } else {
         const int tokens = ROUTE_WAVES * (spread ? 1 : 4);
         const dim3 grid((T + tokens - 1) / tokens), block(64 * ROUTE_WAVES);
-        if (spread && epl == 4) moe_route_kernel<64, 4><<<grid, block, 0, s>>>(a, glanes);
-        else if (spread) moe_route_kernel<64, 16><<<grid, block, 0, s>>>(a, glanes);
-        else if (epl == 4) moe_route_kernel<16, 4><<<grid, block, 0, s>>>(a, glanes);
-        else if (epl == 8) moe_route_kernel<16, 8><<<grid, block, 0, s>>>(a, glanes);
-        else moe_route_kernel<16, 16><<<grid, block, 0, s>>>(a, glanes);
+        if (spread && epl == 4) moe_route_kernel<64, 4, 4><<<grid, block, 0, s>>>(a, glanes);
+        else if (spread) moe_route_kernel<64, 16, 16><<<grid, block, 0, s>>>(a, glanes);
+        else if (epl == 4) moe_route_kernel<16, 4, 4><<<grid, block, 0, s>>>(a, glanes);
+        else if (epl == 8) moe_route_kernel<16, 8, 8><<<grid, block, 0, s>>>(a, glanes);
+        else if (d->k <= 8) moe_route_kernel<16, 16, 8><<<grid, block, 0, s>>>(a, glanes);
+        else moe_route_kernel<16, 16, 16><<<grid, block, 0, s>>>(a, glanes);
     }
     return hipGetLastError() == hipSuccess ? W4A8_OK : W4A8_EHIP;
 }
