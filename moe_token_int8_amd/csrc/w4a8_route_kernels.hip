@@ -18,7 +18,7 @@ struct RouteArgs {
     int T;
     long long ldl;
     const float* bias;
-    int E, k, sigmoid, renorm, groups, keep;
+    int E, k, sigmoid, renorm, groups, keep, gsize;
     float scale;
     int32_t* ids;
     float* w;
@@ -160,29 +160,30 @@ __device__ __forceinline__ void route_sort(double (&key)[EPL]) {
 }
 
 // LANES lanes per token, EPL neighbouring experts in each, of which a lane keeps the DEPTH >= min(k, EPL) best in order;
-// k <= LANES rounds, each the best of the lanes' first keys, which its lane then drops.  A group of experts is `glanes`
-// (1, 2, 4, .. 16) whole lanes.  With 16 lanes a wave serves 4 tokens.  The vector unit is the bound of many tokens: 16384
+// k <= LANES rounds, each the best of the lanes' first keys, which its lane then drops.  A group of experts, or all of
+// them, has 2^gshift whole lanes, of which the last may be filled in part or not at all.  With 16 lanes a wave serves 4 tokens.  The vector unit is the bound of many tokens: 16384
 // of 256 experts with bias and groups take 1282 instructions a wave, 8.5 of the kernel's 12.4 us (a search of all keys in
 // each round and the Taylor series: 1949 and 18.0 us); half of them are the float64 scores and the keys.
 template <int LANES, int EPL, int DEPTH>
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a, int glanes) {
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a, int gshift) {
     constexpr int TOKENS = 64 / LANES * ROUTE_WAVES;
-    const int lane = threadIdx.x % LANES, e0 = lane * EPL;
+    const int lane = threadIdx.x % LANES, group = lane >> gshift, first = (lane - (group << gshift)) * EPL;
+    const int e0 = group * a.gsize + first, count = group < a.groups ? min(a.gsize - first, EPL) : 0;
     const int t0 = int(blockIdx.x) * TOKENS + int(threadIdx.x) / LANES;
     const int t = min(t0, a.T - 1);                             // every lane takes part in the exchanges
     const size_t row = size_t(t) * size_t(a.ldl);
     const auto max64 = [](double x, double y) { return fmax(x, y); };
 
     float x[EPL];
-    const bool full = e0 + EPL <= a.E;
-    const uintptr_t misfit = reinterpret_cast<uintptr_t>(a.logits) | uintptr_t(a.ldl & 3) << 2;
-    if (a.dtype == W4A8_F32 && full && !(misfit & 15)) {
+    const bool full = count == EPL && (e0 & 3) == 0;            // whole and aligned vectors
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.logits);
+    if (a.dtype == W4A8_F32 && full && !(base & 15) && !(a.ldl & 3)) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 4) {
             const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0 + j);
             x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
         }
-    } else if (a.dtype != W4A8_F32 && full && !(misfit & 7) && !(a.ldl & 3)) {
+    } else if (a.dtype != W4A8_F32 && full && !(base & 7) && !(a.ldl & 3)) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 4) {
             const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row + e0 + j);
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) x[j] = e0 + j < a.E ? route_logit(a, row + e0 + j) : -__builtin_huge_valf();
+        for (int j = 0; j < EPL; ++j) x[j] = j < count ? route_logit(a, row + e0 + j) : -__builtin_huge_valf();
     }
     bool bad = false;
     float top = -__builtin_huge_valf();
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) bias[j] = e0 + j < a.E ? a.bias[e0 + j] : 0.0f;
+            for (int j = 0; j < EPL; ++j) bias[j] = j < count ? a.bias[e0 + j] : 0.0f;
         }
         if (a.sigmoid) {
 #pragma unroll
@@ -275,11 +276,11 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
             b2 = fmax(fmax(b2, c2), fmin(b1, c1));
             b1 = fmax(b1, c1);
         };
-        if (glanes > 1) merge(route_across<0>(b1), route_across<0>(b2));
-        if (glanes > 2) merge(route_across<1>(b1), route_across<1>(b2));
-        if (glanes > 4) merge(route_across<2>(b1), route_across<2>(b2));
-        if (glanes > 8) merge(route_across<3>(b1), route_across<3>(b2));
-        const int group = lane / glanes;
+        if (gshift > 0) merge(route_across<0>(b1), route_across<0>(b2));
+        if (gshift > 1) merge(route_across<1>(b1), route_across<1>(b2));
+        if (gshift > 2) merge(route_across<2>(b1), route_across<2>(b2));
+        if (gshift > 3) merge(route_across<3>(b1), route_across<3>(b2));
+        if (gshift > 4) merge(route_across<4>(b1), route_across<4>(b2));
         double score = ROUTE_NONE;
         if (b1 > -1e300 && group < a.groups)
             score = route_key(a.bias && b2 > -1e300 ? route_value(b1) + route_value(b2) : route_value(b1), group);
@@ -316,7 +317,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
     }
 }
 
-// Groups that do not fall on whole lanes of the kernel above: one wave per token, the ranks in LDS for the group scores.
+// More groups than the kernel above has lanes for (100 groups of 2, 3 of 340): one wave per token, the ranks in LDS for the
+// group scores.
 // Lane l holds the experts l, l + 64, ... (EPL of them); ranks as above.
 template <int EPL>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_any_groups_kernel(RouteArgs a) {
@@ -462,28 +464,30 @@ extern "C" int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, con
     if ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(bias)) & 3u)
         return W4A8_EINVAL;
     const RouteArgs a{logits, dtype, T, ldl, bias, d->E, d->k, d->score == W4A8_ROUTE_SIGMOID, d->renormalize, groups, keep,
-                      d->scale, ids, w};
+                      d->E / groups, d->scale, ids, w};
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // 64 lanes a token where the rounds or the experts need more than 16: those are no slower for few tokens either (64
-    // tokens of 256 experts 5.2 against 5.3 us, of 64 experts 2.8 against 4.1) and faster for many (4096: 5.6 against 8.1)
-    const bool spread = d->k > 16 || d->E > 256;
-    const int epl = spread ? (d->E <= 256 ? 4 : 16) : d->E <= 64 ? 4 : d->E <= 128 ? 8 : 16;
-    const int size = d->E / groups, glanes = size / epl;
-    if (groups > 1 && (size % epl || glanes > 16 || (glanes & (glanes - 1)))) {
-        const dim3 grid((T + ROUTE_WAVES - 1) / ROUTE_WAVES), block(64 * ROUTE_WAVES);
+    // The first form that holds a token.  64 lanes only where the rounds or the experts need more than 16: those are no
+    // slower for few tokens either (64 tokens of 256 experts 5.2 against 5.3 us, of 64 experts 2.8 against 4.1) and faster
+    // for many (4096: 5.6 against 8.1).
+    constexpr struct { int lanes, epl; } forms[] = {{16, 4}, {16, 8}, {16, 16}, {64, 4}, {64, 16}};
+    int form = 0, gshift = 0;
+    for (; form < 5; ++form) {
+        gshift = 0;
+        while ((forms[form].epl << gshift) < a.gsize) ++gshift;
+        if (d->k <= forms[form].lanes && (groups << gshift) <= forms[form].lanes) break;
+    }
+    const int tokens = ROUTE_WAVES * (form < 3 ? 4 : 1);
+    const dim3 grid((T + tokens - 1) / tokens), block(64 * ROUTE_WAVES);
+    if (form == 0) moe_route_kernel<16, 4, 4><<<grid, block, 0, s>>>(a, gshift);
+    else if (form == 1) moe_route_kernel<16, 8, 8><<<grid, block, 0, s>>>(a, gshift);
+    else if (form == 2 && d->k <= 8) moe_route_kernel<16, 16, 8><<<grid, block, 0, s>>>(a, gshift);
+    else if (form == 2) moe_route_kernel<16, 16, 16><<<grid, block, 0, s>>>(a, gshift);
+    else if (form == 3) moe_route_kernel<64, 4, 4><<<grid, block, 0, s>>>(a, gshift);
+    else if (form == 4) moe_route_kernel<64, 16, 16><<<grid, block, 0, s>>>(a, gshift);
+    else {
         const size_t lds = size_t(ROUTE_WAVES) * 2 * d->E * sizeof(double);
-        if (d->E <= 64) moe_route_any_groups_kernel<1><<<grid, block, lds, s>>>(a);
-        else if (d->E <= 256) moe_route_any_groups_kernel<4><<<grid, block, lds, s>>>(a);
+        if (d->E <= 256) moe_route_any_groups_kernel<4><<<grid, block, lds, s>>>(a);
         else moe_route_any_groups_kernel<16><<<grid, block, lds, s>>>(a);
-    } else {
-        const int tokens = ROUTE_WAVES * (spread ? 1 : 4);
-        const dim3 grid((T + tokens - 1) / tokens), block(64 * ROUTE_WAVES);
-        if (spread && epl == 4) moe_route_kernel<64, 4, 4><<<grid, block, 0, s>>>(a, glanes);
-        else if (spread) moe_route_kernel<64, 16, 16><<<grid, block, 0, s>>>(a, glanes);
-        else if (epl == 4) moe_route_kernel<16, 4, 4><<<grid, block, 0, s>>>(a, glanes);
-        else if (epl == 8) moe_route_kernel<16, 8, 8><<<grid, block, 0, s>>>(a, glanes);
-        else if (d->k <= 8) moe_route_kernel<16, 16, 8><<<grid, block, 0, s>>>(a, glanes);
-        else moe_route_kernel<16, 16, 16><<<grid, block, 0, s>>>(a, glanes);
     }
     return hipGetLastError() == hipSuccess ? W4A8_OK : W4A8_EHIP;
 }

@@ -177,3 +177,27 @@ def test_many_tokens_other_stream_and_graph():
         torch.cuda.synchronize()
         want = call(x, None, 8, "softmax", True)
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+
+
+@pytest.mark.parametrize("E,groups,keep,k", [(200, 8, 3, 5), (56, 8, 2, 7), (36, 4, 4, 8), (252, 4, 2, 12), (768, 3, 1, 8),
+                                             (1024, 2, 1, 8), (40, 20, 7, 8), (130, 13, 2, 20),
+                                             (200, 100, 30, 8), (1020, 3, 2, 8)])             # the last two: more than the lanes hold
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_that_end_inside_a_lane(E, groups, keep, k, with_bias, score):
+    print("route odd groups", E, groups, keep, k, with_bias, score, flush=True)
+    g = torch.Generator().manual_seed(2 * E + groups)
+    for dt in TYPES.values():
+        x = (torch.randn(65, E + 4, generator=g) * 2).to(dt).to(DEV)[:, :E]     # rows further apart than E
+        bias = (torch.randn(E, generator=g) * 0.2).to(DEV) if with_bias else None
+        check(x, bias, k, score, renorm=True, groups=groups, keep=keep)
+
+
+def test_sigmoid_far_from_zero():
+    """Logits from -700 to 700: scores from 1e-304 to 1, by the sign of the logit one minus almost nothing or almost nothing."""
+    x = torch.linspace(-700, 700, 256).repeat(3, 1).to(DEV)
+    x[1] = x[1].flip(0)
+    x[2] = x[2] - 400                                           # the smallest are below what a score tells apart, none is chosen
+    check(x, None, 8, "sigmoid")
+    check(x, torch.zeros(256, device=DEV), 8, "sigmoid")
+    check(x[:, :100].contiguous(), torch.zeros(100, device=DEV), 8, "sigmoid")
