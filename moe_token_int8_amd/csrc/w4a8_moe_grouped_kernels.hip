@@ -98,7 +98,7 @@ __device__ __forceinline__ TileRows grouped_find(const GroupedArgs& a, int slot,
 }
 
 template <int FMT, bool PAIR, int MS, int CT, bool NT>
-__global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kernel(GroupedArgs a, int ncb) {
+__global__ __launch_bounds__(512, 4) void moe_grouped_stream_kernel(GroupedArgs a, int ncb) {
     using acc_t = typename GroupedAcc<FMT>::type;
     constexpr int COLS = PAIR ? CT * 8 : CT * 16;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -208,28 +208,10 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
         // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
         acc_t* red = reinterpret_cast<acc_t*>(smem);
         constexpr int ITEMS = CT * MS * 64, OUT = PAIR ? ITEMS / 2 : ITEMS;
-        constexpr int KEPT = MS == 4 ? 4 : GS_WAVES;            // planes held at a time
-        if constexpr (KEPT < GS_WAVES) {
-            if (wave >= KEPT) {
 #pragma unroll
-                for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < CT; ++t)
 #pragma unroll
-                    for (int ms = 0; ms < MS; ++ms) red[(wave - KEPT) * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
-            }
-            lds_barrier();
-            if (wave < KEPT) {
-#pragma unroll
-                for (int t = 0; t < CT; ++t)
-#pragma unroll
-                    for (int ms = 0; ms < MS; ++ms) acc[t][ms] += red[wave * ITEMS + (t * MS + ms) * 64 + lane];
-            }
-        }
-        if (wave < KEPT) {                                      // own plane: nobody else reads it before the barrier
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int ms = 0; ms < MS; ++ms) red[wave * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
-        }
+            for (int ms = 0; ms < MS; ++ms) red[wave * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
         // source rows and scales of this thread's outputs, in flight across the barrier
         constexpr int PER = (OUT + 511) / 512;
         int osrc[PER];
@@ -249,7 +231,7 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
         auto total = [&](const int o) __attribute__((always_inline)) {
             acc_t s = red[o];
 #pragma unroll
-            for (int w = 1; w < KEPT; ++w) s += red[w * ITEMS + o];
+            for (int w = 1; w < GS_WAVES; ++w) s += red[w * ITEMS + o];
             return s;
         };
 #pragma unroll
@@ -279,45 +261,44 @@ __global__ __launch_bounds__(512, MS == 1 ? 4 : 2) void moe_grouped_stream_kerne
     }
 }
 
-// Workgroups of a launch over `slots` row tiles: all tiles of the 16-row class; the other classes, which often have few
-// experts or none, go round in a grid that costs a few microseconds when it finds nothing (256 experts of 7168 columns:
-// 29 and 16 us with a workgroup for each possible tile).
+// Workgroups of a launch over `slots` row tiles: all tiles of the 16-row class; 32-row tiles go round in a grid that is
+// resident at once, two workgroups a compute unit (with one for each tile 3614 tokens of 161 experts lose 20 %, and 256
+// experts of 7168 columns took 16 us to find nothing).
 constexpr long long GS_GRID = 512;
 
 template <int FMT, bool PAIR, int MS, int CT, bool NT>
 static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s) {
-    constexpr size_t lds = size_t(MS == 4 ? 4 : GS_WAVES) * CT * MS * 64 * 16;
-    static_assert(lds <= 65536, "two workgroups of 16-row tiles share a compute unit");
+    constexpr size_t lds = size_t(GS_WAVES) * CT * MS * 64 * 16;
+    static_assert(lds <= 65536, "two workgroups share a compute unit");
     constexpr int cols = PAIR ? CT * 8 : CT * 16;
     const int ncb = (a.N + cols - 1) / cols;
     const long long blocks = MS == 1 ? slots * ncb : std::min(slots * ncb, GS_GRID);
     moe_grouped_stream_kernel<FMT, PAIR, MS, CT, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
-// Whether one launch of 64-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
+// Whether one launch of 32-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
 // estimates, in us, use what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates
-// measured on this chip: a compute unit takes a 64 x 64 streaming tile in 3 us and 32 bytes of operands a nanosecond,
-// with all of them 4.5 TB/s of weights, and a 256 x 256 tile in 9 us and 1.5 us for 128 bytes of K; the streaming classes
-// read 6 TB/s; all 4 launches cost 35 us beside that, 2 with many rows 25, those of up to 64 rows 12.  Examples (one launch /
-// by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 51 / 101 us; 205 x 4 of 6, K = 2432, N = 897 in 8 bits: 20 / 42;
-// 2062 x 3 of 8, K = 2104, N = 1410: 171 / 79; 792 x 8 of 50, K = 1928, N = 1952: 276 / 241; 25 x 2 of 138, K = 2160,
-// N = 756: 42 / 29; 64 x 8 of 256, K = 7168, N = 4096 in 8 bits: 1365 / 960.
-static bool one_launch(const GroupedArgs& a, bool pair) {
+// fitted to some 200 measured calls: 512 workgroups at a time take 1.5 to 3 us for a 32 x 64 tile, by its rows, and a
+// nanosecond for 30 (16 bit) or 36 bytes of its operands, all of them together 5 TB/s of weights; a 256 x 256 tile takes 9
+// us and 1.5 us for 128 bytes of K; the 16-row class reads 6 TB/s; the launches by class cost 13 us beside that with many
+// or few rows, else 20.  Examples (one launch / by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 38 / 82 us; 205
+// x 4 of 6, K = 2432, N = 897 in 8 bits: 19 / 43; 2814 x 5 of 68, K = 744, I = 19: 15 / 36; 6288 x 2 of 134, K = 3176,
+// N = 739: 329 / 223; 2913 x 7 of 40, K = 384, N = 413 in 8 bits: 37 / 28; 33 x 6 of 64, K = 4096, I = 1408: 261 / 219.
+static bool one_launch(const GroupedArgs& a, bool i8, bool pair) {
     const double rows = a.rows, E = a.E, avg = rows / E, kb = a.kb, width = pair ? 2.0 * a.N : a.N;
-    const double experts = std::min(E, rows);
-    auto rounds = [](double tiles) { return std::ceil(tiles / 256); };
-    const double weights = experts * width * kb;
-    const double items = (std::floor(rows / 64) + experts) * std::ceil(width / 64);
-    const double one = 6 + std::max(rounds(items) * (3 + (64 + std::min(64.0, avg)) * kb / 32e3), weights / 4.5e6);
-    const double tiles = (std::floor(rows / 256) + std::min(E, std::floor(rows / 65))) * std::ceil(width / 256);
-    const double split = (avg >= 128 ? 25 : rows <= 64 ? 12 : 35) + rounds(tiles) * (9 + kb / 85) * std::min(1.0, avg / 32) + weights / 6e6;
+    const double experts = std::min(E, rows), weights = experts * width * kb;
+    const double items = (std::floor(rows / 32) + experts) * std::ceil(width / 64);
+    const double item = 1.5 + 1.5 * std::min(1.0, avg / 32) + (64 + std::min(32.0, avg)) * kb / (i8 ? 36e3 : 30e3);
+    const double one = 6 + std::max(std::max(1.0, items / 512) * item, weights / 5e6);
+    const double tiles = (std::floor(rows / 256) + 0.75 * std::min(E, std::floor(rows / 65))) * std::ceil(width / 256);
+    const double split = (avg >= 128 ? 13 : rows <= 64 ? 13 : 20) + std::ceil(tiles / 256) * (9 + kb / 85) * std::min(1.0, avg / 32) +
+                         weights / 6e6 * std::max(0.0, 1 - avg / 128);
     return one < split;
 }
 
-// Row classes of the streaming kernel, one launch each: an expert of up to 16 rows costs nothing for rows it does not
-// have, and the launches of classes that no expert can be in are left out.  `slots` bounds the row tiles of the class.
-// Where experts have 128 rows on average, few have less than 65: those go into one launch of 64-row tiles.  Returns the
-// kernels' names for the log.
+// Row classes, one launch each: up to 16 rows, up to 64 (tiles of 32) and the MFMA tiles; classes that no expert can be in
+// are left out.  `slots` bounds the row tiles of a class.  Where experts have 128 rows on average, few have less than 65:
+// those share the second launch.  Returns the kernels' names for the log.
 template <int FMT, bool PAIR>
 static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
@@ -326,10 +307,10 @@ static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
     // a launch has less than 2^32 work-items; the 16-row class has a workgroup for each of its tiles, of 16 columns or more
     const bool wide = std::min(E, rows) * (long long)a.N >= (1ll << 27);
-    if (rows > 16 && (!near || wide || one_launch(a, PAIR))) {
+    if (rows > 16 && (!near || wide || one_launch(a, FMT == GF_I8, PAIR))) {
         a.lo = 1, a.hi = 0x7fffffff;
-        launch_stream_t<FMT, PAIR, 4, 4, false>(a, rows / 64 + std::min(E, rows), s);
-        return "moe_grouped_stream_kernel (64-row tiles)";
+        launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);
+        return "moe_grouped_stream_kernel (32-row tiles)";
     }
     const bool few_small = rows >= 128 * E;
     if (!few_small) {
@@ -348,14 +329,10 @@ static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
             else if (blocks < 1024) launch_stream_t<FMT, PAIR, 1, 2, false>(a, slots, s);
             else launch_stream_t<FMT, PAIR, 1, 4, false>(a, slots, s);
         }
-        if (rows > 16) {
-            a.lo = 17, a.hi = 33;
-            launch_stream_t<FMT, PAIR, 2, 4, false>(a, std::min(E, rows / 17), s);
-        }
     }
-    if (rows > 32) {
-        a.lo = few_small ? 1 : 33, a.hi = 65;
-        launch_stream_t<FMT, PAIR, 4, 4, false>(a, std::min(E, rows / a.lo), s);
+    if (rows > 16) {
+        a.lo = few_small ? 1 : 17, a.hi = 65;
+        launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows / a.lo), s);
     }
     if (rows <= 64) return "moe_grouped_stream_kernel (by rows)";
     a.lo = 65, a.hi = 0x7fffffff;
