@@ -452,6 +452,44 @@ static int run_w16(const void* X, int dtype, int ldx, const int32_t* gather, int
     return launched();
 }
 
+static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace of a layer: pieces in order, each 256-byte aligned.  The W8A8 layer has the pieces and sizes of
+// w4a8_moe_workspace_size; the W16A16 layer the routing, h and the expert outputs.
+struct LayerWs {
+    size_t xq = 0, sx = 0, rows = 0, offs = 0, inv = 0, gu = 0, hq = 0, sh = 0, yd = 0, total = 0;
+};
+
+static LayerWs layer_ws(int T, int k, int H, int I, int E, bool w8) {
+    const size_t R = size_t(T) * size_t(k);
+    LayerWs w;
+    size_t o = 0;
+    auto piece = [&](size_t bytes) {
+        const size_t at = o;
+        o = align256(o + bytes);
+        return at;
+    };
+    if (w8) w.xq = piece(size_t(T) * H), w.sx = piece(size_t(T) * 4);
+    w.rows = piece(R * 4);
+    w.offs = piece(size_t(E + 1) * 4);
+    w.inv = piece(R * 4);
+    w.gu = piece(R * size_t(I) * (w8 ? 4 : 2));                 // gate and up, or h
+    if (w8) w.hq = piece(R * size_t(I)), w.sh = piece(R * 4);
+    w.yd = piece(R * size_t(H) * 2);
+    w.total = o;
+    return w;
+}
+
+static int layer_check(const void* X, const int32_t* ids, const float* w, int T, int k, int E, const void* ws, size_t ws_bytes,
+                size_t need, const void* out) {
+    if (T < 0 || k <= 0 || E <= 0 || E > 1024) return W4A8_EINVAL;
+    if ((long long)T * k > GROUPED_MAX_ROWS) return W4A8_EUNSUPPORTED;
+    if (T == 0) return W4A8_OK;
+    if (!X || !ids || !w || !ws || !out || !aligned16(X) || !aligned16(out)) return W4A8_EINVAL;
+    if (ws_bytes < need) return W4A8_ESIZE;
+    return (reinterpret_cast<uintptr_t>(ws) & 255u) ? W4A8_EINVAL : W4A8_OK;
+}
+
 }  // namespace w4a8
 
 using namespace w4a8;
@@ -486,51 +524,6 @@ int w4a8_moe_gemm_silu_w16a16(const void* X, int dtype, int ldx, const int32_t* 
     return run_w16(X, dtype, ldx, gather, k, offsets, E, rows, src_rows, W, stride, ldw, K, I, true, H, ldh, dtype,
                    static_cast<hipStream_t>(stream));
 }
-
-// ------------------------------------------------------------------------------------
-// MoE layers
-// ------------------------------------------------------------------------------------
-namespace {
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Workspace of a layer: pieces in order, each 256-byte aligned.  The W8A8 layer has the pieces and sizes of
-// w4a8_moe_workspace_size; the W16A16 layer the routing, h and the expert outputs.
-struct LayerWs {
-    size_t xq = 0, sx = 0, rows = 0, offs = 0, inv = 0, gu = 0, hq = 0, sh = 0, yd = 0, total = 0;
-};
-
-LayerWs layer_ws(int T, int k, int H, int I, int E, bool w8) {
-    const size_t R = size_t(T) * size_t(k);
-    LayerWs w;
-    size_t o = 0;
-    auto piece = [&](size_t bytes) {
-        const size_t at = o;
-        o = align256(o + bytes);
-        return at;
-    };
-    if (w8) w.xq = piece(size_t(T) * H), w.sx = piece(size_t(T) * 4);
-    w.rows = piece(R * 4);
-    w.offs = piece(size_t(E + 1) * 4);
-    w.inv = piece(R * 4);
-    w.gu = piece(R * size_t(I) * (w8 ? 4 : 2));                 // gate and up, or h
-    if (w8) w.hq = piece(R * size_t(I)), w.sh = piece(R * 4);
-    w.yd = piece(R * size_t(H) * 2);
-    w.total = o;
-    return w;
-}
-
-int layer_check(const void* X, const int32_t* ids, const float* w, int T, int k, int E, const void* ws, size_t ws_bytes,
-                size_t need, const void* out) {
-    if (T < 0 || k <= 0 || E <= 0 || E > 1024) return W4A8_EINVAL;
-    if ((long long)T * k > GROUPED_MAX_ROWS) return W4A8_EUNSUPPORTED;
-    if (T == 0) return W4A8_OK;
-    if (!X || !ids || !w || !ws || !out || !aligned16(X) || !aligned16(out)) return W4A8_EINVAL;
-    if (ws_bytes < need) return W4A8_ESIZE;
-    return (reinterpret_cast<uintptr_t>(ws) & 255u) ? W4A8_EINVAL : W4A8_OK;
-}
-
-}  // namespace
 
 size_t w4a8_moe_w16a16_workspace_size(int T, int k, int H, int I, int E) {
     if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0) return 0;
