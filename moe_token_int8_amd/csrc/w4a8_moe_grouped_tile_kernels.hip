@@ -1,4 +1,4 @@
-// Expert-grouped GEMMs in 8 and 16 bits: the kernel for experts with many rows (256 x 256 MFMA tiles).
+// Expert-grouped GEMMs in 8 and 16 bits: the kernel for experts with many rows (MFMA tiles of 256 x 256 and 128 x 128).
 //
 // Source: P1 "Kimi 2.7 MoE: from 4-bit storage to INT8 (W4A8)" (pwwt.cn), section 4.4 step 4 (the grouped expert GEMM over
 // router-sorted rows, "the performance key") and section 5.1 (tiles matched to the MFMA operands).
@@ -11,21 +11,18 @@
 
 namespace w4a8 {
 
-// A persistent workgroup of 8 waves per compute unit walks over 256-row x 256-column tiles (paired form: 128 gate and the
-// matching 128 up columns).  A step is 128 bytes of K, a cache line of every row: the 256 activation rows and 256 weight
-// rows are copied straight from memory to LDS (16 bytes a lane, no registers in between), into two 64 KiB stages, one
-// step ahead of the MFMAs.  (Four stages of 64 bytes keep more copies in flight, but ask for every line twice: steps of
-// K = 4096 took 2.0 us against 1.75.)  Wave (wm, wn) owns rows 128 wm .. + 127 and 64 columns: 8 x 4 MFMA tiles, 128
-// accumulators a lane.
-constexpr int GT_M = 256, GT_N = 256;
+// Persistent workgroups of NW waves walk over tiles of 32 NW rows x 32 NW columns (paired form: half of them gate, the
+// matching half up columns): one of 8 waves with 256 x 256 tiles on a compute unit, or two of 4 waves with 128 x 128 tiles,
+// which read twice the bytes for a product but leave fewer rows and compute units empty.  A step is 128 bytes of K, a cache
+// line of every row: the activation rows and as many weight rows are copied straight from memory to LDS (16 bytes a lane,
+// no registers in between), into two stages of 64 or 32 KiB, one step ahead of the MFMAs.  (Four stages of 64 bytes keep
+// more copies in flight, but ask for every line twice: steps of K = 4096 took 2.0 us against 1.75.)  Wave (wm, wn) owns half
+// the rows and 64 columns: NW x 4 MFMA tiles, 128 or 64 accumulators a lane.
 constexpr int GT_STEP = 128;                                    // bytes of K in a step
-constexpr int GT_STAGE = (GT_M + GT_N) * GT_STEP;
-constexpr int GT_WOFF = GT_M * GT_STEP;                         // weights within a stage
 constexpr int GT_PANEL = 4;                                     // row tiles of a panel of consecutive tiles
 constexpr int GT_MAX_E = 1024;
-constexpr int GT_LIST = 512;                                    // tiles looked up at a time, one a thread
 
-// LDS image of a stage: rows of 128 bytes in eight 16-byte chunks, the activations' 256, then the weights'.  Chunk c of row
+// LDS image of a stage: rows of 128 bytes in eight 16-byte chunks, the activations', then the weights'.  Chunk c of row
 // r sits at position c ^ row_swizzle(r): 16 rows read at one chunk, and the halves of two neighbouring chunks that the
 // LDS serves together, then lie in distinct banks.  Weights in 8-bit codes keep the packed layout's order within 16
 // columns, 2 KiB, with neighbouring chunks swapped in the upper 8 columns for the same reason.
@@ -73,17 +70,22 @@ __device__ __forceinline__ int tile_column(bool f32, int n, int c) {
     return f32 ? n * 16 + c : (n >> 1) * 32 + (c >> 2) * 8 + (n & 1) * 4 + (c & 3);
 }
 
-template <int FMT, bool PAIR>
-__global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a) {
+template <int FMT, bool PAIR, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArgs a) {
     using acc_t = typename GroupedAcc<FMT>::type;
-    constexpr int COLS = PAIR ? GT_N / 2 : GT_N;                // columns of Y
+    constexpr int TILE = 32 * NW, THREADS = 64 * NW;
+    constexpr int GT_M = TILE, GT_STAGE = 2 * TILE * GT_STEP;
+    constexpr int GT_WOFF = TILE * GT_STEP;                     // weights within a stage
+    constexpr int GT_LIST = THREADS;                            // tiles looked up at a time, one a thread
+    constexpr int COLS = PAIR ? TILE / 2 : TILE;                // columns of Y
+    constexpr int MT = NW;                                      // 16-row tiles of a wave
     __shared__ __align__(1024) uint8_t stage0[GT_STAGE];
     __shared__ __align__(1024) uint8_t stage1[GT_STAGE];
     __shared__ int4 list[GT_LIST];                              // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[GT_MAX_E + 1];                         // row tiles before expert e
     __shared__ float rowscale[2][GT_M];                         // of this tile's rows and the next one's
     __shared__ int entries[GT_M];                               // gather entries of the next tile's rows
-    __shared__ int wsum[8];
+    __shared__ int wsum[NW];
     const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1;
     const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int q = lane >> 4, c16 = lane & 15;
@@ -91,17 +93,19 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     const int steps = (a.kb + GT_STEP - 1) / GT_STEP;
     const bool f32 = !PAIR && a.out == W4A8_F32;
 
-    // row tiles of every expert of this launch, as a prefix sum (two experts a thread)
+    // row tiles of every expert of this launch, as a prefix sum
     {
+        constexpr int EPT = GT_MAX_E / THREADS;                 // experts of a thread
         const int tid = threadIdx.x;
-        int t[2];
+        int t[EPT], incl = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 2 * tid + i;
+        for (int i = 0; i < EPT; ++i) {
+            const int e = EPT * tid + i;
             const int cnt = e < a.E ? min(a.offsets[e + 1], a.rows) - min(max(a.offsets[e], 0), a.rows) : 0;
-            t[i] = cnt >= a.lo && cnt < a.hi ? (cnt + GT_M - 1) / GT_M : 0;
+            t[i] = cnt >= a.lo && cnt < a.hi ? (cnt + TILE - 1) / TILE : 0;
+            incl += t[i];
         }
-        int incl = t[0] + t[1];
+        int excl = -incl;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int y = __shfl_up(incl, o, 64);
@@ -110,10 +114,13 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         if (lane == 63) wsum[wave] = incl;
         __syncthreads();
         for (int w = 0; w < wave; ++w) incl += wsum[w];
-        const int excl = incl - t[0] - t[1];
-        if (2 * tid <= a.E) first[2 * tid] = excl;
-        if (2 * tid + 1 <= a.E) first[2 * tid + 1] = excl + t[0];
-        if (a.E == GT_MAX_E && tid == 511) first[GT_MAX_E] = incl;
+        excl += incl;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            if (EPT * tid + i <= a.E) first[EPT * tid + i] = excl;
+            excl += t[i];
+        }
+        if (a.E == GT_MAX_E && tid == THREADS - 1) first[GT_MAX_E] = incl;
         __syncthreads();
     }
     const long long total = (long long)first[a.E] * ncb;
@@ -123,7 +130,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     const int mine = rank < total ? int((total - rank + nblk - 1) / nblk) : 0;      // tiles of this workgroup
     if (mine == 0) return;
 
-    // tiles k0 .. k0 + 511 of this workgroup; all threads, between barriers
+    // the tiles from k0 on of this workgroup; all threads, between barriers
     auto look_up = [&](const int k0) __attribute__((always_inline)) {
         const int tid = opaque(int(threadIdx.x));
         if (k0 + tid < mine) {
@@ -156,13 +163,13 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         lds_barrier();
     };
 
-    // Sources of this thread's copies, 4 of the 32 groups of 8 activation rows and 4 of the weights' 32 KiB, as byte offsets
+    // Sources of this thread's copies, 4 of the 4 NW groups of 8 activation rows and as many of the weights, as byte offsets
     // from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.  Rows past the
     // tile's last, weight rows past the last column and bytes past the last row's K lie outside it and load nothing.
     unsigned xoff[4], woff;
     __amdgpu_buffer_rsrc_t xr, wr[PAIR ? 2 : 1];                // paired form: gate rows, up rows
     const unsigned tile_bytes = unsigned(steps) * 2048u;        // GF_I8: 16 columns of codes
-    const unsigned wgroup = FMT == GF_I8 ? 4u * tile_bytes : 64u * a.ldw;   // from one copy to the next
+    const unsigned wgroup = FMT == GF_I8 ? NW / 2 * tile_bytes : 8u * NW * a.ldw;   // from one copy to the next
     // Workgroups that share rows or columns take the steps of every four in another order, each starting at its own: of the
     // lines that they all need, each then fetches a part ahead of the others, and a DRAM page is asked for four
     // neighbouring lines at a time.
@@ -171,8 +178,8 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     auto fill_part = [&](lds_ptr st, const int s0, const int part) __attribute__((always_inline)) {
         const int s = s0 < whole_fours ? (s0 & ~3) | ((s0 + turn) & 3) : s0, i = part >> 1;
         const unsigned wstep = unsigned(s) * (FMT == GF_I8 ? 2048u : GT_STEP);
-        if (part & 1) copy_to_lds(wr[PAIR ? i >> 1 : 0], woff + (wstep + (PAIR ? i & 1 : i) * wgroup), st + GT_WOFF + (i * 8 + wave) * 1024);
-        else copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * 8 + wave) * 1024);
+        if (part & 1) copy_to_lds(wr[PAIR ? i >> 1 : 0], woff + (wstep + (PAIR ? i & 1 : i) * wgroup), st + GT_WOFF + (i * NW + wave) * 1024);
+        else copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * NW + wave) * 1024);
     };
     constexpr int FILL = 8;                                     // copies of a wave in one fill
 
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         if (s < 2 * turns) {
             const int tid = opaque(int(threadIdx.x));
 #pragma unroll 1
-            for (int c = 0; c < GT_STAGE / 8192; ++c) *(LDS v4i*)(st + (c * 512 + tid) * 16) = v4i{0, 0, 0, 0};
+            for (int c = 0; c < GT_STAGE / (THREADS * 16); ++c) *(LDS v4i*)(st + (c * THREADS + tid) * 16) = v4i{0, 0, 0, 0};
         }
     };
     auto supply = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
@@ -217,7 +224,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         xr = a.gather ? buffer_of(a.X, size_t(a.src_rows - 1) * size_t(a.ldx) + size_t(a.kb))
                       : buffer_of(a.X + size_t(g.y) * size_t(a.ldx), size_t(g.z - 1) * size_t(a.ldx) + size_t(a.kb));
         if constexpr (FMT == GF_I8) {
-            wr[0] = buffer_of(wexp + a.codes_off + size_t(g.w) * 16 * tile_bytes, size_t(last_col / 16 + 1) * tile_bytes);
+            wr[0] = buffer_of(wexp + a.codes_off + size_t(g.w) * (COLS / 16) * tile_bytes, size_t(last_col / 16 + 1) * tile_bytes);
         } else {
 #pragma unroll
             for (int p = 0; p < (PAIR ? 2 : 1); ++p)
@@ -230,7 +237,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         turn = __builtin_amdgcn_readfirstlane(g.y / GT_M + g.w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                           // (opaque: a fused multiply-add would leave 64-bit results)
-            const int row = (i * 8 + wave) * 8 + (lane >> 3), chunk = (lane & 7) ^ row_swizzle(row);
+            const int row = (i * NW + wave) * 8 + (lane >> 3), chunk = (lane & 7) ^ row_swizzle(row);
             xoff[i] = unsigned(opaque(int(unsigned(max(source(a.gather ? entries[row] : row), 0)) * unsigned(a.ldx)))) + unsigned(chunk) * 16u;
             if (row >= g.z) xoff[i] = 0xf0000000u;
         }
@@ -247,20 +254,20 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
         supply(st1, 1);
     };
 
-    // Operands of half h (64 bytes of K) of a stage: the 4 weight tiles, and 4 of the 8 row tiles.  Lane group q takes chunk
+    // Operands of half h (64 bytes of K) of a stage: the 4 weight tiles, and half of the row tiles.  Lane group q takes chunk
     // 4 h + q, the packed layout's order.  The compiler may not see into the byte offsets: it would rebuild each address from
     // its terms and lose which stage it belongs to.
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / (NW / 2), wn = wave % (NW / 2);
     int xat[2], wat[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int pos = ((4 * h + q) ^ row_swizzle(c16)) * 16;
-        xat[h] = opaque((wm * 128 + c16) * GT_STEP + pos);
+        xat[h] = opaque((wm * (TILE / 2) + c16) * GT_STEP + pos);
         wat[h] = opaque(GT_WOFF + (FMT == GF_I8 ? wn * 8192 + (2 * lane + (h ^ (c16 >> 3))) * 16
                                                 : ((PAIR ? wn * 32 : wn * 64) + c16) * GT_STEP + pos));
     }
     auto read_w = [&](const lds_ptr st, const int h, const int n) __attribute__((always_inline)) {
-        return *(const LDS v4i*)(st + wat[h] + (PAIR ? (n >> 1) * 128 * GT_STEP + (n & 1) * 2048 : n * 2048));
+        return *(const LDS v4i*)(st + wat[h] + (PAIR ? (n >> 1) * (TILE / 2) * GT_STEP + (n & 1) * 2048 : n * 2048));
     };
     auto read_x = [&](const lds_ptr st, const int h, const int m) __attribute__((always_inline)) {
         return *(const LDS v4i*)(st + xat[h] + m * 2048);
@@ -268,7 +275,7 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
 
     // A tile whose columns come in whole 16-byte stores (of any address) ends, in every wave that computed, with at least
     // STORES of them, which the next tile's first barriers leave in flight.
-    constexpr int STORES = PAIR ? 8 : 16;
+    constexpr int STORES = PAIR ? MT : 2 * MT;
     const bool near_rows = a.ldy < (size_t(1) << 21);           // 32-bit offsets within a tile
     const int quantum = f32 ? 3 : 7;
     bool behind_stores = false;
@@ -296,38 +303,40 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
             g = uniform(list[k % GT_LIST]);
             request_rows(g);
         }
-        if (wm * 128 < cur.z) {
-            acc_t acc[4][8];
+        if (wm * (TILE / 2) < cur.z) {
+            acc_t acc[4][MT];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 8; ++m) acc[n][m] = acc_t{};
-            // 4 of the 64 MFMAs of a step: row tile m against the 4 weight tiles
+                for (int m = 0; m < MT; ++m) acc[n][m] = acc_t{};
+            // 4 of the 8 MT MFMAs of a step: row tile m against the 4 weight tiles
             auto mfma4 = [&](const v4i (&w)[4], const v4i x, const int m) __attribute__((always_inline)) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) acc[n][m] = grouped_mfma<FMT>(w[n], x, acc[n][m]);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            v4i wa[4], wb[4], xa[4], xb[4];
-            // One step: four groups of 16 MFMAs, the operands of each read from LDS during the group before it.  The barrier
+            constexpr int H = MT / 2, WR = 4 / H, CP = FILL / H;   // row tiles, weight reads and copies of a group
+            v4i wa[4], wb[4], xa[H], xb[H];
+            // One step: four groups of 4 H MFMAs, the operands of each read from LDS during the group before it.  The barrier
             // stands before the last group, when this step's last operands are in registers: behind it the next stage is
             // whole and this one is free for the copies of the step after.
             auto step = [&](const lds_ptr st, const lds_ptr next, const int s, const bool early) __attribute__((always_inline)) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    xb[m] = read_x(st, 0, 4 + m);
+                for (int m = 0; m < H; ++m) {
+                    xb[m] = read_x(st, 0, H + m);
                     mfma4(wa, xa[m], m);
                 }
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    wb[m] = read_w(st, 1, m);
+                for (int m = 0; m < H; ++m) {
+#pragma unroll
+                    for (int n = m * WR; n < (m + 1) * WR; ++n) wb[n] = read_w(st, 1, n);
                     xa[m] = read_x(st, 1, m);
-                    mfma4(wa, xb[m], 4 + m);
+                    mfma4(wa, xb[m], H + m);
                 }
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    xb[m] = read_x(st, 1, 4 + m);
+                for (int m = 0; m < H; ++m) {
+                    xb[m] = read_x(st, 1, H + m);
                     mfma4(wb, xa[m], m);
                 }
                 if (early) stage_barrier<STORES>();
@@ -335,19 +344,22 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
                 if (ragged && s + 2 == steps) clear_tail(next);
                 const bool more = s + 2 < steps;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    wa[m] = read_w(next, 0, m);
+                for (int m = 0; m < H; ++m) {
+#pragma unroll
+                    for (int n = m * WR; n < (m + 1) * WR; ++n) wa[n] = read_w(next, 0, n);
                     xa[m] = read_x(next, 0, m);
                     if (more) {
-                        fill_part(st, s + 2, 2 * m);
-                        fill_part(st, s + 2, 2 * m + 1);
+#pragma unroll
+                        for (int part = m * CP; part < (m + 1) * CP; ++part) fill_part(st, s + 2, part);
                     }
-                    mfma4(wb, xb[m], 4 + m);
+                    mfma4(wb, xb[m], H + m);
                 }
                 if (!more) pad(st, s + 2);
             };
 #pragma unroll
-            for (int m = 0; m < 4; ++m) wa[m] = read_w(st0, 0, m), xa[m] = read_x(st0, 0, m);
+            for (int n = 0; n < 4; ++n) wa[n] = read_w(st0, 0, n);
+#pragma unroll
+            for (int m = 0; m < H; ++m) xa[m] = read_x(st0, 0, m);
             for (int s = 0; s < steps; s += 2) {
                 step(st0, st1, s, behind_stores && s == 0);
                 step(st1, st0, s + 1, false);
@@ -391,8 +403,8 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
 #pragma unroll
             for (int n = 0; n < NT; ++n) coff[n] = col[n] < a.N ? unsigned(col[n]) * es : 0x80000000u;
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const int row = wm * 128 + m * 16 + c16;
+            for (int m = 0; m < MT; ++m) {
+                const int row = wm * (TILE / 2) + m * 16 + c16;
                 const float rs = rowscale[buf][row];
                 float y[NT][4];
 #pragma unroll
@@ -439,22 +451,41 @@ __global__ __launch_bounds__(512, 2) void moe_grouped_tile_kernel(GroupedArgs a)
     }
 }
 
+// Which tiles a call takes, and about how long they take, in us.  The host knows rows and E: an expert with more than 64
+// rows ends in a tile that is filled by half on average, and such experts are no more than rows / (65 + rows / E).  A round
+// of 256 large tiles takes 9.7 us and 1.6 us for 128 bytes of K, a round of 512 small ones 8 and 1.0 (with one workgroup a
+// compute unit 0.85, in 8 bits 0.55).  Measured, small / large: 8192 tokens x 6 of 64 experts, K = 1408, N = 4096: 720 /
+// 620 us; in 8 bits, K = 4096, N = 2816: 671 / 579; 4837 x 8 of 220, K = 768, N = 512: 92 / 86; 556 x 8 of 111, K = 1336,
+// I = 1786: 296 / 315; 787 x 5 of 6, K = 3200, N = 632 in 8 bits: 31 / 48; 4346 x 3 of 19, K = 2984, N = 256: 61 / 101.
+TileChoice choose_tiles(const GroupedArgs& a, bool i8, bool pair) {
+    const double rows = a.rows, steps = (a.kb + GT_STEP - 1) / GT_STEP, width = pair ? 2.0 * a.N : a.N;
+    const double ends = 0.5 * std::min(double(a.E), rows / (65 + rows / a.E));
+    const double large = (std::floor(rows / 256) + ends) * std::ceil(width / 256);
+    const double small = (std::floor(rows / 128) + ends) * std::ceil(width / 128);
+    const double us_large = std::ceil(large / 256) * (9.7 + 1.6 * steps);
+    const double us_small = std::ceil(small / 512) * (8 + (small > 256 ? 1.0 : i8 ? 0.55 : 0.85) * steps);
+    return us_small < us_large ? TileChoice{true, us_small} : TileChoice{false, us_large};
+}
+
 template <int FMT, bool PAIR>
-static void launch_tile_t(const GroupedArgs& a, int blocks, hipStream_t s) {
-    moe_grouped_tile_kernel<FMT, PAIR><<<dim3(unsigned(blocks)), dim3(512), 0, s>>>(a);
+static void launch_tile_t(const GroupedArgs& a, hipStream_t s) {
+    auto tiles = [&](long long tile) {                          // an upper bound
+        const long long cols = PAIR ? tile / 2 : tile;
+        return (a.rows / tile + std::min<long long>(a.E, a.rows / a.lo)) * ((a.N + cols - 1) / cols);
+    };
+    if (tiles(256) == 0) return;
+    if (choose_tiles(a, FMT == GF_I8, PAIR).small)
+        moe_grouped_tile_kernel<FMT, PAIR, 4><<<dim3(unsigned(std::min<long long>(512, tiles(128)))), dim3(256), 0, s>>>(a);
+    else
+        moe_grouped_tile_kernel<FMT, PAIR, 8><<<dim3(unsigned(std::min<long long>(256, tiles(256)))), dim3(512), 0, s>>>(a);
 }
 
 void launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s) {
-    // one workgroup a compute unit, fewer when the call has fewer tiles
-    const long long ncb = (a.N + (pair ? GT_N / 2 : GT_N) - 1) / (pair ? GT_N / 2 : GT_N);
-    const long long tiles = (a.rows / GT_M + std::min<long long>(a.E, a.rows / a.lo)) * ncb;
-    const int blocks = int(std::min<long long>(256, tiles));
-    if (blocks == 0) return;
-    if (fmt == GF_I8) launch_tile_t<GF_I8, false>(a, blocks, s);
-    else if (fmt == GF_BF16 && pair) launch_tile_t<GF_BF16, true>(a, blocks, s);
-    else if (fmt == GF_BF16) launch_tile_t<GF_BF16, false>(a, blocks, s);
-    else if (pair) launch_tile_t<GF_F16, true>(a, blocks, s);
-    else launch_tile_t<GF_F16, false>(a, blocks, s);
+    if (fmt == GF_I8) launch_tile_t<GF_I8, false>(a, s);
+    else if (fmt == GF_BF16 && pair) launch_tile_t<GF_BF16, true>(a, s);
+    else if (fmt == GF_BF16) launch_tile_t<GF_BF16, false>(a, s);
+    else if (pair) launch_tile_t<GF_F16, true>(a, s);
+    else launch_tile_t<GF_F16, false>(a, s);
 }
 
 }  // namespace w4a8
