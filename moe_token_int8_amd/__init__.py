@@ -142,16 +142,10 @@ def route_desc(E: int, k: int, score: int = W4A8_ROUTE_SOFTMAX, renormalize: boo
     return RouteDesc(int(E), int(k), int(score), int(bool(renormalize)), int(n_group), int(topk_group), float(scale))
 
 
-_dtypes = {}
-
-
 def _dtype(t) -> int:
     """w4a8_dtype of a tensor."""
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.bfloat16: W4A8_BF16, torch.float32: W4A8_F32, torch.float16: W4A8_F16})
     try:
-        return _dtypes[t.dtype]
+        return _torch().types[t.dtype]
     except KeyError:
         raise ValueError(f"{t.dtype} is not an element type of this call") from None
 
@@ -173,6 +167,30 @@ def _require_current(tensors, int32=(), float32=(), int8=()):
                 raise ValueError(f"expected {want}, got {t.dtype}")
             if t.get_device() != dev or dev < 0:
                 raise ValueError("GPU entry points take device tensors, on the current device")
+
+
+class _Torch:
+    """What the calls below need of torch, looked up once: their host time is most of a small call's."""
+
+    def __init__(self):
+        import torch
+        self.int32, self.int8, self.float32 = torch.int32, torch.int8, torch.float32
+        self.initialized, self.device = torch.cuda.is_initialized, torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.types = {torch.bfloat16: W4A8_BF16, torch.float32: W4A8_F32, torch.float16: W4A8_F16}
+
+    def current(self) -> int:
+        return self.device() if self.initialized() else -2      # a CPU tensor's device is -1
+
+
+_torch_of_calls = None
+
+
+def _torch() -> _Torch:
+    global _torch_of_calls
+    if _torch_of_calls is None:
+        _torch_of_calls = _Torch()
+    return _torch_of_calls
 
 
 def _ptr(x) -> int | None:
@@ -445,64 +463,99 @@ def w4a8_moe_forward_sets(X, topk_ids, topk_w, sets, workspace, out, stream=None
 def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=None) -> None:
     """Top-k routing: logits [T, E] (float32, bfloat16 or float16; rows may be strided) -> topk_ids int32 [T, k],
     topk_w float32 [T, k]; bias: float32 [E] for the choice only."""
-    _require_current((logits,), int32=(topk_ids,), float32=(topk_w, bias))
+    t = _torch()
+    dev = t.current()
+    if not (logits.get_device() == dev and topk_ids.get_device() == dev and topk_ids.dtype is t.int32 and
+            topk_w.get_device() == dev and topk_w.dtype is t.float32 and
+            (bias is None or bias.get_device() == dev and bias.dtype is t.float32)):
+        _require_current((logits,), int32=(topk_ids,), float32=(topk_w, bias))      # says which
     T, E = logits.shape
-    if E != d.E or logits.stride(1) != 1:
+    ldl, step = logits.stride()
+    if E != d.E or step != 1:
         raise ValueError("logits must be [T, E] with contiguous rows")
-    for t in (topk_ids, topk_w):
-        if t.shape != (T, d.k) or not t.is_contiguous():
-            raise ValueError("topk_ids and topk_w must be contiguous [T, k]")
+    want = (T, d.k)
+    if topk_ids.shape != want or topk_w.shape != want or not topk_ids.is_contiguous() or not topk_w.is_contiguous():
+        raise ValueError("topk_ids and topk_w must be contiguous [T, k]")
     if bias is not None and (bias.numel() != E or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous [E]")
-    _check(lib().w4a8_moe_route(logits.data_ptr(), _dtype(logits), T, max(logits.stride(0), E), _ptr(bias), d,
-                                topk_ids.data_ptr(), topk_w.data_ptr(), _stream(stream)), "w4a8_moe_route")
+    _check(lib().w4a8_moe_route(logits.data_ptr(), _dtype(logits), T, ldl if ldl > E else E,
+                                None if bias is None else bias.data_ptr(), d, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_route")
+
+
+_packed_sizes: dict = {}
+
+
+def _packed_size(d: WDesc) -> int:
+    """w4a8_packed_size, a function of the descriptor's bytes alone."""
+    key = bytes(d)
+    size = _packed_sizes.get(key)
+    if size is None:
+        size = _packed_sizes[key] = w4a8_packed_size(d)
+    return size
 
 
 def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int, blobs_dev, expert_stride: int,
                        d: WDesc, Y, out_dtype: int = W4A8_OUT_BF16, stream=None) -> None:
     """Grouped W8A8 GEMM: w4a8_moe_gemm for 8-bit blobs with one scale per output channel (group_size = K)."""
-    _require_current((blobs_dev, Y), int8=(Xq,), float32=(sx,), int32=(gather, expert_offsets))
-    src_rows = Xq.shape[0]
-    if Xq.shape[1] != d.K or not Xq.is_contiguous() or sx.numel() < src_rows or not sx.is_contiguous():
+    t = _torch()
+    dev = t.current()
+    if not (Xq.get_device() == dev and Xq.dtype is t.int8 and sx.get_device() == dev and sx.dtype is t.float32 and
+            expert_offsets.get_device() == dev and expert_offsets.dtype is t.int32 and blobs_dev.get_device() == dev and
+            Y.get_device() == dev and (gather is None or gather.get_device() == dev and gather.dtype is t.int32)):
+        _require_current((blobs_dev, Y), int8=(Xq,), float32=(sx,), int32=(gather, expert_offsets))     # says which
+    src_rows, K = Xq.shape
+    if K != d.K or not Xq.is_contiguous() or sx.numel() < src_rows or not sx.is_contiguous():
         raise ValueError("Xq must be a contiguous [src_rows, K] with one scale in sx for each row")
     if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < rows):
         raise ValueError("expert_offsets must hold E + 1 entries and gather one per routed row")
     if out_dtype != (W4A8_F32 if Y.element_size() == 4 else W4A8_BF16) or Y.numel() < rows * d.N or not Y.is_contiguous():
         raise ValueError("Y must be a contiguous [rows, N] of out_dtype")
-    if blobs_dev.numel() * blobs_dev.element_size() < (E - 1) * expert_stride + w4a8_packed_size(d):
+    if blobs_dev.numel() * blobs_dev.element_size() < (E - 1) * expert_stride + _packed_size(d):
         raise ValueError("blobs_dev does not hold E blobs at expert_stride")
-    _check(lib().w4a8_moe_gemm_w8a8(Xq.data_ptr(), sx.data_ptr(), _ptr(gather), int(k), expert_offsets.data_ptr(), int(E),
-                                    int(rows), src_rows, blobs_dev.data_ptr(), int(expert_stride), d, Y.data_ptr(),
-                                    int(out_dtype), _stream(stream)), "w4a8_moe_gemm_w8a8")
+    _check(lib().w4a8_moe_gemm_w8a8(Xq.data_ptr(), sx.data_ptr(), None if gather is None else gather.data_ptr(), int(k),
+                                    expert_offsets.data_ptr(), int(E), int(rows), src_rows, blobs_dev.data_ptr(),
+                                    int(expert_stride), d, Y.data_ptr(), int(out_dtype),
+                                    t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_w8a8")
 
 
-def _w16_args(X, gather, k, expert_offsets, W, Y, width: int):
-    """Checked arguments of the unquantized grouped products, up to and including the row stride of Y."""
-    _require_current((X, W, Y), int32=(gather, expert_offsets))
-    E, N, K = W.shape
-    if X.dtype != W.dtype or X.shape[1] != K or N != width * Y.shape[1]:
+def _w16_args(X, gather, k, expert_offsets, W, Y, width: int, stream):
+    """Checked arguments of the unquantized grouped products, up to and including the row stride of Y; the stream."""
+    t = _torch()
+    dev = t.current()
+    if not (X.get_device() == dev and W.get_device() == dev and Y.get_device() == dev and
+            expert_offsets.get_device() == dev and expert_offsets.dtype is t.int32 and
+            (gather is None or gather.get_device() == dev and gather.dtype is t.int32)):
+        _require_current((X, W, Y), int32=(gather, expert_offsets))                 # says which
+    (E, N, K), (src_rows, Kx), (rows, I) = W.shape, X.shape, Y.shape
+    (stride, ldw, w1), (ldx, x1), (ldy, y1) = W.stride(), X.stride(), Y.stride()
+    if X.dtype is not W.dtype or Kx != K or N != width * I:
         raise ValueError("X [src_rows, K], W [E, N, K] and Y do not match")
-    if X.stride(1) != 1 or W.stride(2) != 1 or Y.stride(1) != 1:
+    if x1 != 1 or w1 != 1 or y1 != 1:
         raise ValueError("the last dimension of X, W and Y must be contiguous")
-    if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < Y.shape[0]):
+    if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < rows):
         raise ValueError("expert_offsets must hold E + 1 entries and gather one per row of Y")
-    return (X.data_ptr(), _dtype(X), X.stride(0), _ptr(gather), int(k), expert_offsets.data_ptr(), E, Y.shape[0], X.shape[0],
-            W.data_ptr(), W.stride(0), W.stride(1), K, Y.shape[1], Y.data_ptr(), Y.stride(0))
+    # the stride of a dimension of one entry says nothing
+    ldx, ldy = K if src_rows == 1 else ldx, I if rows == 1 else ldy
+    ldw = K if N == 1 else ldw
+    stride = N * ldw if E == 1 else stride
+    return (X.data_ptr(), _dtype(X), ldx, None if gather is None else gather.data_ptr(), int(k), expert_offsets.data_ptr(), E,
+            rows, src_rows, W.data_ptr(), stride, ldw, K, I, Y.data_ptr(), ldy), (t.raw_stream(dev) if stream is None else int(stream))
 
 
 def w4a8_moe_gemm_w16a16(X, gather, k: int, expert_offsets, W, Y, stream=None) -> None:
     """Grouped unquantized GEMM: X [src_rows, K] and W [E, N, K] in bfloat16 or float16, Y [rows, N] in the same type
     or float32; rows may be strided."""
-    args = _w16_args(X, gather, k, expert_offsets, W, Y, 1)
-    _check(lib().w4a8_moe_gemm_w16a16(*args, _dtype(Y), _stream(stream)), "w4a8_moe_gemm_w16a16")
+    args, s = _w16_args(X, gather, k, expert_offsets, W, Y, 1, stream)
+    _check(lib().w4a8_moe_gemm_w16a16(*args, _dtype(Y), s), "w4a8_moe_gemm_w16a16")
 
 
 def w4a8_moe_gemm_silu_w16a16(X, gather, k: int, expert_offsets, W, H, stream=None) -> None:
     """Grouped unquantized gate/up GEMM with silu(gate) * up in its epilogue: W [E, 2I, K], H [rows, I] of X's type."""
-    args = _w16_args(X, gather, k, expert_offsets, W, H, 2)
-    if H.dtype != X.dtype:
+    args, s = _w16_args(X, gather, k, expert_offsets, W, H, 2, stream)
+    if H.dtype is not X.dtype:
         raise ValueError("H must have the type of X")
-    _check(lib().w4a8_moe_gemm_silu_w16a16(*args, _stream(stream)), "w4a8_moe_gemm_silu_w16a16")
+    _check(lib().w4a8_moe_gemm_silu_w16a16(*args, s), "w4a8_moe_gemm_silu_w16a16")
 
 
 def w4a8_moe_w16a16_workspace_size(T: int, k: int, H: int, I: int, E: int) -> int:

@@ -288,3 +288,16 @@ def test_malformed_offsets_stay_inside_the_output():
     assert (buf[:4] == SENTINEL).all() and (buf[44:] == SENTINEL).all()
     y, mag = w16_reference(c)
     assert_within(buf[4:44], y, w16_bound(torch.bfloat16, 64, y, mag), "clamped")
+
+
+@pytest.mark.parametrize("silu", [False, True])
+def test_w16_single_entries_with_any_stride(silu):
+    """One row, one expert, one column: their strides say nothing."""
+    c = w16_inputs(14, torch.bfloat16, [1], 64, 2 if silu else 1)
+    want = run_w16(c, silu=silu)
+    X, W = c["X"].to(DEV).as_strided((1, 64), (0, 1)), c["W"].to(DEV)
+    W = W.as_strided(W.shape, (3, 64, 1))
+    Y = torch.zeros(1, 1, dtype=torch.bfloat16, device=DEV).as_strided((1, 1), (0, 1))
+    f = L.w4a8_moe_gemm_silu_w16a16 if silu else L.w4a8_moe_gemm_w16a16
+    f(X, None, 1, c["offsets"].to(DEV), W, Y)
+    assert torch.equal(Y, want)
