@@ -578,6 +578,9 @@ def w4a8_moe_forward_w8a8(X, topk_ids, topk_w, E: int, gu_blobs, gu_stride: int,
     _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
     if X.shape[1] != gu_desc.K:
         raise ValueError("X must be [T, K of the gate/up weights]")
+    for blobs, stride, d in ((gu_blobs, gu_stride, gu_desc), (d_blobs, d_stride, d_desc)):
+        if blobs.numel() * blobs.element_size() < (E - 1) * stride + _packed_size(d):
+            raise ValueError("the weights do not hold E blobs at their stride")
     T, k = topk_ids.shape
     _check(lib().w4a8_moe_forward_w8a8(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, int(E), _ptr(gu_blobs), int(gu_stride),
                                        gu_desc, _ptr(d_blobs), int(d_stride), d_desc, _ptr(workspace),
@@ -592,7 +595,7 @@ def w4a8_moe_forward_w16a16(X, topk_ids, topk_w, Wgu, Wd, workspace, out, stream
     E, I2, H = Wgu.shape
     if Wd.shape != (E, H, I2 // 2) or X.shape[1] != H or I2 % 2 or Wgu.dtype != X.dtype or Wd.dtype != X.dtype:
         raise ValueError("Wgu [E, 2I, H] and Wd [E, H, I] must be bfloat16 and match X")
-    if not Wgu[0].is_contiguous() or not Wd[0].is_contiguous():
+    if E == 0 or not Wgu[0].is_contiguous() or not Wd[0].is_contiguous():
         raise ValueError("each expert's weights must be dense")
     T, k = topk_ids.shape
     _check(lib().w4a8_moe_forward_w16a16(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, E, _ptr(Wgu), Wgu.stride(0), _ptr(Wd),

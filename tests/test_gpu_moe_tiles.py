@@ -1,4 +1,4 @@
-"""Grouped products at sizes whose experts are worth 256 x 256 MFMA tiles, beside experts of every smaller row class, and at
+"""Grouped products at sizes whose experts are worth MFMA tiles, of 128 x 128 (about 2050 columns) and of 256 x 256 (4100), beside experts of every smaller row class, and at
 the limits of the launches: many experts, more tiles than a workgroup lists at once, weights past the Infinity Cache,
 activations that 32-bit offsets do not reach."""
 import numpy as np
@@ -24,14 +24,14 @@ LARGE = [129, 255, 300, 700, 1031]
 MIXED = [1, 2, 16, 17, 32, 33, 64, 65, 129, 255, 257, 0, 511, 300, 5, 0]
 
 
-@pytest.mark.parametrize("K,N", [(1152, 2306), (1280, 2049)])                 # an odd and an even number of 128-byte steps
+@pytest.mark.parametrize("K,N", [(1152, 2306), (1280, 2049), (1152, 4102), (1280, 4097)])     # an odd and an even number of steps
 def test_w8_tiles(K, N):
     print("w8 tiles", K, N, flush=True)
     check_w8(w8_inputs(21, LARGE, K, N))
     check_w8(w8_inputs(22, LARGE, K, N, src_rows=333, k=3, extra_rows=70), (torch.bfloat16,))
 
 
-@pytest.mark.parametrize("K,N", [(1096, 2050), (1152, 2051)])                 # K ends inside a step; whole steps, odd rows
+@pytest.mark.parametrize("K,N", [(1096, 2050), (1152, 2051), (1096, 4100), (1152, 4099)])     # K ends inside a step; whole steps
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_w16_tiles(K, N, dtype):
     print("w16 tiles", K, N, dtype, flush=True)
@@ -39,7 +39,7 @@ def test_w16_tiles(K, N, dtype):
     check_w16(w16_inputs(24, dtype, LARGE, K, N, src_rows=333, k=3, extra_rows=70), (dtype,), pad=8)
 
 
-@pytest.mark.parametrize("K,I", [(1096, 1100), (1280, 1153)])
+@pytest.mark.parametrize("K,I", [(1096, 1100), (1280, 1153), (1096, 2060), (1280, 2051)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_silu_tiles(K, I, dtype):
     print("silu tiles", K, I, dtype, flush=True)
@@ -49,6 +49,7 @@ def test_silu_tiles(K, I, dtype):
 
 def test_every_row_class_in_one_call():
     print("classes w16", flush=True)
+    check_w16(w16_inputs(48, torch.bfloat16, MIXED, 2200, 4100, src_rows=500, k=4, extra_rows=3), (torch.bfloat16,))
     check_w16(w16_inputs(27, torch.bfloat16, MIXED, 2200, 2050, src_rows=500, k=4, extra_rows=3), (torch.bfloat16,))
     print("classes silu", flush=True)
     check_silu(w16_inputs(28, torch.bfloat16, MIXED, 2200, 2 * 1030, std=0.02))
@@ -56,9 +57,10 @@ def test_every_row_class_in_one_call():
     check_w8(w8_inputs(29, MIXED, 2304, 4100, src_rows=500, k=4, extra_rows=3), (torch.bfloat16,))
 
 
-def test_tiles_gather_entries_that_name_no_row():
+@pytest.mark.parametrize("N", [2050, 4100])
+def test_tiles_gather_entries_that_name_no_row(N):
     """Invalid entries give zero rows in tiles, and no row reads the one they would clamp to."""
-    c = w16_inputs(30, torch.bfloat16, LARGE, 1096, 2050, src_rows=50, k=2)
+    c = w16_inputs(30, torch.bfloat16, LARGE, 1096, N, src_rows=50, k=2)
     c["gather"][::5] = -1
     c["gather"][1::7] = 100
     c["gather"][2::9] = 2 ** 31 - 1
@@ -70,28 +72,30 @@ def test_tiles_gather_entries_that_name_no_row():
     assert torch.isnan(Y[src == 0]).all() and torch.isfinite(Y[~zero & (src != 0)]).all()
 
 
-def test_tiles_infinity_in_the_last_values_of_k():
+@pytest.mark.parametrize("N", [2050, 4100])
+def test_tiles_infinity_in_the_last_values_of_k(N):
     """K = 1096 ends inside a 128-byte step; behind it the rows hold NaN, which must not reach any sum."""
-    c = w16_inputs(31, torch.bfloat16, LARGE, 1096, 2050)
+    c = w16_inputs(31, torch.bfloat16, LARGE, 1096, N)
     c["X"][140, 1095] = float("inf")
     c["W"][3, 7, 1094] = float("-inf")
     Y = run_w16(c, torch.float32, pad=8).cpu()
     off = c["offsets"].tolist()
-    bad = torch.zeros(c["rows"], 2050, dtype=torch.bool)
+    bad = torch.zeros(c["rows"], N, dtype=torch.bool)
     bad[140] = True
     bad[off[3]:off[4], 7] = True
     assert not torch.isfinite(Y[bad]).any() and torch.isfinite(Y[~bad]).all()
 
 
-def test_tiles_output_views_and_repeats():
-    c = w16_inputs(32, torch.bfloat16, LARGE, 1096, 2047)
+@pytest.mark.parametrize("N", [2047, 4095])
+def test_tiles_output_views_and_repeats(N):
+    c = w16_inputs(32, torch.bfloat16, LARGE, 1096, N)
     want = run_w16(c)
-    buf = torch.full((c["rows"] + 2, 2053), SENTINEL, dtype=torch.bfloat16, device=DEV)
-    got = run_w16(c, Y=buf[1:-1, 3:2050])
+    buf = torch.full((c["rows"] + 2, N + 6), SENTINEL, dtype=torch.bfloat16, device=DEV)
+    got = run_w16(c, Y=buf[1:-1, 3:N + 3])
     assert torch.equal(got, want)
-    buf[1:-1, 3:2050] = SENTINEL
+    buf[1:-1, 3:N + 3] = SENTINEL
     assert (buf == SENTINEL).all()
-    c8 = w8_inputs(33, LARGE, 1152, 2306)
+    c8 = w8_inputs(33, LARGE, 1152, N)
     dw = w8_device(c8)
     assert torch.equal(run_w8(c8, dw=dw), run_w8(c8, dw=dw))
 
@@ -117,6 +121,20 @@ def test_the_most_rows():
     wt = W[0].float().t().contiguous()
     for a in range(0, rows, 1 << 21):
         assert torch.equal(Y[a:a + (1 << 21)].float(), X[a:a + (1 << 21)].float() @ wt), a
+
+
+def test_the_most_rows_of_small_tiles():
+    """2^24 rows of two experts and 100 columns: 131073 tiles of 128 rows, one more than 512 workgroups list at once."""
+    rows, K, N, cut = 1 << 24, 8, 100, (1 << 23) + 1
+    g = torch.Generator(device=DEV).manual_seed(42)
+    X = torch.randint(-4, 5, (rows, K), generator=g, device=DEV).to(torch.bfloat16)
+    W = torch.randint(-4, 5, (2, N, K), generator=g, device=DEV).to(torch.bfloat16)
+    Y = torch.full((rows, N), SENTINEL, dtype=torch.bfloat16, device=DEV)
+    print("most rows, small tiles", flush=True)
+    L.w4a8_moe_gemm_w16a16(X, None, 1, torch.tensor([0, cut, rows], dtype=torch.int32, device=DEV), W, Y)
+    torch.cuda.synchronize()
+    for e, (a, b) in enumerate(((0, cut), (cut, rows))):
+        assert torch.equal(Y[a:b].float(), X[a:b].float() @ W[e].float().t().contiguous()), e
 
 
 def test_weights_past_the_infinity_cache():
@@ -184,3 +202,41 @@ def test_silu_at_the_ends_of_the_range(rows, dtype):
     assert (H[top].double().abs() >= torch.finfo(dtype).max).all() and torch.equal(torch.sign(H[top]).double(), torch.sign(want[top]))
     e = 8 * 2.0 ** -23 * want[fit].abs() + 2.0 ** -126 * (g.double() * u.double()).abs().expand(rows, -1)[fit].nan_to_num(posinf=0)
     assert_within(H[fit], want[fit], e + half_step(dtype, want[fit].abs() + e) + 1e-38, "silu edges")
+
+
+@pytest.mark.parametrize("N", [1026, 4100])
+def test_tiles_in_a_graph(N):
+    """Every product captured at tile sizes, replayed on other splits of the rows with eager calls between."""
+    rows, E = 2400, 5
+    c8 = w8_inputs(49, [rows, 0, 0, 0, 0], 1152, N, src_rows=200, k=3)
+    c16 = w16_inputs(50, torch.bfloat16, [rows, 0, 0, 0, 0], 1096, N)
+    d, w, t = w8_device(c8)
+    X, W, off = c16["X"].to(DEV), c16["W"].to(DEV), t["offsets"]
+    Y = [torch.zeros(rows, n, dtype=torch.bfloat16, device=DEV) for n in (N, N, N // 2)]
+
+    def step():
+        L.w4a8_moe_gemm_w8a8(t["Xq"], t["sx"], t["gather"], 3, off, E, rows, w.blob, w.stride, d, Y[0])
+        L.w4a8_moe_gemm_w16a16(X, None, 1, off, W, Y[1])
+        L.w4a8_moe_gemm_silu_w16a16(X, None, 1, off, W, Y[2])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for counts in ([rows, 0, 0, 0, 0], [300, 129, 70, 1800, 101], [0, 16, 33, 64, 2000], [480] * 5):
+        off.copy_(torch.from_numpy(offsets_of(counts)))
+        for y in Y:
+            y.fill_(SENTINEL)
+        step()
+        torch.cuda.synchronize()
+        want = [y.clone() for y in Y]
+        for y in Y:
+            y.fill_(SENTINEL)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(Y, want))
+        assert all((y[sum(counts):] == SENTINEL).all() for y in Y)
