@@ -388,12 +388,11 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
                     y[3] = (float(acc[n][m][3]) * sw[n].w) * rs;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = PAIR ? silu_gate(acc[n][m][i]) * acc[n + (PAIR ? 2 : 0)][m][i] : acc[n][m][i];
-                        y[i] = rs == 0.0f ? 0.0f : v;
-                    }
+                    for (int i = 0; i < 4; ++i) y[i] = PAIR ? silu_gate(acc[n][m][i]) * acc[n + (PAIR ? 2 : 0)][m][i] : acc[n][m][i];
                 }
             };
+            // 16 bit: the outputs of a gather entry that names no row
+            auto none = [&](const float rs) __attribute__((always_inline)) { return FMT != GF_I8 && rs == 0.0f; };
             // stores of 16 bytes that exist whole or not at all: one each, dropped by the descriptor where they do not
             const bool regular = near_rows && ((a.N & quantum) == 0 || (cur.w + 1) * COLS <= a.N);
             const unsigned es = f32 ? 4u : 2u, pitch = unsigned(a.ldy) * es;
@@ -402,34 +401,51 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
             unsigned coff[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) coff[n] = col[n] < a.N ? unsigned(col[n]) * es : 0x80000000u;
+            float rs[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int row = wm * (TILE / 2) + m * 16 + c16;
-                const float rs = rowscale[buf][row];
-                float y[NT][4];
+            for (int m = 0; m < MT; ++m) rs[m] = rowscale[buf][wm * (TILE / 2) + m * 16 + c16];
+            if (!regular) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) value(n, m, rs, y[n]);
-                if (!regular) {
+                for (int m = 0; m < MT; ++m) {
+                    const int row = wm * (TILE / 2) + m * 16 + c16;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n) {
+                        float y[4];
+                        value(n, m, rs[m], y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = none(rs[m]) ? 0.0f : y[i];
                         if (row < cur.z && col[n] < a.N)
-                            grouped_store(a, size_t(cur.y + row) * a.ldy + col[n], min(4, a.N - col[n]), y[n][0], y[n][1], y[n][2],
-                                          y[n][3]);
-                } else if (f32) {
+                            grouped_store(a, size_t(cur.y + row) * a.ldy + col[n], min(4, a.N - col[n]), y[0], y[1], y[2], y[3]);
+                    }
+                }
+            } else if (f32) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v4f{y[n][0], y[n][1], y[n][2], y[n][3]}), yr,
-                                                               unsigned(row) * pitch + coff[n], 0, 0);
-                } else {
+                for (int m = 0; m < MT; ++m) {
+                    const unsigned at = unsigned(wm * (TILE / 2) + m * 16 + c16) * pitch;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float y[4];
+                        value(n, m, rs[m], y);
+                        const v4i h = __builtin_bit_cast(v4i, v4f{y[0], y[1], y[2], y[3]});
+                        __builtin_amdgcn_raw_buffer_store_b128(none(rs[m]) ? v4i{0, 0, 0, 0} : h, yr, at + coff[n], 0, 0);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const unsigned at = unsigned(wm * (TILE / 2) + m * 16 + c16) * pitch;
 #pragma unroll
                     for (int n = 0; n < NT; n += 2) {
+                        float y[2][4];
+                        value(n, m, rs[m], y[0]);
+                        value(n + 1, m, rs[m], y[1]);
                         v4i h;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float lo = y[n + (i >> 1)][2 * (i & 1)], hi = y[n + (i >> 1)][2 * (i & 1) + 1];
+                            const float lo = y[i >> 1][2 * (i & 1)], hi = y[i >> 1][2 * (i & 1) + 1];
                             h[i] = int(FMT == GF_F16 ? f32_to_f16_pair(lo, hi) : f32_to_bf16_pair(lo, hi));
                         }
-                        __builtin_amdgcn_raw_buffer_store_b128(h, yr, unsigned(row) * pitch + coff[n], 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(none(rs[m]) ? v4i{0, 0, 0, 0} : h, yr, at + coff[n], 0, 0);
                     }
                 }
             }
