@@ -151,18 +151,6 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
         __syncthreads();
     };
 
-    // Where K ends inside the last step the chunks behind it receive other bytes of the tile's rows, or what a read past
-    // the end of a descriptor gives: they are set to zero in LDS once that step's copies have landed, in both operands,
-    // so that an infinity or a NaN there meets nothing.
-    const bool ragged = FMT != GF_I8 && a.kb % GT_STEP != 0;
-    auto clear_tail = [&](lds_ptr st) __attribute__((always_inline)) {
-        const int row = opaque(int(threadIdx.x));
-#pragma unroll 1
-        for (int c = (a.kb % GT_STEP) >> 4; c < 8; ++c)
-            *(LDS v4i*)(st + row * GT_STEP + (c ^ row_swizzle(row)) * 16) = v4i{0, 0, 0, 0};
-        lds_barrier();
-    };
-
     // Sources of this thread's copies, 4 of the 4 NW groups of 8 activation rows and as many of the weights, as byte offsets
     // from bases that are uniform over the workgroup; each descriptor ends where the tile's data does.  Rows past the
     // tile's last, weight rows past the last column and bytes past the last row's K lie outside it and load nothing.
@@ -174,12 +162,21 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
     // lines that they all need, each then fetches a part ahead of the others, and a DRAM page is asked for four
     // neighbouring lines at a time.
     int turn = 0;
-    const int whole_fours = (a.kb / GT_STEP) & ~3;
+    const int whole = a.kb / GT_STEP, whole_fours = whole & ~3;
+    const unsigned own_chunk = unsigned(((lane & 7) ^ row_swizzle(wave * 8 + (lane >> 3))) * 16);   // of a row's 128 bytes, in every copy
     auto fill_part = [&](lds_ptr st, const int s0, const int part) __attribute__((always_inline)) {
         const int s = s0 < whole_fours ? (s0 & ~3) | ((s0 + turn) & 3) : s0, i = part >> 1;
         const unsigned wstep = unsigned(s) * (FMT == GF_I8 ? 2048u : GT_STEP);
-        if (part & 1) copy_to_lds(wr[PAIR ? i >> 1 : 0], woff + (wstep + (PAIR ? i & 1 : i) * wgroup), st + GT_WOFF + (i * NW + wave) * 1024);
-        else copy_to_lds(xr, xoff[i] + unsigned(s) * GT_STEP, st + (i * NW + wave) * 1024);
+        // chunks behind K: out of every range, which leaves zeros in LDS, in both operands, so that an infinity or a NaN there
+        // meets nothing
+        const bool in = s0 < whole || (FMT != GF_I8 && unsigned(s) * GT_STEP + own_chunk < unsigned(a.kb));
+        if (part & 1) {
+            const unsigned off = woff + (wstep + (PAIR ? i & 1 : i) * wgroup);
+            copy_to_lds(wr[PAIR ? i >> 1 : 0], in ? off : 0xfffffff0u, st + GT_WOFF + (i * NW + wave) * 1024);
+        } else {
+            const unsigned off = xoff[i] + unsigned(s) * GT_STEP;
+            copy_to_lds(xr, in ? off : 0xfffffff0u, st + (i * NW + wave) * 1024);
+        }
     };
     constexpr int FILL = 8;                                     // copies of a wave in one fill
 
@@ -190,18 +187,6 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
 #pragma unroll
         for (int part = 0; part < FILL; ++part) fill_part(st, s, part);
     };
-    auto pad = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
-        if (s < 2 * turns) {
-            const int tid = opaque(int(threadIdx.x));
-#pragma unroll 1
-            for (int c = 0; c < GT_STAGE / (THREADS * 16); ++c) *(LDS v4i*)(st + (c * THREADS + tid) * 16) = v4i{0, 0, 0, 0};
-        }
-    };
-    auto supply = [&](lds_ptr st, const int s) __attribute__((always_inline)) {
-        if (s < steps) fill(st, s);
-        else pad(st, s);
-    };
-
     // Gather entries of a tile's rows, copied to LDS a tile ahead.
     auto request_rows = [&](const int4 g) __attribute__((always_inline)) {
         if (a.gather && wave < GT_M / 64)
@@ -250,8 +235,8 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
             const int col = (PAIR ? (wave >> 2) * 32 : 0) + tile_column(f32, n, row & 15);
             woff = unsigned(opaque(int(unsigned(col) * a.ldw))) + unsigned((lane & 7) ^ row_swizzle(row)) * 16u;
         }
-        supply(st0, 0);
-        supply(st1, 1);
+        fill(st0, 0);
+        fill(st1, 1);
     };
 
     // Operands of half h (64 bytes of K) of a stage: the 4 weight tiles, and half of the row tiles.  Lane group q takes chunk
@@ -296,7 +281,6 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
         if (behind_stores) stage_barrier<FILL + STORES>();
         else stage_barrier<0>();
         if (threadIdx.x < GT_M) rowscale[buf][threadIdx.x] = own_scale;
-        if (ragged && steps == 1) clear_tail(st0);
         // the next tile, and its gather entries: requested here, first needed at the end of this tile
         if (++k < mine) {
             if (k % GT_LIST == 0) look_up(k);
@@ -341,8 +325,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
                 }
                 if (early) stage_barrier<STORES>();
                 else stage_barrier<0>();
-                if (ragged && s + 2 == steps) clear_tail(next);
-                const bool more = s + 2 < steps;
+                const bool more = s + 2 < 2 * turns;
 #pragma unroll
                 for (int m = 0; m < H; ++m) {
 #pragma unroll
@@ -354,7 +337,6 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
                     }
                     mfma4(wb, xb[m], H + m);
                 }
-                if (!more) pad(st, s + 2);
             };
 #pragma unroll
             for (int n = 0; n < 4; ++n) wa[n] = read_w(st0, 0, n);
@@ -455,9 +437,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
             for (int s = 0; s < 2 * turns; ++s) {
                 if (s == 0 && behind_stores) stage_barrier<STORES>();
                 else stage_barrier<0>();
-                if (ragged && s + 2 == steps) clear_tail(s & 1 ? st0 : st1);
-                if (s & 1) supply(st1, s + 2);
-                else supply(st0, s + 2);
+                if (s + 2 < 2 * turns) fill(s & 1 ? st1 : st0, s + 2);
             }
             lds_barrier();
             if (k == mine) break;
