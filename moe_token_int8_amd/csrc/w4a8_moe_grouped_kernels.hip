@@ -279,7 +279,7 @@ static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s
 // Whether one launch of 32-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
 // estimates, in us, use what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates
 // fitted to some 200 measured calls: 512 workgroups at a time take 1.5 to 3 us for a 32 x 64 tile, by its rows, and a
-// nanosecond for 30 (16 bit) or 36 bytes of its operands, all of them together 5 TB/s of weights; the 16-row class reads 6
+// nanosecond for 30 (16 bit) or 36 bytes of its operands, all of them together 5.6 TB/s of weights; the 16-row class reads 6.7
 // TB/s; the launches by class cost 13 us beside that and the MFMA tiles with many or few rows, else 20.  Examples (one launch / by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 38 / 82 us; 205
 // x 4 of 6, K = 2432, N = 897 in 8 bits: 19 / 43; 2814 x 5 of 68, K = 744, I = 19: 15 / 36; 6288 x 2 of 134, K = 3176,
 // N = 739: 329 / 223; 2913 x 7 of 40, K = 384, N = 413 in 8 bits: 37 / 28; 33 x 6 of 64, K = 4096, I = 1408: 261 / 219.
@@ -288,10 +288,10 @@ static bool one_launch(const GroupedArgs& a, bool i8, bool pair) {
     const double experts = std::min(E, rows), weights = experts * width * kb;
     const double items = (std::floor(rows / 32) + experts) * std::ceil(width / 64);
     const double item = 1.5 + 1.5 * std::min(1.0, avg / 32) + (64 + std::min(32.0, avg)) * kb / (i8 ? 36e3 : 30e3);
-    const double one = 6 + std::max(std::max(1.0, items / 512) * item, weights / 5e6);
+    const double one = 6 + std::max(std::max(1.0, items / 512) * item, weights / 5.6e6);
     const double split = (avg >= 128 ? 13 : rows <= 64 ? 13 : 20) +
                          (rows > 64 ? choose_tiles(a, i8, pair).us * std::min(1.0, avg / 32) : 0.0) +
-                         weights / 6e6 * std::max(0.0, 1 - avg / 128);
+                         weights / 6.7e6 * std::max(0.0, 1 - avg / 128);
     return one < split;
 }
 

@@ -450,9 +450,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
 // Which tiles a call takes, and about how long they take, in us.  The host knows rows and E: an expert with more than 64
 // rows ends in a tile that is filled by half on average, and such experts are no more than rows / (65 + rows / E).  A round
 // of 256 large tiles takes 9.7 us and 1.6 us for 128 bytes of K, a round of 512 small ones 8 and 1.0 (with one workgroup a
-// compute unit 0.85, in 8 bits 0.55).  Measured, small / large: 8192 tokens x 6 of 64 experts, K = 1408, N = 4096: 720 /
-// 620 us; in 8 bits, K = 4096, N = 2816: 671 / 579; 4837 x 8 of 220, K = 768, N = 512: 92 / 86; 556 x 8 of 111, K = 1336,
-// I = 1786: 296 / 315; 787 x 5 of 6, K = 3200, N = 632 in 8 bits: 31 / 48; 4346 x 3 of 19, K = 2984, N = 256: 61 / 101.
+// compute unit 0.85, in 8 bits 0.55).  Measured, small / large: 8192 tokens x 6 of 64 experts, K = 1408, N = 4096: 683 /
+// 588 us; in 8 bits, K = 4096, N = 2816: 672 / 570; 4837 x 8 of 220, K = 768, N = 512: 88 / 80; 556 x 8 of 111, K = 1336,
+// I = 1786: 296 / 308; 787 x 5 of 6, K = 3200, N = 632 in 8 bits: 31 / 48; 4346 x 3 of 19, K = 2984, N = 256: 55 / 90.
 TileChoice choose_tiles(const GroupedArgs& a, bool i8, bool pair) {
     const double rows = a.rows, steps = (a.kb + GT_STEP - 1) / GT_STEP, width = pair ? 2.0 * a.N : a.N;
     const double ends = 0.5 * std::min(double(a.E), rows / (65 + rows / a.E));
