@@ -493,7 +493,9 @@ int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, const float* b
  * the sum exact in int32, then float32, then rounded to nearest even for bfloat16.
  *   d   weight_bits = 8, group_size = K, float32 scales, K < 133144; other formats EUNSUPPORTED
  * Rows at or past expert_offsets[E] are not written.  Other arguments, bounds and errors as
- * w4a8_moe_gemm; additionally E <= 1024 (EINVAL) and EUNSUPPORTED for N > 2^20 or rows > 2^24. */
+ * w4a8_moe_gemm; additionally E <= 1024 (EINVAL) and EUNSUPPORTED for N > 2^20 or rows > 2^24.  k
+ * also tells, with or without a gather, that no expert should have more than rows / k rows: the
+ * launches are chosen by it, and the result is the same whatever it is (1 if unknown). */
 int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather, int k,
                        const int32_t* expert_offsets, int E, int rows, int src_rows,
                        const void* blobs_dev, size_t expert_stride, const w4a8_wdesc* d, void* Y,
@@ -506,7 +508,7 @@ int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather,
  *   W         device, same type, [E, N, K]: output channels by inputs, K contiguous, row stride ldw
  *             and expert stride expert_stride, both in elements
  *   Y         device [rows, N], row stride ldy; out_dtype is dtype or W4A8_F32
- *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm
+ *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm_w8a8
  * K, ldx, ldw and expert_stride are multiples of 8, X and W 16-byte aligned (EINVAL); any N.  Rows
  * at or past expert_offsets[E] are not written, nor is Y past column N.  A gather entry that
  * names no row of X gives a row of zeros.  E <= 1024 (EINVAL).  EUNSUPPORTED: N > 2^20, ldw > 2^23,

@@ -276,50 +276,71 @@ static void launch_stream_t(const GroupedArgs& a, long long slots, hipStream_t s
     moe_grouped_stream_kernel<FMT, PAIR, MS, CT, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
-// Whether one launch of 32-row streaming tiles over every expert beats the launches by row class and the MFMA tiles.  The
-// estimates, in us, use what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates
-// fitted to some 200 measured calls: 512 workgroups at a time take 1.5 to 3 us for a 32 x 64 tile, by its rows, and a
-// nanosecond for 30 (16 bit) or 36 bytes of its operands, all of them together 5.6 TB/s of weights; the 16-row class reads 6.7
-// TB/s; the launches by class cost 13 us beside that and the MFMA tiles with many or few rows, else 20.  Examples (one launch / by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 38 / 82 us; 205
-// x 4 of 6, K = 2432, N = 897 in 8 bits: 19 / 43; 2814 x 5 of 68, K = 744, I = 19: 15 / 36; 6288 x 2 of 134, K = 3176,
-// N = 739: 329 / 223; 2913 x 7 of 40, K = 384, N = 413 in 8 bits: 37 / 28; 33 x 6 of 64, K = 4096, I = 1408: 261 / 219.
+// Rows that an expert has at most in a call whose tokens go to k different experts each (k as the gather has it; without a
+// sensible k, all rows).  The launches are chosen by it; experts with more rows, of calls that name an expert twice for a
+// token, are handled all the same.
+static long long usual_most(const GroupedArgs& a) {
+    return a.topk >= 1 && a.topk <= a.E ? (a.rows + a.topk - 1) / a.topk : a.rows;
+}
+
+// Whether one launch of 32-row streaming tiles over every expert beats the launches by row class.  The estimates, in us, use
+// what the host knows (an upper bound of the tiles; rows / E for the rows of an expert) and rates fitted to some 300
+// measured calls: 512 workgroups at a time take 1.5 to 3 us for a 32 x 64 tile, by its rows, and a nanosecond for 30 (16
+// bit) or 36 bytes of its operands, all of them together 5.6 TB/s of weights; the 16-row class reads 6.7 TB/s, and its
+// workgroups, some 768 at a time, take 1.9 us and 1 for 585 bytes of K; a launch costs 5 or 6; few tokens name 0.6 of the
+// experts that they could.  Examples (one launch / by class): 330 tokens x 4 of 72 experts, K = 1240, I = 370: 38 / 82 us;
+// 205 x 4 of 6, K = 2432, N = 897 in 8 bits: 19 / 43; 2814 x 5 of 68, K = 744, I = 19: 15 / 36; 9 x 8 of 72, K = 232,
+// I = 1683: 24 / 35; 10 x 7 of 241, K = 816, I = 1764: 35 / 54; 6288 x 2 of 134, K = 3176, N = 739: 329 / 223; 2913 x 7 of
+// 40, K = 384, N = 413 in 8 bits: 37 / 28; 33 x 6 of 64, K = 4096, I = 1408: 261 / 214.
 static bool one_launch(const GroupedArgs& a, bool i8, bool pair) {
     const double rows = a.rows, E = a.E, avg = rows / E, kb = a.kb, width = pair ? 2.0 * a.N : a.N;
-    const double experts = std::min(E, rows), weights = experts * width * kb;
+    const double most = double(usual_most(a)), experts = std::min(E, rows);
+    const double weights = experts * width * kb * (most <= 64 ? 0.6 : 1.0);
     const double items = (std::floor(rows / 32) + experts) * std::ceil(width / 64);
     const double item = 1.5 + 1.5 * std::min(1.0, avg / 32) + (64 + std::min(32.0, avg)) * kb / (i8 ? 36e3 : 30e3);
-    const double one = 6 + std::max(std::max(1.0, items / 512) * item, weights / 5.6e6);
-    const double split = (avg >= 128 ? 13 : rows <= 64 ? 13 : 20) +
-                         (rows > 64 ? choose_tiles(a, i8, pair).us * std::min(1.0, avg / 32) : 0.0) +
-                         weights / 6.7e6 * std::max(0.0, 1 - avg / 128);
+    const double tiles32 = std::max(1.0, items / 512) * item;
+    const double one = 6 + std::max(tiles32, weights / 5.6e6);
+    double split;
+    if (most <= 64) {
+        const double wgs = pair ? experts * std::ceil(a.N / 16.0) : experts * std::ceil(a.N / (experts * a.N / 64 < 1024 ? 32.0 : 64.0));
+        const double small = std::max(weights / 6.7e6, wgs / 768 * (1.9 + kb / 585));
+        const double more = most <= 16 ? 0.0 : std::min(1.0, avg / 32);     // of the work in experts with more than 16 rows
+        split = (most <= 16 ? 6 : 11) + small * (1 - more) + tiles32 * more;
+    } else {
+        split = (avg >= 128 ? 13 : 20) + choose_tiles(a, i8, pair).us * std::min(1.0, avg / 32) +
+                weights / 6.7e6 * std::max(0.0, 1 - avg / 128);
+    }
     return one < split;
 }
 
-// Row classes, one launch each: up to 16 rows, up to 64 (tiles of 32) and the MFMA tiles; classes that no expert can be in
-// are left out.  `slots` bounds the row tiles of a class.  Where experts have 128 rows on average, few have less than 65:
-// those share the second launch.  Returns the kernels' names for the log.
+// Row classes, one launch each: up to 16 rows, up to 64 (tiles of 32) and the MFMA tiles.  Classes that no expert of an
+// ordinary call is in are left out, and the last one that is there takes all larger experts (33 tokens x 6 of 64: a launch
+// that finds nothing is 5 of 214 us).  `slots` bounds the row tiles of a class.  Where experts have 128 rows on average, few
+// have less than 65: those share the second launch.  Returns the kernels' names for the log.
 template <int FMT, bool PAIR>
 static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
-    const long long rows = a.rows, E = a.E;
+    const long long rows = a.rows, E = a.E, most = usual_most(a);
+    constexpr int ALL = 0x7fffffff;
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     constexpr long long REACH = 0xe0000000ll;
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
     // a launch has less than 2^32 work-items; the 16-row class has a workgroup for each of its tiles, of 16 columns or more
-    const bool wide = std::min(E, rows) * (long long)a.N >= (1ll << 27);
+    const long long slots = std::min(E, rows) + (most <= 16 ? rows / 16 : 0);
+    const bool wide = slots * (long long)a.N >= (1ll << 27);
     if (rows > 16 && (!near || wide || one_launch(a, FMT == GF_I8, PAIR))) {
-        a.lo = 1, a.hi = 0x7fffffff;
+        a.lo = 1, a.hi = ALL;
         launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);
         return "moe_grouped_stream_kernel (32-row tiles)";
     }
     const bool few_small = rows >= 128 * E;
     if (!few_small) {
-        a.lo = 1, a.hi = 17;
+        a.lo = 1, a.hi = most <= 16 ? ALL : 17;
         // non-temporal reads where the call's weights cannot be found in the 256 MiB Infinity Cache by the next one: 6.4 GB
         // of codes 1.09 -> 0.96 ms, but 69 MB 17.6 -> 19.5 us
         const bool nt = std::min(E, rows) * (long long)a.N * (PAIR ? 2 : 1) * a.kb > (256ll << 20);
         // column tiles of a workgroup: 4, or 2 where there are few workgroups to spread over the chip (a single token's 69 MB:
         // 17.5 -> 15.4 us; 64-token steps of 256 experts lose 4 %) and in the paired form (33 tokens: 240 -> 225 us)
-        const long long slots = std::min(E, rows), blocks = slots * ((a.N + 63) / 64);
+        const long long blocks = slots * ((a.N + 63) / 64);
         if constexpr (PAIR) {
             if (nt) launch_stream_t<FMT, PAIR, 1, 2, true>(a, slots, s);
             else launch_stream_t<FMT, PAIR, 1, 2, false>(a, slots, s);
@@ -328,13 +349,12 @@ static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
             else if (blocks < 1024) launch_stream_t<FMT, PAIR, 1, 2, false>(a, slots, s);
             else launch_stream_t<FMT, PAIR, 1, 4, false>(a, slots, s);
         }
+        if (most <= 16) return "moe_grouped_stream_kernel (16-row tiles)";
     }
-    if (rows > 16) {
-        a.lo = few_small ? 1 : 17, a.hi = 65;
-        launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows / a.lo), s);
-    }
-    if (rows <= 64) return "moe_grouped_stream_kernel (by rows)";
-    a.lo = 65, a.hi = 0x7fffffff;
+    a.lo = few_small ? 1 : 17, a.hi = most <= 64 ? ALL : 65;
+    launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows / a.lo), s);
+    if (most <= 64) return "moe_grouped_stream_kernel (by rows)";
+    a.lo = 65, a.hi = ALL;
     launch_grouped_tile(a, FMT, PAIR, s);
     return "moe_grouped_stream_kernel (by rows), moe_grouped_tile_kernel";
 }

@@ -240,3 +240,14 @@ def test_tiles_in_a_graph(N):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(Y, want))
         assert all((y[sum(counts):] == SENTINEL).all() for y in Y)
+
+
+@pytest.mark.parametrize("E,counts", [(8, [100]), (64, [300, 0, 16, 5, 17, 0, 33]), (512, [70, 1, 2])])
+def test_experts_named_more_than_once_by_a_token(E, counts):
+    """With k = 8 no expert of an ordinary call has more than rows / 8 rows; these have, as if tokens named one repeatedly."""
+    print("repeated", E, counts, flush=True)
+    counts = counts + [0] * (E - len(counts))
+    N = 2000 if E < 100 else 260
+    check_w8(w8_inputs(51, counts, 2048, N, src_rows=30, k=8, extra_rows=2), (torch.bfloat16,))
+    check_w16(w16_inputs(52, torch.bfloat16, counts, 2048, N, src_rows=30, k=8), (torch.bfloat16,))
+    check_silu(w16_inputs(53, torch.float16, counts, 2048, N, src_rows=30, k=8, std=0.02))
