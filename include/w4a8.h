@@ -480,7 +480,8 @@ typedef struct {
  * with weight 0, which w4a8_moe_align leaves out and w4a8_moe_combine skips (a padded token: all
  * logits -Inf).  A row with a NaN logit or rank, or
  * with a +Inf logit under softmax, has no order: it gets the ids 0..k-1 with NaN weights.
- * Scores are computed in float64, without a bias the denominator of the softmax in float32.
+ * Scores are computed in float64, without a bias the denominator of the softmax in float32; with a
+ * bias and sigmoid scores, logits below -708 may rank as -708.
  * T == 0 is a no-op.  EINVAL: E, k or score out of range, n_group not dividing E, topk_group
  * outside 1..n_group or leaving fewer than k experts, ldl < E, scale not finite, NULL or misaligned pointers;
  * EUNSUPPORTED: E > 1024, k > 64, T > 2^24. */
