@@ -461,7 +461,7 @@ def w4a8_moe_forward_sets(X, topk_ids, topk_w, sets, workspace, out, stream=None
 
 
 def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=None) -> None:
-    """Top-k routing: logits [T, E] (float32, bfloat16 or float16; rows may be strided) -> topk_ids int32 [T, k],
+    """Top-k routing: logits [T, E] (float32, bfloat16 or float16; rows may be further apart than E) -> topk_ids int32 [T, k],
     topk_w float32 [T, k]; bias: float32 [E] for the choice only."""
     t = _torch()
     dev = t.current()
@@ -471,14 +471,16 @@ def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=Non
         _require_current((logits,), int32=(topk_ids,), float32=(topk_w, bias))      # says which
     T, E = logits.shape
     ldl, step = logits.stride()
-    if E != d.E or step != 1:
-        raise ValueError("logits must be [T, E] with contiguous rows")
+    if T <= 1:
+        ldl = E                                                 # the stride of a single row says nothing
+    if E != d.E or step != 1 or ldl < E:
+        raise ValueError("logits must be [T, E] with contiguous rows that do not overlap")
     want = (T, d.k)
     if topk_ids.shape != want or topk_w.shape != want or not topk_ids.is_contiguous() or not topk_w.is_contiguous():
         raise ValueError("topk_ids and topk_w must be contiguous [T, k]")
     if bias is not None and (bias.numel() != E or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous [E]")
-    _check(lib().w4a8_moe_route(logits.data_ptr(), _dtype(logits), T, ldl if ldl > E else E,
+    _check(lib().w4a8_moe_route(logits.data_ptr(), _dtype(logits), T, ldl,
                                 None if bias is None else bias.data_ptr(), d, topk_ids.data_ptr(), topk_w.data_ptr(),
                                 t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_route")
 

@@ -1,0 +1,68 @@
+"""Argument checks of the Python calls of the router and of the 8-bit and 16-bit grouped products.  Every refusal comes before
+the library is called, so these run without a GPU: the calls see meta tensors (shapes, strides and types without storage) as
+tensors of the current device, and the library is replaced by one that records its arguments."""
+import pytest
+import torch
+
+import moe_token_int8_amd as L
+
+META = torch.empty(0, device="meta").get_device()
+
+
+class Recorder:
+    """Stands for the library: every entry point returns OK and notes its arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return L.W4A8_OK
+        return entry
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    t = L._Torch()
+    t.device, t.initialized, t.raw_stream = lambda: META, lambda: True, lambda dev: 0
+    rec = Recorder()
+    L.lib()                                                     # the real one stays loaded for the sizes of blobs
+    monkeypatch.setattr(L, "_torch_of_calls", t)
+    monkeypatch.setattr(L, "_require_current", lambda *a, **k: None)
+    monkeypatch.setattr(L, "_stream", lambda s: 0)
+    monkeypatch.setattr(L, "_packed_size", lambda d, real=L.lib(): int(real.w4a8_packed_size(d)))
+    monkeypatch.setattr(L, "lib", lambda: rec)
+    return rec.calls
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+def route(x, k=4, bias=None):
+    T, E = x.shape
+    L.w4a8_moe_route(x, L.route_desc(E, k), meta(T, k, dtype=torch.int32), meta(T, k), bias=bias)
+
+
+# ------------------------------------------------------------------------------------------- router
+@pytest.mark.parametrize("stride", [0, 1, 63])
+def test_route_rows_that_overlap(calls, stride):
+    """A row stride below E would have the kernel read E elements of every row from storage that ends before them."""
+    with pytest.raises(ValueError, match="overlap"):
+        route(torch.empty_strided((5, 64), (stride, 1), device="meta"))
+    assert not calls
+
+
+def test_route_expanded_rows(calls):
+    with pytest.raises(ValueError, match="overlap"):
+        route(meta(64).expand(5, 64))
+    assert not calls
+
+
+@pytest.mark.parametrize("T,stride,ldl", [(1, 0, 64), (1, 7, 64), (1, 640, 64), (0, 0, 64), (5, 64, 64), (5, 101, 101)])
+def test_route_row_stride(calls, T, stride, ldl):
+    """The stride of a single row says nothing; any other is handed on."""
+    route(torch.empty_strided((T, 64), (stride, 1), device="meta"))
+    (name, args), = calls
+    assert name == "w4a8_moe_route" and args[2:4] == (T, ldl)
