@@ -511,8 +511,8 @@ def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int
         raise ValueError("Xq must be a contiguous [src_rows, K] with one scale in sx for each row")
     if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < rows):
         raise ValueError("expert_offsets must hold E + 1 entries and gather one per routed row")
-    if out_dtype != (W4A8_F32 if Y.element_size() == 4 else W4A8_BF16) or Y.numel() < rows * d.N or not Y.is_contiguous():
-        raise ValueError("Y must be a contiguous [rows, N] of out_dtype")
+    if t.types.get(Y.dtype) != out_dtype or out_dtype == W4A8_F16 or Y.numel() < rows * d.N or not Y.is_contiguous():
+        raise ValueError("Y must be a contiguous [rows, N] of out_dtype, bfloat16 or float32")
     if blobs_dev.numel() * blobs_dev.element_size() < (E - 1) * expert_stride + _packed_size(d):
         raise ValueError("blobs_dev does not hold E blobs at expert_stride")
     _check(lib().w4a8_moe_gemm_w8a8(Xq.data_ptr(), sx.data_ptr(), None if gather is None else gather.data_ptr(), int(k),

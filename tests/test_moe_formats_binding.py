@@ -66,3 +66,36 @@ def test_route_row_stride(calls, T, stride, ldl):
     route(torch.empty_strided((T, 64), (stride, 1), device="meta"))
     (name, args), = calls
     assert name == "w4a8_moe_route" and args[2:4] == (T, ldl)
+
+
+# ------------------------------------------------------------------------------------------- W8A8 product
+I32, BF16, F16 = torch.int32, torch.bfloat16, torch.float16
+
+
+def w8(rows=6, K=256, N=48, E=3, k=2, gather=True, off=None, blob=None, stride=None, Y=None, out=L.W4A8_OUT_BF16):
+    d = L.desc(K, N, K, False, bits=8)
+    size = L._packed_size(d)
+    src = 4 if gather is not None else rows
+    g = meta(rows, dtype=I32) if gather is True else gather
+    L.w4a8_moe_gemm_w8a8(meta(src, K, dtype=torch.int8), meta(src), g, k, meta(E + 1, dtype=I32) if off is None else off, E, rows,
+                         meta(E, size, dtype=torch.uint8) if blob is None else blob, size if stride is None else stride, d,
+                         meta(rows, N, dtype=BF16) if Y is None else Y, out)
+
+
+@pytest.mark.parametrize("dtype,out", [
+    (F16, L.W4A8_OUT_BF16),                                     # would be filled with bfloat16 bits
+    (torch.int16, L.W4A8_OUT_BF16), (torch.int32, L.W4A8_OUT_F32),
+    (torch.uint8, L.W4A8_OUT_BF16), (torch.int8, L.W4A8_OUT_BF16),      # would be written to twice their length
+    (torch.float64, L.W4A8_OUT_BF16), (torch.float32, L.W4A8_OUT_BF16), (BF16, L.W4A8_OUT_F32), (F16, L.W4A8_F16),
+])
+def test_w8_output_type(calls, dtype, out):
+    with pytest.raises(ValueError, match="out_dtype"):
+        w8(Y=meta(6, 48, dtype=dtype), out=out)
+    assert not calls
+
+
+def test_w8_output_types_that_fit(calls):
+    w8()
+    w8(Y=meta(6, 48), out=L.W4A8_OUT_F32)
+    w8(Y=meta(7, 48, dtype=BF16))                               # longer than the rows of the call
+    assert [c[0] for c in calls] == ["w4a8_moe_gemm_w8a8"] * 3
