@@ -497,6 +497,14 @@ def _packed_size(d: WDesc) -> int:
     return size
 
 
+def _check_rows(gather, expert_offsets, E: int, rows: int) -> None:
+    """The index arrays of the grouped products: read from their first entry on, one after another."""
+    if expert_offsets.numel() != E + 1 or not expert_offsets.is_contiguous():
+        raise ValueError("expert_offsets must be a contiguous [E + 1]")
+    if gather is not None and (gather.numel() < rows or not gather.is_contiguous()):
+        raise ValueError("gather must be contiguous, with an entry for each routed row")
+
+
 def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int, blobs_dev, expert_stride: int,
                        d: WDesc, Y, out_dtype: int = W4A8_OUT_BF16, stream=None) -> None:
     """Grouped W8A8 GEMM: w4a8_moe_gemm for 8-bit blobs with one scale per output channel (group_size = K)."""
@@ -509,8 +517,7 @@ def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int
     src_rows, K = Xq.shape
     if K != d.K or not Xq.is_contiguous() or sx.numel() < src_rows or not sx.is_contiguous():
         raise ValueError("Xq must be a contiguous [src_rows, K] with one scale in sx for each row")
-    if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < rows):
-        raise ValueError("expert_offsets must hold E + 1 entries and gather one per routed row")
+    _check_rows(gather, expert_offsets, E, rows)
     if t.types.get(Y.dtype) != out_dtype or out_dtype == W4A8_F16 or Y.numel() < rows * d.N or not Y.is_contiguous():
         raise ValueError("Y must be a contiguous [rows, N] of out_dtype, bfloat16 or float32")
     if blobs_dev.numel() * blobs_dev.element_size() < (E - 1) * expert_stride + _packed_size(d):
@@ -535,8 +542,7 @@ def _w16_args(X, gather, k, expert_offsets, W, Y, width: int, stream):
         raise ValueError("X [src_rows, K], W [E, N, K] and Y do not match")
     if x1 != 1 or w1 != 1 or y1 != 1:
         raise ValueError("the last dimension of X, W and Y must be contiguous")
-    if expert_offsets.numel() != E + 1 or (gather is not None and gather.numel() < rows):
-        raise ValueError("expert_offsets must hold E + 1 entries and gather one per row of Y")
+    _check_rows(gather, expert_offsets, E, rows)
     # the stride of a dimension of one entry says nothing
     ldx, ldy = K if src_rows == 1 else ldx, I if rows == 1 else ldy
     ldw = K if N == 1 else ldw

@@ -99,3 +99,39 @@ def test_w8_output_types_that_fit(calls):
     w8(Y=meta(6, 48), out=L.W4A8_OUT_F32)
     w8(Y=meta(7, 48, dtype=BF16))                               # longer than the rows of the call
     assert [c[0] for c in calls] == ["w4a8_moe_gemm_w8a8"] * 3
+
+
+# ------------------------------------------------------------------------------------------- 16-bit products
+def w16(X=None, W=None, Y=None, rows=6, K=64, N=48, E=3, k=2, gather=True, off=None, silu=False):
+    src = 4 if gather is not None else rows
+    f = L.w4a8_moe_gemm_silu_w16a16 if silu else L.w4a8_moe_gemm_w16a16
+    f(meta(src, K, dtype=BF16) if X is None else X, meta(rows, dtype=I32) if gather is True else gather, k,
+      meta(E + 1, dtype=I32) if off is None else off, meta(E, (2 if silu else 1) * N, K, dtype=BF16) if W is None else W,
+      meta(rows, N, dtype=BF16) if Y is None else Y)
+
+
+PRODUCTS = [pytest.param(w8, id="w8a8"), pytest.param(w16, id="w16a16"),
+            pytest.param(lambda **a: w16(silu=True, **a), id="silu_w16a16")]
+
+
+@pytest.mark.parametrize("call", PRODUCTS)
+@pytest.mark.parametrize("bad", [dict(gather=meta(6, 2, dtype=I32)[:, 0]), dict(gather=meta(12, dtype=I32)[::2]),
+                                 dict(gather=meta(1, dtype=I32).expand(6)), dict(gather=meta(5, dtype=I32)),
+                                 dict(off=meta(4, 2, dtype=I32)[:, 1]), dict(off=meta(8, dtype=I32)[::2]),
+                                 dict(off=meta(1, dtype=I32).expand(4)), dict(off=meta(5, dtype=I32)),
+                                 dict(off=meta(3, dtype=I32))])
+def test_index_arrays_are_dense(calls, call, bad):
+    """The kernels read them one entry after another: a column, every other entry or an expanded one would be read as if its
+    storage were dense, and past its end."""
+    with pytest.raises(ValueError, match="contiguous"):
+        call(**bad)
+    assert not calls
+
+
+@pytest.mark.parametrize("call", PRODUCTS)
+def test_index_arrays_that_fit(calls, call):
+    call()
+    call(gather=None)
+    call(gather=meta(9, dtype=I32))                             # longer than the rows of the call
+    call(gather=meta(9, dtype=I32)[2:8], off=meta(9, dtype=I32)[5:])
+    assert len(calls) == 4
