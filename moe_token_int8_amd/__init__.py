@@ -505,6 +505,11 @@ def _check_rows(gather, expert_offsets, E: int, rows: int) -> None:
         raise ValueError("gather must be contiguous, with an entry for each routed row")
 
 
+def _check_blobs(blobs, E: int, stride: int, d: WDesc) -> None:
+    if stride < 0 or blobs.numel() * blobs.element_size() < (E - 1) * stride + _packed_size(d) or not blobs.is_contiguous():
+        raise ValueError("the packed weights must be contiguous and hold E blobs at their stride")
+
+
 def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int, blobs_dev, expert_stride: int,
                        d: WDesc, Y, out_dtype: int = W4A8_OUT_BF16, stream=None) -> None:
     """Grouped W8A8 GEMM: w4a8_moe_gemm for 8-bit blobs with one scale per output channel (group_size = K)."""
@@ -520,8 +525,7 @@ def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int
     _check_rows(gather, expert_offsets, E, rows)
     if t.types.get(Y.dtype) != out_dtype or out_dtype == W4A8_F16 or Y.numel() < rows * d.N or not Y.is_contiguous():
         raise ValueError("Y must be a contiguous [rows, N] of out_dtype, bfloat16 or float32")
-    if blobs_dev.numel() * blobs_dev.element_size() < (E - 1) * expert_stride + _packed_size(d):
-        raise ValueError("blobs_dev does not hold E blobs at expert_stride")
+    _check_blobs(blobs_dev, E, expert_stride, d)
     _check(lib().w4a8_moe_gemm_w8a8(Xq.data_ptr(), sx.data_ptr(), None if gather is None else gather.data_ptr(), int(k),
                                     expert_offsets.data_ptr(), int(E), int(rows), src_rows, blobs_dev.data_ptr(),
                                     int(expert_stride), d, Y.data_ptr(), int(out_dtype),
@@ -586,9 +590,8 @@ def w4a8_moe_forward_w8a8(X, topk_ids, topk_w, E: int, gu_blobs, gu_stride: int,
     _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
     if X.shape[1] != gu_desc.K:
         raise ValueError("X must be [T, K of the gate/up weights]")
-    for blobs, stride, d in ((gu_blobs, gu_stride, gu_desc), (d_blobs, d_stride, d_desc)):
-        if blobs.numel() * blobs.element_size() < (E - 1) * stride + _packed_size(d):
-            raise ValueError("the weights do not hold E blobs at their stride")
+    _check_blobs(gu_blobs, E, gu_stride, gu_desc)
+    _check_blobs(d_blobs, E, d_stride, d_desc)
     T, k = topk_ids.shape
     _check(lib().w4a8_moe_forward_w8a8(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, int(E), _ptr(gu_blobs), int(gu_stride),
                                        gu_desc, _ptr(d_blobs), int(d_stride), d_desc, _ptr(workspace),

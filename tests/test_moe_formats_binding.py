@@ -135,3 +135,48 @@ def test_index_arrays_that_fit(calls, call):
     call(gather=meta(9, dtype=I32))                             # longer than the rows of the call
     call(gather=meta(9, dtype=I32)[2:8], off=meta(9, dtype=I32)[5:])
     assert len(calls) == 4
+
+
+# ------------------------------------------------------------------------------------------- packed weights
+BLOB = L.w4a8_packed_size(L.desc(256, 48, 256, False, bits=8))
+
+
+def layer8(blob=None, stride=None, down=False, E=3, H=256, I=128, T=4, k=2):
+    """A layer whose gate/up (or down) weights are the given ones."""
+    gu, dn = L.desc(H, 2 * I, H, False, bits=8), L.desc(I, H, I, False, bits=8)
+    w = [[meta(E, L._packed_size(d), dtype=torch.uint8), L._packed_size(d)] for d in (gu, dn)]
+    if blob is not None:
+        w[down][0] = blob(w[down][1])
+    if stride is not None:
+        w[down][1] = stride(w[down][1])
+    L.w4a8_moe_forward_w8a8(meta(T, H, dtype=BF16), meta(T, k, dtype=I32), meta(T, k), E, w[0][0], w[0][1], gu, w[1][0], w[1][1], dn,
+                            meta(1 << 20, dtype=torch.uint8), meta(T, H, dtype=BF16))
+
+
+def product8(blob=None, stride=None):
+    w8(blob=None if blob is None else blob(BLOB), stride=None if stride is None else stride(BLOB))
+
+
+PACKED = [pytest.param(product8, id="product"), pytest.param(layer8, id="layer_gate_up"),
+          pytest.param(lambda **a: layer8(down=True, **a), id="layer_down")]
+
+
+@pytest.mark.parametrize("call", PACKED)
+@pytest.mark.parametrize("bad", [
+    dict(blob=lambda n: meta(1, n, dtype=torch.uint8).expand(3, n)),            # one blob seen as three
+    dict(blob=lambda n: meta(3, 2 * n, dtype=torch.uint8)[:, :n]), dict(blob=lambda n: meta(n, 3, dtype=torch.uint8).t()),
+    dict(blob=lambda n: meta(3 * n - 1, dtype=torch.uint8)), dict(stride=lambda n: n + 16),
+    dict(stride=lambda n: -16), dict(stride=lambda n: -n),                      # a size_t past every check of the library
+])
+def test_packed_weights_that_do_not_lie_as_said(calls, call, bad):
+    with pytest.raises(ValueError, match="packed weights"):
+        call(**bad)
+    assert not calls
+
+
+@pytest.mark.parametrize("call", PACKED)
+def test_packed_weights_that_fit(calls, call):
+    call()
+    call(blob=lambda n: meta(3, n + 256, dtype=torch.uint8), stride=lambda n: n + 256)
+    call(blob=lambda n: meta(3 * n + 5, dtype=torch.uint8))
+    assert len(calls) == 3
