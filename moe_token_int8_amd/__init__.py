@@ -193,6 +193,12 @@ def _torch() -> _Torch:
     return _torch_of_calls
 
 
+def _check_int32(*sizes) -> None:
+    """The library's int arguments: ctypes would hand on the low 32 bits of anything larger."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError("a size or a stride does not fit in 32 bits")
+
+
 def _ptr(x) -> int | None:
     """Data pointer of a torch tensor or numpy array (None passes NULL)."""
     if x is None:
@@ -475,6 +481,7 @@ def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=Non
         ldl = E                                                 # the stride of a single row says nothing
     if E != d.E or step != 1 or ldl < E:
         raise ValueError("logits must be [T, E] with contiguous rows that do not overlap")
+    _check_int32(T, ldl)
     want = (T, d.k)
     if topk_ids.shape != want or topk_w.shape != want or not topk_ids.is_contiguous() or not topk_w.is_contiguous():
         raise ValueError("topk_ids and topk_w must be contiguous [T, k]")
@@ -522,6 +529,7 @@ def w4a8_moe_gemm_w8a8(Xq, sx, gather, k: int, expert_offsets, E: int, rows: int
     src_rows, K = Xq.shape
     if K != d.K or not Xq.is_contiguous() or sx.numel() < src_rows or not sx.is_contiguous():
         raise ValueError("Xq must be a contiguous [src_rows, K] with one scale in sx for each row")
+    _check_int32(k, E, rows, src_rows)
     _check_rows(gather, expert_offsets, E, rows)
     if t.types.get(Y.dtype) != out_dtype or out_dtype == W4A8_F16 or Y.numel() < rows * d.N or not Y.is_contiguous():
         raise ValueError("Y must be a contiguous [rows, N] of out_dtype, bfloat16 or float32")
@@ -551,6 +559,7 @@ def _w16_args(X, gather, k, expert_offsets, W, Y, width: int, stream):
     ldx, ldy = K if src_rows == 1 else ldx, I if rows == 1 else ldy
     ldw = K if N == 1 else ldw
     stride = N * ldw if E == 1 else stride
+    _check_int32(ldx, k, E, rows, src_rows, ldw, K, N, ldy)
     return (X.data_ptr(), _dtype(X), ldx, None if gather is None else gather.data_ptr(), int(k), expert_offsets.data_ptr(), E,
             rows, src_rows, W.data_ptr(), stride, ldw, K, I, Y.data_ptr(), ldy), (t.raw_stream(dev) if stream is None else int(stream))
 
@@ -571,6 +580,7 @@ def w4a8_moe_gemm_silu_w16a16(X, gather, k: int, expert_offsets, W, H, stream=No
 
 
 def w4a8_moe_w16a16_workspace_size(T: int, k: int, H: int, I: int, E: int) -> int:
+    _check_int32(T, k, H, I, E)
     return int(lib().w4a8_moe_w16a16_workspace_size(T, k, H, I, E))
 
 
@@ -580,6 +590,7 @@ def _check_layer(X, topk_ids, topk_w, workspace, out, *weights) -> None:
         raise ValueError("X and out must be bfloat16 [T, H]")
     if topk_ids.shape != topk_w.shape or topk_ids.shape[0] != X.shape[0]:
         raise ValueError("topk_ids and topk_w must be [T, k]")
+    _check_int32(*X.shape, *topk_ids.shape)
     if not all(t.is_contiguous() for t in (X, topk_ids, topk_w, workspace, out)):
         raise ValueError("the layer's tensors must be contiguous")
 
@@ -590,6 +601,7 @@ def w4a8_moe_forward_w8a8(X, topk_ids, topk_w, E: int, gu_blobs, gu_stride: int,
     _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
     if X.shape[1] != gu_desc.K:
         raise ValueError("X must be [T, K of the gate/up weights]")
+    _check_int32(E)
     _check_blobs(gu_blobs, E, gu_stride, gu_desc)
     _check_blobs(d_blobs, E, d_stride, d_desc)
     T, k = topk_ids.shape
@@ -606,6 +618,7 @@ def w4a8_moe_forward_w16a16(X, topk_ids, topk_w, Wgu, Wd, workspace, out, stream
     E, I2, H = Wgu.shape
     if Wd.shape != (E, H, I2 // 2) or X.shape[1] != H or I2 % 2 or Wgu.dtype != X.dtype or Wd.dtype != X.dtype:
         raise ValueError("Wgu [E, 2I, H] and Wd [E, H, I] must be bfloat16 and match X")
+    _check_int32(E, I2)
     if E == 0 or not Wgu[0].is_contiguous() or not Wd[0].is_contiguous():
         raise ValueError("each expert's weights must be dense")
     T, k = topk_ids.shape

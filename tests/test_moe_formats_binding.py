@@ -180,3 +180,40 @@ def test_packed_weights_that_fit(calls, call):
     call(blob=lambda n: meta(3, n + 256, dtype=torch.uint8), stride=lambda n: n + 256)
     call(blob=lambda n: meta(3 * n + 5, dtype=torch.uint8))
     assert len(calls) == 3
+
+
+# ------------------------------------------------------------------------------------------- sizes past 32 bits
+BIG = 1 << 32                                                   # each of these would arrive as a small number
+
+
+def strided(rows, width, stride, dtype=BF16):
+    return torch.empty_strided((rows, width), (stride, 1), dtype=dtype, device="meta")
+
+
+def layer16(T=4, k=2, E=3, H=64, I=24):
+    L.w4a8_moe_forward_w16a16(meta(T, H, dtype=BF16), meta(T, k, dtype=I32), meta(T, k), meta(E, 2 * I, H, dtype=BF16),
+                              meta(E, H, I, dtype=BF16), meta(1 << 20, dtype=torch.uint8), meta(T, H, dtype=BF16))
+
+
+@pytest.mark.parametrize("call", [
+    lambda: route(strided(5, 64, BIG + 64, torch.float32)), lambda: route(meta(BIG + 1, 4), k=1),
+    lambda: w8(k=BIG + 2), lambda: w8(rows=BIG + 6), lambda: w8(E=BIG + 3, blob=meta(1 << 45, dtype=torch.uint8)),
+    lambda: w16(X=strided(4, 64, BIG + 64)), lambda: w16(Y=strided(6, 48, BIG + 48)), lambda: w16(k=BIG + 2),
+    lambda: w16(W=torch.empty_strided((3, 48, 64), (48 * (BIG + 64), BIG + 64, 1), dtype=BF16, device="meta")),
+    lambda: w16(X=meta(BIG + 4, 64, dtype=BF16)), lambda: w16(rows=BIG + 6),
+    lambda: w16(silu=True, Y=strided(6, 48, BIG + 48)), lambda: layer8(T=BIG + 4), lambda: layer8(E=BIG + 3),
+    lambda: layer16(T=BIG + 4), lambda: layer16(E=BIG + 3), lambda: layer16(I=BIG + 24),
+    lambda: L.w4a8_moe_w16a16_workspace_size(BIG + 4, 2, 64, 24, 3),
+])
+def test_sizes_past_32_bits(calls, call):
+    with pytest.raises(ValueError, match="32 bits"):
+        call()
+    assert not calls
+
+
+def test_largest_strides(calls):
+    route(strided(5, 64, (1 << 31) - 1, torch.float32))
+    w16(X=strided(4, 64, (1 << 31) - 8), Y=strided(6, 48, (1 << 31) - 1))
+    layer16()
+    layer8()
+    assert len(calls) == 4
