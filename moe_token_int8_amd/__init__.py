@@ -479,7 +479,7 @@ def w4a8_moe_route(logits, d: RouteDesc, topk_ids, topk_w, bias=None, stream=Non
     ldl, step = logits.stride()
     if T <= 1:
         ldl = E                                                 # the stride of a single row says nothing
-    if E != d.E or step != 1 or ldl < E:
+    if E != d.E or (step != 1 and E > 1) or ldl < E:
         raise ValueError("logits must be [T, E] with contiguous rows that do not overlap")
     _check_int32(T, ldl)
     want = (T, d.k)
@@ -552,7 +552,7 @@ def _w16_args(X, gather, k, expert_offsets, W, Y, width: int, stream):
     (stride, ldw, w1), (ldx, x1), (ldy, y1) = W.stride(), X.stride(), Y.stride()
     if X.dtype is not W.dtype or Kx != K or N != width * I:
         raise ValueError("X [src_rows, K], W [E, N, K] and Y do not match")
-    if x1 != 1 or w1 != 1 or y1 != 1:
+    if x1 != 1 or w1 != 1 or (y1 != 1 and I > 1):
         raise ValueError("the last dimension of X, W and Y must be contiguous")
     _check_rows(gather, expert_offsets, E, rows)
     # the stride of a dimension of one entry says nothing

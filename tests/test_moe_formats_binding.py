@@ -217,3 +217,22 @@ def test_largest_strides(calls):
     layer16()
     layer8()
     assert len(calls) == 4
+
+
+# ------------------------------------------------------------------------------------------- single columns
+def test_single_columns_with_any_stride(calls):
+    """One expert, one output column: the step to a next one says nothing, as in torch's own idea of contiguous."""
+    route(meta(1, 5).t(), k=1)
+    assert calls[-1][1][2:4] == (5, 1)
+    w16(N=1, Y=meta(1, 6, dtype=BF16).t())
+    assert calls[-1][1][14:16] == (0, 1)
+    w16(N=1, silu=True, Y=torch.empty_strided((6, 1), (9, 7), dtype=BF16, device="meta"))
+    assert calls[-1][1][14:16] == (0, 9)
+
+
+@pytest.mark.parametrize("call", [lambda: route(meta(64, 5).t()), lambda: w16(Y=meta(48, 6, dtype=BF16).t()),
+                                  lambda: w16(X=meta(64, 4, dtype=BF16).t())])
+def test_columns_that_are_not_next_to_each_other(calls, call):
+    with pytest.raises(ValueError, match="contiguous"):
+        call()
+    assert not calls
