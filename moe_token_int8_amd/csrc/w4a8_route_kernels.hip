@@ -237,9 +237,10 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const double r = p[j] + double(bias[j]);
-            bad |= r != r;
+            const bool masked = x[j] == -__builtin_huge_valf();
+            bad |= !masked && r != r;                           // the bias of a masked expert is never looked at
             // an infinite bias stays a number
-            key[j] = route_mask(route_key(fmin(r, 1e300), e0 + j), x[j] == -__builtin_huge_valf() || r < -1e39);
+            key[j] = route_mask(route_key(fmin(r, 1e300), e0 + j), masked || r < -1e39);
         }
     } else {
         if (!a.sigmoid) {
