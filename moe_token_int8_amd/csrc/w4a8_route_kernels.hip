@@ -284,7 +284,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
         if (gshift > 4) merge(route_across<4>(b1), route_across<4>(b2));
         double score = ROUTE_NONE;
         if (b1 > -1e300 && group < a.groups)
-            score = route_key(a.bias && b2 > -1e300 ? route_value(b1) + route_value(b2) : route_value(b1), group);
+            score = route_key(fmin(a.bias && b2 > -1e300 ? route_value(b1) + route_value(b2) : route_value(b1), 1e300), group);
         bool kept = false;
         for (int r = 0; r < a.keep; ++r) {
             const double best = route_all<LANES>(score, max64);

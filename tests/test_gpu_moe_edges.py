@@ -40,3 +40,20 @@ def test_nan_bias_of_a_masked_expert(E, groups, keep, score):
     check(x.to(DEV), bias.to(DEV), 6, score, renorm=True, groups=groups, keep=keep)
     ids, w = call(x.to(DEV), bias.to(DEV), 6, score, groups=groups, keep=keep)
     assert (ids[1] == -1).all() and (w[1] == 0).all() and torch.isfinite(w[[0, 1, 2]]).all() and torch.isnan(w[3:]).all()
+
+
+@pytest.mark.parametrize("E,groups,keep", [(64, 4, 1), (64, 4, 2), (1024, 2, 1), (200, 100, 1), (200, 100, 30)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases_of_groups(E, groups, keep, score):
+    """A group with one +Inf bias and a later one with two both have the score +Inf: equal, so the lower index goes first."""
+    print("infinite bias", E, groups, keep, score, flush=True)
+    size = E // groups
+    x = torch.randn(4, E, generator=torch.Generator().manual_seed(E + keep))
+    bias = torch.zeros(E)
+    last = (groups - 1) * size
+    bias[last - size + 1], bias[last], bias[last + 1] = INF, INF, INF
+    x[2, last - size + 1] = -INF                                # masked: the bias does not bring it back
+    k = min(6, keep * size)
+    check(x.to(DEV), bias.to(DEV), k, score, groups=groups, keep=keep)
+    ids, _ = call(x.to(DEV), bias.to(DEV), k, score, groups=groups, keep=keep)
+    assert ids[:, 0].tolist() == [last - size + 1] * 2 + [last] + [last - size + 1]
