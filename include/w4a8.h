@@ -474,8 +474,8 @@ typedef struct {
  *   bias      device float32 [E] or NULL: an offset used for the choice only, not for the weights
  *   topk_ids  device int32 [T, k], best first; topk_w device float32 [T, k]
  * Experts are ranked by their logit, or by p_i + bias_i in float64 if a bias is given, of which 42
- * bits of the mantissa count; a group by its best expert, or with a bias by the sum of its two best.
- * Equal ranks go to the lower index.  An expert whose logit (or bias) is -Inf is masked: never chosen;
+ * bits of the mantissa count; a group by its best expert, or with a bias by the sum of its two best
+ * ranks, of which again 42 bits count.  Equal ranks go to the lower index.  An expert whose logit (or bias) is -Inf is masked: never chosen;
  * a -Inf logit also has p_i = 0.  Where fewer than k can be chosen, the remaining entries are id -1
  * with weight 0, which w4a8_moe_align leaves out and w4a8_moe_combine skips (a padded token: all
  * logits -Inf).  A row with a NaN logit or rank, or

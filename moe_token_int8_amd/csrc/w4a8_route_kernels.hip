@@ -79,7 +79,7 @@ __device__ __forceinline__ float exp_neg32(float a) {
 
 // A rank as a sorting key: the float64 value with its last 10 mantissa bits replaced by the index, turned so that of two
 // equal values the lower index is the larger key (of a negative value the larger mantissa is the smaller number).  One
-// v_max_f64 then compares value and index.  Logits are float32 and lose nothing; p + bias keeps 42 bits.
+// v_max_f64 then compares value and index.  Logits are float32 and lose nothing; p + bias, and the sum of two of them that ranks a group, keep 42 bits.
 constexpr double ROUTE_NONE = -1.7e308;                         // a masked or taken expert; ranks are above -1e39
 
 __device__ __forceinline__ double route_key(double v, int index) {
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_any_groups_kernel(
                     if (r > b1) b2 = b1, b1 = r;
                     else if (r > b2) b2 = r;
                 }
-            best[i] = a.bias && b2 != NEG ? b1 + b2 : b1;
+            best[i] = a.bias && b2 != NEG ? route_value(b1 + b2) : b1;
         }
         for (int r = 0; r < a.keep; ++r) {
             double m = NEG;

@@ -57,3 +57,20 @@ def test_infinite_biases_of_groups(E, groups, keep, score):
     check(x.to(DEV), bias.to(DEV), k, score, groups=groups, keep=keep)
     ids, _ = call(x.to(DEV), bias.to(DEV), k, score, groups=groups, keep=keep)
     assert ids[:, 0].tolist() == [last - size + 1] * 2 + [last] + [last - size + 1]
+
+
+@pytest.mark.parametrize("E,groups", [(64, 4), (256, 8), (512, 4), (200, 100), (1020, 3)])
+def test_group_scores_count_42_bits(E, groups):
+    """Ranks 1000 + p of two groups, all truncated to a multiple of 2^-33 (1000 has 10 bits before the point): p(-40) = 4e-18
+    counts as nothing and p(-22.5) = 1.69e-10 as 2^-33.  The sums 2000 and 2000 + 2^-33 are equal once 42 bits of them count
+    (a step of 2^-32), so the lower group goes first; one step more, p(-21) = 7.6e-10 = 6 2^-33, tells them apart."""
+    size, low, high = E // groups, 1, groups - 1
+    x = torch.zeros(2, E)
+    bias = torch.zeros(E)
+    for g in (low, high):
+        x[:, g * size:(g + 1) * size] = -40.0
+        bias[g * size:g * size + 2] = 1000.0
+    x[0, high * size], x[1, high * size] = -22.5, -21.0
+    ids, _ = call(x.to(DEV), bias.to(DEV), 2, "sigmoid", groups=groups, keep=1)
+    assert ids[0].tolist() == [low * size, low * size + 1]
+    assert ids[1].tolist() == [high * size, high * size + 1]
