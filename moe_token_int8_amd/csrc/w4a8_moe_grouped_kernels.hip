@@ -324,9 +324,10 @@ static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
     // the MFMA-tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     constexpr long long REACH = 0xe0000000ll;
     const bool near = a.ldx <= (1 << 23) && a.kb <= (1 << 23) && (!a.gather || (long long)a.src_rows * a.ldx < REACH);
-    // a launch has less than 2^32 work-items; the 16-row class has a workgroup for each of its tiles, of 16 columns or more
+    // a launch has less than 2^32 work-items; the 16-row class has a workgroup of 512 for each of its tiles, of 16 columns or
+    // more (1024 experts of 131071 columns: 8192 tiles each, the last one short of a column, are 2^32)
     const long long slots = std::min(E, rows) + (most <= 16 ? rows / 16 : 0);
-    const bool wide = slots * (long long)a.N >= (1ll << 27);
+    const bool wide = slots * ((a.N + 15) / 16) >= (1ll << 23);
     if (rows > 16 && (!near || wide || one_launch(a, FMT == GF_I8, PAIR))) {
         a.lo = 1, a.hi = ALL;
         launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);

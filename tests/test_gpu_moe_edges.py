@@ -74,3 +74,31 @@ def test_group_scores_count_42_bits(E, groups):
     ids, _ = call(x.to(DEV), bias.to(DEV), 2, "sigmoid", groups=groups, keep=1)
     assert ids[0].tolist() == [low * size, low * size + 1]
     assert ids[1].tolist() == [high * size, high * size + 1]
+
+
+# ------------------------------------------------------------------------------------------- grouped products
+def test_as_many_workgroups_as_a_launch_may_not_have():
+    """1024 experts of 131071 columns in the paired form (2^32 work-items in tiles of 16 columns).  Small integers: both sums are
+    exact, and h adds the 8 2^-23 of its float32 evaluation and half a bfloat16 step, 2^-8.  Gates reach -8 * 16 = -128, and for
+    g < -87.3 exp(g) may count as 0: g exp(g) u / (1 + exp(g)) is then 0 in place of up to |g u| 2^-126 <= 2^-112, far above
+    bfloat16's least value, so that much is allowed for."""
+    E, I, K = 1024, 131071, 8
+    counts = [2] * 16 + [1] * (E - 16)
+    rows = sum(counts)
+    g = torch.Generator(device=DEV).manual_seed(70)
+    X = torch.randint(-4, 5, (rows, K), generator=g, device=DEV).to(torch.bfloat16)
+    W = torch.randint(-4, 5, (E, 2 * I, K), generator=g, device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    H = torch.full((rows, I), 7.0, dtype=torch.bfloat16, device=DEV)
+    off = offsets_of(counts)
+    print("2^32 work-items", flush=True)
+    L.w4a8_moe_gemm_silu_w16a16(X, None, 1, torch.from_numpy(off).to(DEV), W, H)
+    torch.cuda.synchronize()
+    for e in range(0, E, 31):
+        r = slice(int(off[e]), int(off[e + 1]))
+        y = X[r].float() @ W[e].float().t().contiguous()
+        a, u = y[:, :I].double(), y[:, I:].double()
+        h = a * torch.sigmoid(a) * u
+        e8 = 8 * 2.0 ** -23 * h.abs() + 2.0 ** -126 * (a * u).abs() * (a < 0)
+        over = (H[r].double() - h).abs() - (e8 + (h.abs() + e8) * 2.0 ** -8 + 1e-38)
+        i = int(over.argmax())
+        assert float(over.reshape(-1)[i]) <= 0, (e, float(a.reshape(-1)[i]), float(u.reshape(-1)[i]), float(H[r].reshape(-1)[i]))
