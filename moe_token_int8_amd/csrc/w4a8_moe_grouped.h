@@ -130,12 +130,12 @@ __device__ __forceinline__ int grouped_src(const GroupedArgs& a, int r) {
     return t < a.src_rows ? t : -1;
 }
 
-// MFMA tiles (w4a8_moe_grouped_tile_kernels.hip) over the experts with a.lo <= rows < a.hi.
+// MFMA tiles (w4a8_moe_grouped_tile_kernels.hip) over the experts with a.lo <= rows < a.hi; returns whether small ones.
 struct TileChoice {
     bool small;
     double us;
 };
 TileChoice choose_tiles(const GroupedArgs& a, bool i8, bool pair);
-void launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s);
+bool launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s);
 
 }  // namespace w4a8

@@ -356,8 +356,8 @@ static const char* launch_grouped(GroupedArgs a, hipStream_t s) {
     launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows / a.lo), s);
     if (most <= 64) return "moe_grouped_stream_kernel (by rows)";
     a.lo = 65, a.hi = ALL;
-    launch_grouped_tile(a, FMT, PAIR, s);
-    return "moe_grouped_stream_kernel (by rows), moe_grouped_tile_kernel";
+    return launch_grouped_tile(a, FMT, PAIR, s) ? "moe_grouped_stream_kernel (by rows), moe_grouped_tile_kernel (128 x 128)"
+                                                : "moe_grouped_stream_kernel (by rows), moe_grouped_tile_kernel (256 x 256)";
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -464,24 +464,24 @@ TileChoice choose_tiles(const GroupedArgs& a, bool i8, bool pair) {
 }
 
 template <int FMT, bool PAIR>
-static void launch_tile_t(const GroupedArgs& a, hipStream_t s) {
+static bool launch_tile_t(const GroupedArgs& a, hipStream_t s) {
     auto tiles = [&](long long tile) {                          // an upper bound
         const long long cols = PAIR ? tile / 2 : tile;
         return (a.rows / tile + std::min<long long>(a.E, a.rows / a.lo)) * ((a.N + cols - 1) / cols);
     };
-    if (tiles(256) == 0) return;
-    if (choose_tiles(a, FMT == GF_I8, PAIR).small)
+    const bool small = choose_tiles(a, FMT == GF_I8, PAIR).small;
+    if (tiles(256) == 0) return small;
+    if (small)
         moe_grouped_tile_kernel<FMT, PAIR, 4><<<dim3(unsigned(std::min<long long>(512, tiles(128)))), dim3(256), 0, s>>>(a);
     else
         moe_grouped_tile_kernel<FMT, PAIR, 8><<<dim3(unsigned(std::min<long long>(256, tiles(256)))), dim3(512), 0, s>>>(a);
+    return small;
 }
 
-void launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s) {
-    if (fmt == GF_I8) launch_tile_t<GF_I8, false>(a, s);
-    else if (fmt == GF_BF16 && pair) launch_tile_t<GF_BF16, true>(a, s);
-    else if (fmt == GF_BF16) launch_tile_t<GF_BF16, false>(a, s);
-    else if (pair) launch_tile_t<GF_F16, true>(a, s);
-    else launch_tile_t<GF_F16, false>(a, s);
+bool launch_grouped_tile(const GroupedArgs& a, int fmt, bool pair, hipStream_t s) {
+    if (fmt == GF_I8) return launch_tile_t<GF_I8, false>(a, s);
+    if (fmt == GF_BF16) return pair ? launch_tile_t<GF_BF16, true>(a, s) : launch_tile_t<GF_BF16, false>(a, s);
+    return pair ? launch_tile_t<GF_F16, true>(a, s) : launch_tile_t<GF_F16, false>(a, s);
 }
 
 }  // namespace w4a8

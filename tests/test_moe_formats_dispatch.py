@@ -7,6 +7,8 @@ import sys
 
 import pytest
 
+from test_gpu_moe_tiles import LARGE, MIXED
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 CHILD = r"""
@@ -47,3 +49,23 @@ def test_no_launch_of_2_to_the_32_work_items():
                        [("silu", False, 1024, 1024, 16384, 8, n) for n in (65535, 65521, 65536)])
     one = "moe_grouped_stream_kernel (32-row tiles)"
     assert [n == one for n in names] == [True, True, False, True, True, True, True], names
+
+
+SMALL, BIG = "moe_grouped_tile_kernel (128 x 128)", "moe_grouped_tile_kernel (256 x 256)"
+
+
+def test_log_names_the_tiles():
+    """The sizes at which tests/test_gpu_moe_tiles.py means to reach each tile size, in every product, do."""
+    rows, E = sum(LARGE), len(LARGE)
+    small = [("w8", 1152, 2306), ("w8", 1280, 2049), ("w8", 1152, 2047), ("w16", 1096, 2050), ("w16", 1152, 2051), ("w16", 1096, 2047),
+             ("silu", 1096, 1100), ("silu", 1280, 1153)]
+    big = [("w8", 1152, 4102), ("w8", 1280, 4097), ("w8", 1152, 4095), ("w16", 1096, 4100), ("w16", 1152, 4099), ("w16", 1096, 4095),
+           ("silu", 1096, 2060), ("silu", 1280, 2051)]
+    for want, shapes in ((SMALL, small), (BIG, big)):
+        names = kernels_of([(op, False, 1, E, rows, K, N) for op, K, N in shapes] +
+                           [(op, True, 3, E, rows + 70, K, N) for op, K, N in shapes])
+        assert all(n.endswith(want) for n in names), (want, names)
+    rows, E = sum(MIXED), len(MIXED)
+    names = kernels_of([("w16", True, 4, E, rows + 3, 2200, 4100), ("w8", True, 4, E, rows + 3, 2304, 4100),
+                        ("w16", True, 4, E, rows + 3, 2200, 2050), ("silu", False, 1, E, rows, 2200, 1030)])
+    assert [n.endswith(BIG) for n in names] == [True, True, False, False] and all(n.endswith(SMALL) for n in names[2:]), names
