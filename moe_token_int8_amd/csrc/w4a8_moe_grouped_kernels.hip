@@ -246,6 +246,8 @@ __global__ __launch_bounds__(512, 4) void moe_grouped_stream_kernel(GroupedArgs 
                 y[1] = (float(s[1]) * osw[i].y) * osx[i];
                 y[2] = (float(s[2]) * osw[i].z) * osx[i];
                 y[3] = (float(s[3]) * osw[i].w) * osx[i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = osrc[i] < 0 ? 0.0f : y[k];
             } else if constexpr (PAIR) {
                 const acc_t up = total(o + ITEMS / 2);
 #pragma unroll

@@ -199,7 +199,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
         const int t = g < 0 ? -1 : int(unsigned(g) / unsigned(a.topk));
         return t < a.src_rows ? t : -1;
     };
-    // scale of row threadIdx.x; 16 bit: 0 marks a gather entry that names no row
+    // scale of row threadIdx.x (16 bit: 1); NO_ROW marks a gather entry that names no row, whose outputs are zeros.  A row whose
+    // scale is -0 is taken for one, which has zeros too.
+    constexpr float NO_ROW = FMT == GF_I8 ? -0.0f : 0.0f;
     float own_scale = 0.0f;
     // descriptors, offsets and row scales of a tile, and the copies of its first steps
     auto begin = [&](const int4 g) __attribute__((always_inline)) {
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
                                   size_t(last_col) * a.ldw + size_t(a.kb));
         }
         const int own = tid < g.z ? source(a.gather ? entries[tid] : g.y + tid) : -1;
-        own_scale = own < 0 ? 0.0f : 1.0f;
+        own_scale = own < 0 ? NO_ROW : 1.0f;
         if (FMT == GF_I8 && own >= 0) own_scale = a.sx[own];
         turn = __builtin_amdgcn_readfirstlane(g.y / GT_M + g.w);
 #pragma unroll
@@ -373,8 +375,10 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
                     for (int i = 0; i < 4; ++i) y[i] = PAIR ? silu_gate(acc[n][m][i]) * acc[n + (PAIR ? 2 : 0)][m][i] : acc[n][m][i];
                 }
             };
-            // 16 bit: the outputs of a gather entry that names no row
-            auto none = [&](const float rs) __attribute__((always_inline)) { return FMT != GF_I8 && rs == 0.0f; };
+            // the outputs of a gather entry that names no row: zeros, whatever its stand-in row and the weights' scales hold
+            auto none = [&](const float rs) __attribute__((always_inline)) {
+                return FMT == GF_I8 ? __float_as_uint(rs) == __float_as_uint(NO_ROW) : rs == NO_ROW;
+            };
             // stores of 16 bytes that exist whole or not at all: one each, dropped by the descriptor where they do not
             const bool regular = near_rows && ((a.N & quantum) == 0 || (cur.w + 1) * COLS <= a.N);
             const unsigned es = f32 ? 4u : 2u, pitch = unsigned(a.ldy) * es;

@@ -5,8 +5,10 @@ import pytest
 import torch
 
 import moe_token_int8_amd as L
-from moe_formats_cases import DEV, offsets_of
+from moe_formats_cases import DEV, assert_within, half_step, offsets_of, w8_device, w8_inputs, w8_reference
+from test_gpu_moe_formats import COUNTS, run_w8
 from test_gpu_moe_route import call, check
+from test_gpu_moe_tiles import LARGE
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
@@ -102,3 +104,40 @@ def test_as_many_workgroups_as_a_launch_may_not_have():
         over = (H[r].double() - h).abs() - (e8 + (h.abs() + e8) * 2.0 ** -8 + 1e-38)
         i = int(over.argmax())
         assert float(over.reshape(-1)[i]) <= 0, (e, float(a.reshape(-1)[i]), float(u.reshape(-1)[i]), float(H[r].reshape(-1)[i]))
+
+
+# W8A8 calls (counts of the experts, K, N; with a gather of k = 2) and the kernel that each is there for
+W8_FORMS = {
+    "16-row tiles": ([5, 0, 2], 256, 70),
+    "32-row tiles": (COUNTS["edges"], 256, 70),
+    "128 x 128": (LARGE, 1152, 2306),
+    "128 x 128, whole stores": (LARGE, 1152, 2304),
+    "256 x 256": (LARGE, 1152, 4102),
+    "256 x 256, whole stores": (LARGE, 1152, 4096),
+}
+
+
+@pytest.mark.parametrize("form", list(W8_FORMS))
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_w8_rows_of_nothing_under_any_scale(form, out):
+    """A gather entry that names no row gives zeros also where the channel's scale is infinite, NaN or so large that its product
+    with another row's sum overflows; the other rows are as ever."""
+    counts, K, N = W8_FORMS[form]
+    print("rows of nothing", form, out, flush=True)
+    c = w8_inputs(71, counts, K, N, src_rows=50, k=2)
+    c["gather"][::5] = -1
+    c["gather"][1::7] = 100                                     # token 50 of 50
+    c["gather"][2::9] = 2 ** 31 - 1
+    odd = [3, 4, 5, 6, N - 1]
+    c["sw"][:, odd] = np.array([np.inf, np.nan, -np.inf, 3e38, np.nan], np.float32)
+    c["codes"][:, :, 6] = 127
+    c["Xq"][0] = 127
+    Y = run_w8(c, out).cpu()
+    none = torch.from_numpy((c["gather"] < 0) | (c["gather"] >= 100))
+    assert none.any() and (Y[none] == 0).all()
+    keep = [n for n in range(N) if n not in odd]
+    with np.errstate(all="ignore"):
+        want = torch.from_numpy(w8_reference(c))[:, keep]
+    e = 4 * 2.0 ** -24 * want.abs()
+    assert_within(Y[:, keep], want, e + half_step(out, want.abs() + e) + 1e-38, form)
+    assert torch.isnan(Y[~none][:, [4, N - 1]]).all() and not torch.isfinite(Y[~none][:, [3, 5]]).any()

@@ -7,6 +7,7 @@ import sys
 
 import pytest
 
+from test_gpu_moe_edges import W8_FORMS
 from test_gpu_moe_tiles import LARGE, MIXED
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -69,3 +70,9 @@ def test_log_names_the_tiles():
     names = kernels_of([("w16", True, 4, E, rows + 3, 2200, 4100), ("w8", True, 4, E, rows + 3, 2304, 4100),
                         ("w16", True, 4, E, rows + 3, 2200, 2050), ("silu", False, 1, E, rows, 2200, 1030)])
     assert [n.endswith(BIG) for n in names] == [True, True, False, False] and all(n.endswith(SMALL) for n in names[2:]), names
+
+
+def test_forms_of_the_edge_tests():
+    """tests/test_gpu_moe_edges.py runs the kernel that each of its forms is named for."""
+    names = kernels_of([("w8", True, 2, len(c), sum(c), K, N) for c, K, N in W8_FORMS.values()])
+    assert all(form.split(",")[0] in name for form, name in zip(W8_FORMS, names)), names
