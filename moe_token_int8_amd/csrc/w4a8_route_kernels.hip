@@ -236,11 +236,11 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const double r = p[j] + double(bias[j]);
-            const bool masked = x[j] == -__builtin_huge_valf();
-            bad |= !masked && r != r;                           // the bias of a masked expert is never looked at
+            // a masked expert ranks as one with a bias of -Inf, whatever its own is
+            const double r = p[j] + double(x[j] == -__builtin_huge_valf() ? x[j] : bias[j]);
+            bad |= r != r;
             // an infinite bias stays a number
-            key[j] = route_mask(route_key(fmin(r, 1e300), e0 + j), masked || r < -1e39);
+            key[j] = route_mask(route_key(fmin(r, 1e300), e0 + j), r < -1e39);
         }
     } else {
         if (!a.sigmoid) {
