@@ -8,6 +8,7 @@ import sys
 import pytest
 
 from test_gpu_moe_edges import W8_FORMS
+from test_gpu_moe_tile_edges import SPLITS, TILES
 from test_gpu_moe_tiles import LARGE, MIXED
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -76,3 +77,13 @@ def test_forms_of_the_edge_tests():
     """tests/test_gpu_moe_edges.py runs the kernel that each of its forms is named for."""
     names = kernels_of([("w8", True, 2, len(c), sum(c), K, N) for c, K, N in W8_FORMS.values()])
     assert all(form.split(",")[0] in name for form, name in zip(W8_FORMS, names)), names
+
+
+@pytest.mark.parametrize("tile", list(TILES))
+def test_tiles_of_the_tile_edge_tests(tile):
+    """Every size in tests/test_gpu_moe_tile_edges.py reaches the tile size it is listed under, however its rows are gathered."""
+    N, I = TILES[tile]
+    assert all(sum(s) <= sum(LARGE) for s in SPLITS)
+    names = kernels_of([(op, g, k, len(LARGE), sum(LARGE), K, n) for op, K, n in (("w8", 1152, N), ("w16", 1096, N), ("silu", 1096, I))
+                        for g, k in ((False, 1), (True, 1), (True, 2), (True, 3))])
+    assert all(n.endswith(f"({tile})") for n in names), names
