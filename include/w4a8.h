@@ -496,7 +496,9 @@ int w4a8_moe_route(const void* logits, int dtype, int T, int ldl, const float* b
  * Rows at or past expert_offsets[E] are not written.  Other arguments, bounds and errors as
  * w4a8_moe_gemm; additionally E <= 1024 (EINVAL) and EUNSUPPORTED for N > 2^20 or rows > 2^24.  k
  * also tells, with or without a gather, that no expert should have more than rows / k rows: the
- * launches are chosen by it, and the result is the same whatever it is (1 if unknown). */
+ * launches are chosen by it (1 if unknown).  A row's result is the same bit for bit whatever k and
+ * the other rows are.  A row whose scale is -0 gives zeros, like
+ * a gather entry that names no row. */
 int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather, int k,
                        const int32_t* expert_offsets, int E, int rows, int src_rows,
                        const void* blobs_dev, size_t expert_stride, const w4a8_wdesc* d, void* Y,
@@ -504,7 +506,10 @@ int w4a8_moe_gemm_w8a8(const int8_t* Xq, const float* sx, const int32_t* gather,
 
 /* Expert-grouped unquantized GEMM (P1 section 8: sensitive experts kept in a finer format):
  *   Y[r, n] = sum_k X[src, k] W[e, n, k],
- * the products exact and summed in float32, then rounded to nearest even if Y has 16 bits.
+ * the products exact and summed in float32, then rounded to nearest even if Y has 16 bits.  A call
+ * repeats bit for bit, but the order of a row's sum, and with it its last bits, depend on the kernel
+ * that E, rows and k select and on the row's place among the rows of its expert and of the call:
+ * the same token may round to a neighbouring value in another batch.
  *   X         device bfloat16 or float16 (dtype) [src_rows, K], row stride ldx elements
  *   W         device, same type, [E, N, K]: output channels by inputs, K contiguous, row stride ldw
  *             and expert stride expert_stride, both in elements

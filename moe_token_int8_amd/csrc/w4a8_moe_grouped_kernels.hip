@@ -223,7 +223,7 @@ __global__ __launch_bounds__(512, 4) void moe_grouped_stream_kernel(GroupedArgs 
             const int col = cb * COLS + ((o >> 6) / MS) * 16 + 4 * (l >> 4);
             osrc[i] = grouped_src(a, rbeg + (row < nrows ? row : 0));
             if constexpr (FMT == GF_I8) {
-                osx[i] = osrc[i] < 0 ? 0.0f : a.sx[osrc[i]];
+                osx[i] = osrc[i] < 0 ? -0.0f : a.sx[osrc[i]];     // -0: no row, as in the tile kernel
                 osw[i] = *reinterpret_cast<const float4*>(wexp + a.scales_off + size_t(min(col, (a.N - 1) & ~3)) * 4);
             }
         }
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(512, 4) void moe_grouped_stream_kernel(GroupedArgs 
                 y[2] = (float(s[2]) * osw[i].z) * osx[i];
                 y[3] = (float(s[3]) * osw[i].w) * osx[i];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = osrc[i] < 0 ? 0.0f : y[k];
+                for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(osx[i]) == 0x80000000u ? 0.0f : y[k];
             } else if constexpr (PAIR) {
                 const acc_t up = total(o + ITEMS / 2);
 #pragma unroll

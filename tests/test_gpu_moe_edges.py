@@ -141,3 +141,29 @@ def test_w8_rows_of_nothing_under_any_scale(form, out):
     e = 4 * 2.0 ** -24 * want.abs()
     assert_within(Y[:, keep], want, e + half_step(out, want.abs() + e) + 1e-38, form)
     assert torch.isnan(Y[~none][:, [4, N - 1]]).all() and not torch.isfinite(Y[~none][:, [3, 5]]).any()
+
+
+def test_w8_rows_do_not_depend_on_the_call():
+    """The same rows, bit for bit, in calls of every kernel, with any k, alone and among others; scales of 0, -0 and NaN among them."""
+    K, N = 1152, 4102
+    c = w8_inputs(72, LARGE, K, N)
+    c["sx"][:4] = np.array([0.0, -0.0, np.nan, -0.5], np.float32)
+    c["sw"][0, :3] = np.array([np.inf, np.nan, -1.0], np.float32)
+    dw = w8_device(c)
+    d, w, t = dw
+    want = run_w8(c, torch.float32, dw)                         # 256 x 256 tiles
+    assert (want[:2, 2:] == 0).all() and (want[1] == 0).all() and not torch.signbit(want[1]).any()
+    bits = want.view(torch.int32)
+    print("k", flush=True)
+    for k in (2, 3, 5):
+        assert torch.equal(run_w8(dict(c, k=k), torch.float32, dw).view(torch.int32), bits), k
+    print("alone", flush=True)
+    for a, b in ((0, 1), (0, 4), (0, 16), (0, 40), (100, 129)): # rows of expert 0: one, a few, two tiles of 32
+        off = torch.tensor([0] + [b - a] * 5, dtype=torch.int32, device=DEV)
+        Y = torch.empty(b - a, N, device=DEV)
+        L.w4a8_moe_gemm_w8a8(t["Xq"][a:b], t["sx"][a:b], None, 1, off, 5, b - a, w.blob, w.stride, d, Y, L.W4A8_OUT_F32)
+        assert torch.equal(Y.view(torch.int32), bits[a:b]), (a, b)
+    print("narrow", flush=True)
+    narrow = w8_inputs(72, LARGE, K, N)
+    narrow.update(sx=c["sx"], sw=c["sw"][:, :2306].copy(), codes=narrow["codes"][:, :, :2306].copy())
+    assert torch.equal(run_w8(narrow, torch.float32).view(torch.int32), bits[:, :2306])        # 128 x 128 tiles
