@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import moe_token_int8_amd as L
-from moe_formats_cases import DEV, assert_within, half_step, offsets_of, w8_device, w8_inputs, w8_reference
+from moe_formats_cases import DEV, assert_within, half_step, offsets_of, route_reference, w8_device, w8_inputs, w8_reference
 from test_gpu_moe_formats import COUNTS, run_w8
 from test_gpu_moe_route import call, check
 from test_gpu_moe_tiles import LARGE
@@ -76,6 +76,36 @@ def test_group_scores_count_42_bits(E, groups):
     ids, _ = call(x.to(DEV), bias.to(DEV), 2, "sigmoid", groups=groups, keep=1)
     assert ids[0].tolist() == [low * size, low * size + 1]
     assert ids[1].tolist() == [high * size, high * size + 1]
+
+
+def weight_error(E, groups, k, score, with_bias, renorm, dtype, seed):
+    """Largest |got - want| / |want| of a call's weights, in units of 2^-24 (half a unit of float32, the last rounding's share)."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(64, E, generator=g) * 2).to(dtype)
+    bias = torch.randn(E, generator=g) * 0.2 if with_bias else None
+    ids, w = call(x.to(DEV), None if bias is None else bias.to(DEV), k, score, renorm=renorm, scale=2.5, groups=groups, keep=groups)
+    ri, rw = route_reference(x.float().numpy(), None if bias is None else bias.numpy(), E, k, score, renorm, 2.5, groups, groups)
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    return float((np.abs(w.cpu().numpy().astype(np.float64) - rw) / rw).max() * 2.0 ** 24)
+
+
+@pytest.mark.parametrize("E,groups,k", [(60, 1, 6), (64, 4, 8), (256, 1, 8), (256, 8, 8), (1000, 1, 10), (200, 100, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_weights_are_float64_but_for_one_denominator(E, groups, k, dtype):
+    """Everything but the softmax denominator without a bias is formed in float64 (2^-45 at worst), so that a weight errs by its one
+    rounding to float32, 2^-24, and renormalized weights, in which that denominator cancels, do too.
+
+    That denominator is a float32 sum of exp(-d), d = max - x.  With p = exp(-d) / sum, each d rounded by 2^-24 d moves the sum by
+    sum p d 2^-24 <= ln(E) 2^-24 (the entropy of p, less ln sum >= 0); the exponential is good to 2 units, 4 2^-24; at most
+    15 + 6 additions on the way of a term round by 2^-24 each; and the weight once: under (ln E + 4 + 21 + 1) 2^-24."""
+    for score in ("softmax", "sigmoid"):
+        for with_bias in (False, True):
+            for renorm in (False, True):
+                float32_sum = score == "softmax" and not with_bias and not renorm and groups < 100
+                bound = np.log(E) + 26 if float32_sum else 1 + 2.0 ** -16
+                err = weight_error(E, groups, k, score, with_bias, renorm, dtype, E + k)
+                print(E, groups, score, with_bias, renorm, dtype, "%.2f of %.2f" % (err, bound), flush=True)
+                assert err <= bound, (score, with_bias, renorm, err, bound)
 
 
 # ------------------------------------------------------------------------------------------- grouped products
