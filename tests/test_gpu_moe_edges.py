@@ -5,8 +5,11 @@ import pytest
 import torch
 
 import moe_token_int8_amd as L
+import oracle as O
+from gpu_cases import check_moe
 from moe_formats_cases import DEV, assert_within, half_step, offsets_of, route_reference, w8_device, w8_inputs, w8_reference
 from test_gpu_moe_formats import COUNTS, run_w8
+from test_gpu_moe_layers import routed, run8, weights8
 from test_gpu_moe_route import call, check
 from test_gpu_moe_tiles import LARGE
 
@@ -197,3 +200,16 @@ def test_w8_rows_do_not_depend_on_the_call():
     narrow = w8_inputs(72, LARGE, K, N)
     narrow.update(sx=c["sx"], sw=c["sw"][:, :2306].copy(), codes=narrow["codes"][:, :, :2306].copy())
     assert torch.equal(run_w8(narrow, torch.float32).view(torch.int32), bits[:, :2306])        # 128 x 128 tiles
+
+
+# ------------------------------------------------------------------------------------------- layers
+@pytest.mark.parametrize("T,E,k,H,I,hot", [(3, 16, 4, 384, 128, None), (40, 8, 3, 256, 640, None), (300, 4, 2, 1152, 1280, 1)])
+def test_w8_layer_of_unequal_widths_against_the_oracle(T, E, k, H, I, hot):
+    """H and I apart: a channel's one scale is given to the oracle as the scales of its groups of 128, which is the same sum."""
+    X, ids, w = routed(91, T, E, k, H, hot=hot)
+    wts = weights8(92, E, H, I)
+    per_group = {e: (cgu, np.repeat(sgu, H // 128, axis=0), None, cd, np.repeat(sd, I // 128, axis=0), None)
+                 for e, (cgu, sgu, _, cd, sd, _) in wts[4].items()}
+    print("layer", T, E, k, H, I, flush=True)
+    ref = O.moe_layer(X.float().cpu().numpy(), ids.cpu().numpy(), w.cpu().numpy(), lambda e: per_group[e], E, I, 128)
+    check_moe(run8(X, ids, w, E, wts), ref, {e: per_group[e] for e in np.unique(ids.cpu().numpy())}, 128)
