@@ -593,9 +593,9 @@ def w4a8_moe_w16a16_workspace_size(T: int, k: int, H: int, I: int, E: int) -> in
 
 def _check_layer(X, topk_ids, topk_w, workspace, out, *weights) -> None:
     _require_current((X, workspace, out) + weights, int32=(topk_ids,), float32=(topk_w,))
-    if str(X.dtype) != "torch.bfloat16" or X.dtype != out.dtype or X.shape != out.shape:
+    if str(X.dtype) != "torch.bfloat16" or X.dtype != out.dtype or X.shape != out.shape or X.dim() != 2:
         raise ValueError("X and out must be bfloat16 [T, H]")
-    if topk_ids.shape != topk_w.shape or topk_ids.shape[0] != X.shape[0]:
+    if topk_ids.dim() != 2 or topk_ids.shape != topk_w.shape or topk_ids.shape[0] != X.shape[0]:
         raise ValueError("topk_ids and topk_w must be [T, k]")
     _check_int32(*X.shape, *topk_ids.shape)
     if not all(t.is_contiguous() for t in (X, topk_ids, topk_w, workspace, out)):

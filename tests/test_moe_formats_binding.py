@@ -236,3 +236,27 @@ def test_columns_that_are_not_next_to_each_other(calls, call):
     with pytest.raises(ValueError, match="contiguous"):
         call()
     assert not calls
+
+
+# ------------------------------------------------------------------------------------------- shapes of a layer
+def shaped16(X=(4, 64), ids=(4, 2), w=(4, 2), out=None, E=3, H=64, I=24):
+    L.w4a8_moe_forward_w16a16(meta(*X, dtype=BF16), meta(*ids, dtype=I32), meta(*w), meta(E, 2 * I, H, dtype=BF16),
+                              meta(E, H, I, dtype=BF16), meta(1 << 20, dtype=torch.uint8), meta(*(out or X), dtype=BF16))
+
+
+def shaped8(X=(4, 256), ids=(4, 2), w=(4, 2), out=None, E=3, H=256, I=128):
+    gu, dn = L.desc(H, 2 * I, H, False, bits=8), L.desc(I, H, I, False, bits=8)
+    L.w4a8_moe_forward_w8a8(meta(*X, dtype=BF16), meta(*ids, dtype=I32), meta(*w), E, meta(E, L._packed_size(gu), dtype=torch.uint8),
+                            L._packed_size(gu), gu, meta(E, L._packed_size(dn), dtype=torch.uint8), L._packed_size(dn), dn,
+                            meta(1 << 20, dtype=torch.uint8), meta(*(out or X), dtype=BF16))
+
+
+@pytest.mark.parametrize("call,H", [(shaped16, 64), (shaped8, 256)])
+def test_layers_take_matrices(calls, call, H):
+    """A third dimension behind [T, H] or [T, k] would be read as more rows of them."""
+    call()
+    for bad in (dict(X=(4, H, 3)), dict(X=(4, H, 1)), dict(ids=(4, 2, 2), w=(4, 2, 2)), dict(ids=(4,), w=(4,)), dict(X=(4,)),
+                dict(out=(5, H)), dict(ids=(4, 3)), dict(ids=(5, 2), w=(5, 2)), dict(X=(4, H + 8))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    assert len(calls) == 1
