@@ -162,7 +162,7 @@ __device__ __forceinline__ void route_sort(double (&key)[EPL]) {
 // LANES lanes per token, EPL neighbouring experts in each, of which a lane keeps the DEPTH >= min(k, EPL) best in order;
 // k <= LANES rounds, each the best of the lanes' first keys, which its lane then drops.  A group of experts, or all of
 // them, has 2^gshift whole lanes, of which the last may be filled in part or not at all.  With 16 lanes a wave serves 4 tokens.  The vector unit is the bound of many tokens: 16384
-// of 256 experts with bias and groups take 1282 instructions a wave, 8.5 of the kernel's 12.4 us (a search of all keys in
+// of 256 experts with bias and groups take 1273 instructions a wave, 8.5 of the kernel's 12.5 us (a search of all keys in
 // each round and the Taylor series: 1949 and 18.0 us); half of them are the float64 scores and the keys.
 template <int LANES, int EPL, int DEPTH>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(RouteArgs a, int gshift) {
