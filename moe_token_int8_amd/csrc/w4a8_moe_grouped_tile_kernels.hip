@@ -101,7 +101,8 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_grouped_tile_kernel(GroupedArg
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             const int e = EPT * tid + i;
-            const int cnt = e < a.E ? min(a.offsets[e + 1], a.rows) - min(max(a.offsets[e], 0), a.rows) : 0;
+            // both ends clamped to the rows of the call: whatever the offsets hold, the difference does not overflow
+            const int cnt = e < a.E ? min(max(a.offsets[e + 1], 0), a.rows) - min(max(a.offsets[e], 0), a.rows) : 0;
             t[i] = cnt >= a.lo && cnt < a.hi ? (cnt + TILE - 1) / TILE : 0;
             incl += t[i];
         }

@@ -161,3 +161,46 @@ def test_tiles_in_a_graph(tile):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(Y, want))
         assert all((y[sum(counts):] == SENTINEL).all() for y in Y)
+
+
+LEAST, MOST = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("tile", list(TILES))
+@pytest.mark.parametrize("off,owner", [
+    ([600, 1300, LEAST, LEAST, 600, 600], {0: (600, 1300), 3: (0, 600)}),       # an end so low that its difference to a start overflows
+    ([0, 500, 500, -7, LEAST, 500], {0: (0, 500), 4: (0, 500)}),
+    ([LEAST, 129, MOST, LEAST, -1, 0], {0: (0, 129), 1: (129, 2415)}),
+    ([MOST, MOST, LEAST, LEAST, LEAST, LEAST], {}),
+])
+def test_malformed_offsets_stay_inside_the_rows(tile, off, owner):
+    """An expert owns the rows between its two offsets, each clamped to the rows of the call, and none where they do not ascend."""
+    rows, (N, I) = sum(LARGE), TILES[tile]
+    o = torch.tensor(off, dtype=torch.int32)
+    written = torch.zeros(rows, dtype=torch.bool)
+    for a, b in owner.values():
+        written[a:b] = True
+    print("malformed", tile, off, flush=True)
+    c = w16_inputs(89, BF16, LARGE, 1096, N)
+    if off[1] == 500:
+        c["W"][4] = c["W"][0]                                   # two experts own the same rows: let them say the same
+    buf = torch.full((rows + 2, N), SENTINEL, dtype=BF16, device=DEV)
+    run_w16(dict(c, offsets=o), Y=buf[1:-1])
+    assert (buf[0] == SENTINEL).all() and (buf[-1] == SENTINEL).all() and (buf[1:-1][~written.to(DEV)] == SENTINEL).all()
+    for e, (a, b) in owner.items():
+        one = dict(X=c["X"][a:b], W=c["W"][e:e + 1], gather=None, k=1, offsets=torch.tensor([0, b - a]), rows=b - a)
+        y, mag = w16_reference(one)
+        assert_within(buf[1 + a:1 + b], y, w16_bound(BF16, 1096, y, mag), (tile, e))
+    c8 = w8_inputs(90, LARGE, 1152, N)
+    c8["offsets"] = np.array(off, np.int64).astype(np.int32)
+    if off[1] == 500:
+        c8["codes"][4], c8["sw"][4] = c8["codes"][0], c8["sw"][0]
+    Y = run_w8(c8).cpu()
+    assert (Y[~written] == SENTINEL).all()
+    for e, (a, b) in owner.items():
+        s = (c8["Xq"][a:b].astype(np.float64) @ c8["codes"][e].astype(np.float64)) * c8["sx"][a:b, None].astype(np.float64)
+        want = torch.from_numpy(s * c8["sw"][e].astype(np.float64))
+        bound = 4 * 2.0 ** -24 * want.abs()
+        assert_within(Y[a:b], want, bound + half_step(BF16, want.abs() + bound) + 1e-38, (tile, e))
+    H = run_w16(dict(c, W=c["W"][:, :2 * I] if 2 * I <= N else torch.cat([c["W"], c["W"]], 1)[:, :2 * I], offsets=o), silu=True)
+    assert (H[~written.to(DEV)] == SENTINEL).all()
