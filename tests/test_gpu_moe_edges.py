@@ -213,3 +213,45 @@ def test_w8_layer_of_unequal_widths_against_the_oracle(T, E, k, H, I, hot):
     print("layer", T, E, k, H, I, flush=True)
     ref = O.moe_layer(X.float().cpu().numpy(), ids.cpu().numpy(), w.cpu().numpy(), lambda e: per_group[e], E, I, 128)
     check_moe(run8(X, ids, w, E, wts), ref, {e: per_group[e] for e in np.unique(ids.cpu().numpy())}, 128)
+
+
+# ------------------------------------------------------------------------------------------- refusals on device tensors
+def test_refusals_leave_the_output_alone():
+    """Wrong types, CPU tensors among device ones, gaps and overlaps: refused before anything is launched."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    x, ids, w, d = torch.randn(4, 64, device=DEV), torch.full((4, 2), -7, **i32), torch.full((4, 2), -7.0, device=DEV), L.route_desc(64, 2)
+    bad = [lambda: L.w4a8_moe_route(x, d, ids.long(), w), lambda: L.w4a8_moe_route(x, d, ids, w.half()),
+           lambda: L.w4a8_moe_route(x.cpu(), d, ids, w), lambda: L.w4a8_moe_route(x, d, ids, w, bias=torch.zeros(64)),
+           lambda: L.w4a8_moe_route(x, d, ids, w, bias=torch.zeros(64, dtype=torch.float64, device=DEV)),
+           lambda: L.w4a8_moe_route(x[:1].expand(4, 64), d, ids, w), lambda: L.w4a8_moe_route(x.double(), d, ids, w),
+           lambda: L.w4a8_moe_route(x, d, ids.t().contiguous().t(), w)]
+    dw = L.desc(128, 32, 128, False, bits=8)
+    size = L.w4a8_packed_size(dw)
+    blob, xq, sx = torch.zeros(2, size, dtype=torch.uint8, device=DEV), torch.zeros(4, 128, dtype=torch.int8, device=DEV), torch.zeros(4, device=DEV)
+    off, ga, Y = torch.tensor([0, 2, 4], **i32), torch.zeros(4, **i32), torch.full((4, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+
+    def w8(xq=xq, sx=sx, ga=ga, off=off, blob=blob, stride=size, Y=Y, out=L.W4A8_OUT_BF16):
+        L.w4a8_moe_gemm_w8a8(xq, sx, ga, 1, off, 2, 4, blob, stride, dw, Y, out)
+
+    Y8 = torch.full((8, 32), 7, dtype=torch.uint8, device=DEV)
+    bad += [lambda: w8(xq=xq.to(torch.uint8)), lambda: w8(sx=sx.half()), lambda: w8(ga=ga.long()), lambda: w8(ga=ga.cpu()), lambda: w8(off=off.long()),
+            lambda: w8(off=torch.zeros(3, 2, **i32)[:, 0]), lambda: w8(ga=torch.zeros(8, **i32)[::2]), lambda: w8(Y=Y.half()),
+            lambda: w8(Y=Y8[:4]), lambda: w8(out=L.W4A8_OUT_F32), lambda: w8(blob=blob[:1].expand(2, size)), lambda: w8(stride=-size)]
+    X, W = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 32, 64, dtype=torch.bfloat16, device=DEV)
+    for f in (L.w4a8_moe_gemm_w16a16, L.w4a8_moe_gemm_silu_w16a16):
+        y = Y if f is L.w4a8_moe_gemm_w16a16 else Y[:, :16]
+        bad += [lambda f=f, y=y: f(X.half(), ga, 1, off, W, y), lambda f=f, y=y: f(X.float(), ga, 1, off, W.float(), y),
+                lambda f=f, y=y: f(X, ga.long(), 1, off, W, y), lambda f=f, y=y: f(X, ga, 1, off, W.cpu(), y),
+                lambda f=f, y=y: f(X, ga, 1, torch.zeros(6, **i32)[::2], W, y), lambda f=f, y=y: f(X, ga, 1, off, W, y.half()),
+                lambda f=f, y=y: f(X, ga, 1, off, W, y[:1].expand(4, y.shape[1])), lambda f=f, y=y: f(X, ga, 1, off, W[:1].expand(2, 32, 64), y)]
+    for i, call_it in enumerate(bad):
+        with pytest.raises((ValueError, L.W4A8Error)):
+            call_it()
+    torch.cuda.synchronize()
+    assert (ids == -7).all() and (w == -7).all() and (Y == 7).all() and (Y8 == 7).all()
+    w8()                                                        # and what they were refused for is all that was wrong
+    L.w4a8_moe_gemm_w16a16(X, ga, 1, off, W, Y)
+    L.w4a8_moe_gemm_silu_w16a16(X, ga, 1, off, W, Y[:, :16])
+    L.w4a8_moe_route(x, d, ids, w)
+    torch.cuda.synchronize()
+    assert (Y == 0).all() and (ids >= 0).all()
