@@ -565,6 +565,157 @@ int w4a8_moe_forward_w16a16(const void* X_bf16, const int32_t* topk_ids, const f
                             size_t d_stride, int H, int I, void* workspace, size_t workspace_bytes,
                             void* out_bf16, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Microscaled formats (MXFP4, MXFP8): quantization, products and the expert layer
+ * (P3 names them beside the integer formats; the layer's steps are those of P1 section 4.4)
+ *
+ * Blocks of 32 neighbours along K share one scale 2^(b - 127), kept as the byte b (E8M0; 255 is NaN).
+ * Elements are E2M1 (MXFP4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; sign, two bits of exponent,
+ * one of mantissa; two to a byte, the lower k in the low half) or E4M3 (MXFP8: up to 448, one byte).
+ *
+ * Quantization of a block: b = max(0, floor(log2 amax) + 127 - e), e = 2 (E2M1) or 8 (E4M3), amax the
+ * largest magnitude; element = x / 2^(b - 127) rounded to nearest even, saturating at 6 or 448.  A
+ * block of zeros has b = 0.  A block with a NaN or an infinity has b = 255 and elements 0, and makes
+ * every product with it NaN.
+ *
+ * Activations [M, K]: rows are padded to Kp = 128 ceil(K / 128); codes uint8 [M, Kp / 2] (MXFP4) or
+ * [M, Kp] (MXFP8), scales uint8 [M, Kp / 32], both dense.  Elements and scales behind K are 0:
+ * the quantizing calls write them, and the products rely on it.
+ *
+ * Packed weights (MXFP4, [N, K] output channels by inputs; no header, the caller keeps N and K):
+ *   codes   tile n / 16, then step k / 128, then lane 16 (k % 128 / 32) + n % 16: the 16 bytes of one
+ *           block, the operand of an MFMA
+ *   scales  (at the next multiple of 256) tile n / 64, then step k / 128, then lane (as above), then
+ *           n % 64 / 16: one byte each
+ *   N and K are padded to whole tiles and steps with zeros.
+ *
+ * Limits: K and N at most 2^20, packed codes below 2 GiB (EUNSUPPORTED).
+ * ------------------------------------------------------------------------------------ */
+
+/* Formats of activations.  W4A8_QUANT_INT8, the codes and scales of w4a8_quant_act, is taken by
+ * w4a8_norm_residual_quant only. */
+typedef enum { W4A8_MX_FP4 = 0, W4A8_MX_FP8 = 1, W4A8_QUANT_INT8 = 2 } w4a8_act_format;
+
+/* Block quantization of activations.
+ *   X       device bfloat16, float16 or float32 (dtype) [M, K], row stride ldx >= K elements, aligned to
+ *           its element; any K
+ *   Xq, sx  device, as above; Xq 16-byte, sx 4-byte aligned
+ * M == 0 is a no-op.  EINVAL: fmt, dtype, K <= 0, ldx < K, NULL or misaligned pointers. */
+int w4a8_mx_quant(const void* X, int dtype, int M, int K, int ldx, int fmt, void* Xq, uint8_t* sx, void* stream);
+
+/* The values that codes and scales stand for: Y [M, K] in bfloat16, float16 or float32 (dtype), row stride
+ * ldy (exact in float32 and, where their range has them, in bfloat16; else rounded to nearest even).
+ * Nothing behind column K is written. */
+int w4a8_mx_dequant(const void* Xq, const uint8_t* sx, int fmt, int M, int K, void* Y, int dtype, int ldy, void* stream);
+
+/* Bytes of packed MXFP4 weights [N, K] (0 if invalid). */
+size_t w4a8_mx_packed_size(int K, int N);
+
+/* Quantization and packing of weights on the device.
+ *   W      device bfloat16, float16 or float32 (dtype) [E, N, K], row stride ldw and expert stride
+ *          expert_stride in elements (ignored for E = 1)
+ *   blobs  device, 16-byte aligned, E packed matrices, blob_stride bytes apart (a multiple of 16, >=
+ *          w4a8_mx_packed_size)
+ * E <= 1024 (EINVAL); E == 0 is a no-op; E N / 64 K / 128 < 2^24 (EUNSUPPORTED). */
+int w4a8_mx_pack(const void* W, int dtype, int E, int N, int K, int ldw, size_t expert_stride, void* blobs,
+                 size_t blob_stride, void* stream);
+
+/* Packing of existing MXFP4 codes (a checkpoint, or w4a8_mx_quant's of weights): codes uint8 [N, K / 2] with
+ * row stride ldc bytes (a multiple of 16), scales uint8 [N, K / 32] with row stride lds; K % 32 == 0
+ * (EINVAL).  w4a8_mx_unpack_codes is the inverse, into the layout of activations (rows of Kp). */
+int w4a8_mx_pack_codes(const uint8_t* codes, const uint8_t* scales, int N, int K, int ldc, int lds, void* blob, void* stream);
+int w4a8_mx_unpack_codes(const void* blob, int N, int K, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Product of MX activations with MXFP4 weights,
+ *   Y[m, n] = sum over blocks i of 2^(sx[m, i] + sw[n, i] - 254) sum_{k in block i} x[m, k] w[n, k],
+ * on the scaled MFMA (v_mfma_scale_f32_16x16x128_f8f6f4), summed in float32, rounded to nearest even if Y
+ * has 16 bits.  With MXFP8 and a 16-bit Y, each of 8 neighbouring products loses what lies below 2^-13 of
+ * the largest one's power of two (5e-6 of the result on normal values); with a float32 Y, and with MXFP4,
+ * products are exact.  Terms below 2^-126 may count as 0.  A call repeats bit for bit; the order of a sum
+ * depends on the kernel, which M, K and N select.
+ *   Xq, sx, fmt  device activations [M, K], W4A8_MX_FP4 or W4A8_MX_FP8
+ *   blob         device, packed [N, K]
+ *   Y            device [M, N] bfloat16, float16 or float32 (out_dtype), row stride ldy; any N
+ * M == 0 is a no-op.  EUNSUPPORTED: M > 2^24. */
+int w4a8_mx_gemm(const void* Xq, const uint8_t* sx, int fmt, int M, const void* blob, int K, int N, void* Y,
+                 int ldy, int out_dtype, void* stream);
+
+/* The same by expert: rows [expert_offsets[e], expert_offsets[e + 1]) of Y are products with blob e.
+ *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm_w8a8
+ *   blobs, expert_stride   E packed [N, K], expert_stride bytes apart (a multiple of 16)
+ * Rows at or past expert_offsets[E] are not written, nor is Y past column N.  A gather entry that names no
+ * row gives a row of zeros.  E <= 1024 (EINVAL); EUNSUPPORTED: rows or src_rows > 2^24. */
+int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k,
+                     const int32_t* expert_offsets, int E, int rows, int src_rows, const void* blobs,
+                     size_t expert_stride, int K, int N, void* Y, int ldy, int out_dtype, void* stream);
+
+/* Grouped gate/up product with the gated activation in its epilogue, H[r, c] = silu(g) u from the float32
+ * sums (silu as w4a8_moe_gemm_silu_w16a16).
+ *   blobs   packed [2I, K]: the I gate channels, then the I up channels; I % 16 == 0 (EINVAL)
+ *   H       device [rows, I] bfloat16 or float16 (out_dtype), row stride ldh
+ * Other arguments and errors as w4a8_moe_gemm_mx. */
+int w4a8_moe_gemm_silu_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k,
+                          const int32_t* expert_offsets, int E, int rows, int src_rows, const void* blobs,
+                          size_t expert_stride, int K, int I, void* H, int ldh, int out_dtype, void* stream);
+
+/* The same with H quantized in the epilogue (a block of 32 columns needs no reduction over the row): codes
+ * and scales of the float32 H in h_fmt, the activations [rows, I] of the down product. */
+int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k,
+                                const int32_t* expert_offsets, int E, int rows, int src_rows, const void* blobs,
+                                size_t expert_stride, int K, int I, int h_fmt, void* Hq, uint8_t* sh, void* stream);
+
+/* Workspace bytes needed by w4a8_moe_forward_mx (0 if invalid). */
+size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt);
+
+/* One MoE expert layer on MXFP4 experts with activations in fmt: w4a8_mx_quant(X) -> w4a8_moe_align ->
+ * w4a8_moe_gemm_silu_mx_quant (gathered) -> w4a8_moe_gemm_mx (down, float32) -> the weighted sum per token,
+ * in float32 and rounded once.
+ *   X_bf16     device bfloat16 [T, H]; topk_ids / topk_w device [T, k] (ids outside [0, E) add nothing)
+ *   gu_blobs   E packed [2I, H], gate channels first; d_blobs E packed [H, I]; strides in bytes
+ *   workspace  device, >= w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt) bytes, 256-aligned
+ *   out_bf16   device bfloat16 [T, H]
+ * I % 16 == 0 (EINVAL); T*k <= 2^24 and T ceil(H / 1024) < 2^24 (EUNSUPPORTED).  Every check of the chained
+ * steps runs before the first launch. */
+int w4a8_moe_forward_mx(const void* X_bf16, const int32_t* topk_ids, const float* topk_w, int T, int k, int E,
+                        int fmt, const void* gu_blobs, size_t gu_stride, const void* d_blobs, size_t d_stride,
+                        int H, int I, void* workspace, size_t workspace_bytes, void* out_bf16, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The norm around a block
+ * ------------------------------------------------------------------------------------ */
+
+typedef struct {
+    float eps;        /* of the norm of the residual stream */
+    float eps_post;   /* of the norm of the block's output */
+    float alpha;      /* factor on the block's output */
+} w4a8_norm_desc;
+
+/* The end of one block and the start of the next, row by row:
+ *   u  = X rsqrt(mean(X^2) + eps_post) post_w, or X where post_w is NULL
+ *   r' = residual + alpha gate u, rounded to res_dtype       -> residual_out
+ *   h  = r' rsqrt(mean(r'^2) + eps) w, rounded to dtype      -> Y
+ * in float32 (squares past its range make the mean infinite and h 0 or NaN).
+ *   X             device [M, H] of dtype (bfloat16, float16 or float32), row stride ldx
+ *   residual      device [M, H] of res_dtype, row stride ldr, or NULL (zeros: with alpha = 1 and no gate the
+ *                 call is the norm of X alone)
+ *   gate          device of dtype, [M, H] with row stride ldg, or one row for all (ldg = 0), or NULL (ones)
+ *   post_w, w     device float32 [H]
+ *   residual_out  row stride ldo, or NULL (not stored); may be residual itself
+ *   Y             row stride ldy, or NULL (r' only; w is not read)
+ * Any H up to 65536 (EUNSUPPORTED beyond, and for M > 2^22), rows aligned to their element.  M == 0 is a
+ * no-op.  EINVAL: types, strides below H, eps negative or not finite, alpha not finite, NULL X, no output. */
+int w4a8_norm_residual(const void* X, int dtype, int ldx, const void* residual, int res_dtype, int ldr,
+                       const void* gate, int ldg, const float* post_w, const float* w, const w4a8_norm_desc* d,
+                       int M, int H, void* residual_out, int ldo, void* Y, int ldy, void* stream);
+
+/* The same with h quantized in place of stored: the codes and scales that w4a8_mx_quant (fmt W4A8_MX_FP4 or
+ * W4A8_MX_FP8) or w4a8_quant_act (W4A8_QUANT_INT8: int8 [M, H] and float32 [M], H % 16 == 0) give for h, bit
+ * for bit.  Xq 16-byte, sx 4-byte aligned. */
+int w4a8_norm_residual_quant(const void* X, int dtype, int ldx, const void* residual, int res_dtype, int ldr,
+                             const void* gate, int ldg, const float* post_w, const float* w,
+                             const w4a8_norm_desc* d, int M, int H, void* residual_out, int ldo, int fmt, void* Xq,
+                             void* sx, void* stream);
+
 /* Name of the kernel variant w4a8_gemm resolves to for (d, M), or "unsupported"
  * (P4: record target and resolved backend so a silent fallback is visible):
  * {w4a8,w8a8}_{decode_m16,decode_m32,prefill}_{sym,asym}_g{64,128,256,K,32}[_h16], and

@@ -20,6 +20,7 @@ W4A8_OK, W4A8_EINVAL, W4A8_ESIZE, W4A8_EUNSUPPORTED, W4A8_EHIP = 0, -1, -2, -3, 
 W4A8_OUT_BF16, W4A8_OUT_F32 = 0, 1
 W4A8_BF16, W4A8_F32, W4A8_F16 = 0, 1, 2
 W4A8_ROUTE_SOFTMAX, W4A8_ROUTE_SIGMOID = 0, 1
+W4A8_MX_FP4, W4A8_MX_FP8, W4A8_QUANT_INT8 = 0, 1, 2
 HEADER_BYTES = 256
 
 EXPORTED = [
@@ -33,6 +34,9 @@ EXPORTED = [
     "w4a16_gemm", "w4a16_kernel_name",
     "w4a8_moe_route", "w4a8_moe_gemm_w8a8", "w4a8_moe_gemm_w16a16", "w4a8_moe_gemm_silu_w16a16",
     "w4a8_moe_forward_w8a8", "w4a8_moe_w16a16_workspace_size", "w4a8_moe_forward_w16a16",
+    "w4a8_mx_quant", "w4a8_mx_dequant", "w4a8_mx_packed_size", "w4a8_mx_pack", "w4a8_mx_pack_codes", "w4a8_mx_unpack_codes",
+    "w4a8_mx_gemm", "w4a8_moe_gemm_mx", "w4a8_moe_gemm_silu_mx", "w4a8_moe_gemm_silu_mx_quant",
+    "w4a8_moe_mx_workspace_size", "w4a8_moe_forward_mx", "w4a8_norm_residual", "w4a8_norm_residual_quant",
     "w4a8_kernel_name", "w4a8_status_string", "w4a8_version",
 ]
 
@@ -61,6 +65,10 @@ class ExpertSet(ctypes.Structure):
 class RouteDesc(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("eps_post", ctypes.c_float), ("alpha", ctypes.c_float)]
 
 
 _lib = None
@@ -107,6 +115,20 @@ def lib() -> ctypes.CDLL:
             "w4a8_moe_forward_w8a8": (I, [P, P, P, I, I, I, P, SZ, DP, P, SZ, DP, P, SZ, P, VP]),
             "w4a8_moe_w16a16_workspace_size": (SZ, [I, I, I, I, I]),
             "w4a8_moe_forward_w16a16": (I, [P, P, P, I, I, I, P, SZ, P, SZ, I, I, P, SZ, P, VP]),
+            "w4a8_mx_quant": (I, [P, I, I, I, I, I, P, P, VP]),
+            "w4a8_mx_dequant": (I, [P, P, I, I, I, P, I, I, VP]),
+            "w4a8_mx_packed_size": (SZ, [I, I]),
+            "w4a8_mx_pack": (I, [P, I, I, I, I, I, SZ, P, SZ, VP]),
+            "w4a8_mx_pack_codes": (I, [P, P, I, I, I, I, P, VP]),
+            "w4a8_mx_unpack_codes": (I, [P, I, I, P, P, VP]),
+            "w4a8_mx_gemm": (I, [P, P, I, I, P, I, I, P, I, I, VP]),
+            "w4a8_moe_gemm_mx": (I, [P, P, I, P, I, P, I, I, I, P, SZ, I, I, P, I, I, VP]),
+            "w4a8_moe_gemm_silu_mx": (I, [P, P, I, P, I, P, I, I, I, P, SZ, I, I, P, I, I, VP]),
+            "w4a8_moe_gemm_silu_mx_quant": (I, [P, P, I, P, I, P, I, I, I, P, SZ, I, I, I, P, P, VP]),
+            "w4a8_moe_mx_workspace_size": (SZ, [I, I, I, I, I, I]),
+            "w4a8_moe_forward_mx": (I, [P, P, P, I, I, I, I, P, SZ, P, SZ, I, I, P, SZ, P, VP]),
+            "w4a8_norm_residual": (I, [P, I, I, P, I, I, P, I, P, P, ctypes.POINTER(NormDesc), I, I, P, I, P, I, VP]),
+            "w4a8_norm_residual_quant": (I, [P, I, I, P, I, I, P, I, P, P, ctypes.POINTER(NormDesc), I, I, P, I, I, P, P, VP]),
             "w4a8_kernel_name": (ctypes.c_char_p, [DP, I]),
             "w4a16_gemm": (I, [P, I, I, P, DP, P, I, I, VP]),
             "w4a16_kernel_name": (ctypes.c_char_p, [DP, I]),
@@ -142,6 +164,11 @@ def route_desc(E: int, k: int, score: int = W4A8_ROUTE_SOFTMAX, renormalize: boo
     return RouteDesc(int(E), int(k), int(score), int(bool(renormalize)), int(n_group), int(topk_group), float(scale))
 
 
+def norm_desc(eps: float = 1e-6, eps_post: float = 1e-6, alpha: float = 1.0) -> NormDesc:
+    """Constants of the norm around a block: see w4a8_norm_desc."""
+    return NormDesc(float(eps), float(eps_post), float(alpha))
+
+
 def _dtype(t) -> int:
     """w4a8_dtype of a tensor."""
     try:
@@ -174,7 +201,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.int32, self.int8, self.float32 = torch.int32, torch.int8, torch.float32
+        self.int32, self.int8, self.float32, self.uint8 = torch.int32, torch.int8, torch.float32, torch.uint8
         self.initialized, self.device = torch.cuda.is_initialized, torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.types = {torch.bfloat16: W4A8_BF16, torch.float32: W4A8_F32, torch.float16: W4A8_F16}
@@ -633,6 +660,276 @@ def w4a8_moe_forward_w16a16(X, topk_ids, topk_w, Wgu, Wd, workspace, out, stream
                                          Wd.stride(0), H, I2 // 2, _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
            "w4a8_moe_forward_w16a16")
+
+
+# ------------------------------------------------------------------------------ microscaled formats
+def mx_row_bytes(fmt: int, K: int) -> int:
+    """Bytes of a row of codes: K rounded up to 128, two E2M1 codes to a byte."""
+    Kp = -(-K // 128) * 128
+    return Kp // 2 if fmt == W4A8_MX_FP4 else Kp
+
+
+def mx_empty(fmt: int, M: int, K: int, device="cuda"):
+    """Uninitialized codes and scales of M rows of K, as the quantizing calls take them."""
+    import torch
+    return (torch.empty((M, mx_row_bytes(fmt, K)), dtype=torch.uint8, device=device),
+            torch.empty((M, -(-K // 128) * 4), dtype=torch.uint8, device=device))
+
+
+def _on_device(t, *tensors) -> int:
+    """The current device, on which all the tensors (or None) are."""
+    dev = t.current()
+    for x in tensors:
+        if x is not None and x.get_device() != dev:
+            _require_current([y for y in tensors if y is not None])         # says which
+    return dev
+
+
+def _row_stride(x, what: str) -> int:
+    """Elements between the rows of a matrix whose rows are contiguous; that of a single row says nothing."""
+    (M, N), (ld, step) = x.shape, x.stride()
+    if M <= 1:
+        ld = N
+    if (step != 1 and N > 1) or ld < N:
+        raise ValueError(f"{what} must be a matrix with contiguous rows that do not overlap")
+    if M | N | ld > _INT_MAX:
+        _check_int32(M, N, ld)
+    return ld
+
+
+def _check_mx(t, Xq, sx, fmt: int, K: int) -> int:
+    """Codes and scales as w4a8_mx_quant leaves them; their rows."""
+    if fmt != W4A8_MX_FP4 and fmt != W4A8_MX_FP8:
+        raise ValueError("fmt must be W4A8_MX_FP4 or W4A8_MX_FP8")
+    if not 0 < K <= _INT_MAX:
+        raise ValueError("K must be positive and fit in 32 bits")
+    Kp = -(-K // 128) * 128
+    M = Xq.shape[0]
+    if (Xq.dtype is not t.uint8 or sx.dtype is not t.uint8 or Xq.shape != (M, Kp // 2 if fmt == W4A8_MX_FP4 else Kp) or
+            sx.shape != (M, Kp // 32) or not Xq.is_contiguous() or not sx.is_contiguous()):
+        raise ValueError("the codes and scales must be contiguous uint8 [M, K rounded up to 128 (MXFP4: / 2)] and [M, the same / 32]")
+    if M > _INT_MAX:
+        _check_int32(M)
+    return M
+
+
+_mx_packed_sizes: dict = {}
+
+
+def w4a8_mx_packed_size(K: int, N: int) -> int:
+    """Bytes of packed MXFP4 weights [N, K]."""
+    size = _mx_packed_sizes.get((K, N))
+    if size is None:
+        _check_int32(K, N)
+        size = int(lib().w4a8_mx_packed_size(int(K), int(N)))
+        if len(_mx_packed_sizes) < 4096:
+            _mx_packed_sizes[K, N] = size
+    return size
+
+
+def _check_mx_blobs(t, blobs, E: int, stride: int, K: int, N: int) -> None:
+    size = w4a8_mx_packed_size(K, N)
+    if size == 0:
+        raise W4A8Error(W4A8_EINVAL, "w4a8_mx_packed_size")
+    if E < 1 or stride < 0 or blobs.dtype is not t.uint8 or not blobs.is_contiguous() or blobs.numel() < (E - 1) * stride + size:
+        raise ValueError("the packed weights must be contiguous uint8 and hold E matrices at their stride")
+
+
+def w4a8_mx_quant(X, fmt: int, Xq, sx, stream=None) -> None:
+    """X [M, K] (bfloat16, float16 or float32, rows may be strided) -> MX codes and scales (mx_empty)."""
+    t = _torch()
+    dev = _on_device(t, X, Xq, sx)
+    M, K = X.shape
+    ldx = _row_stride(X, "X")
+    if _check_mx(t, Xq, sx, fmt, K) != M:
+        raise ValueError("X and its codes must have the same rows")
+    _check(lib().w4a8_mx_quant(X.data_ptr(), _dtype(X), M, K, ldx, fmt, Xq.data_ptr(), sx.data_ptr(),
+                               t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_quant")
+
+
+def w4a8_mx_dequant(Xq, sx, fmt: int, Y, stream=None) -> None:
+    """The values of MX codes and scales: Y [M, K] in bfloat16, float16 or float32, rows may be strided."""
+    t = _torch()
+    dev = _on_device(t, Y, Xq, sx)
+    M, K = Y.shape
+    ldy = _row_stride(Y, "Y")
+    if _check_mx(t, Xq, sx, fmt, K) != M:
+        raise ValueError("Y and its codes must have the same rows")
+    _check(lib().w4a8_mx_dequant(Xq.data_ptr(), sx.data_ptr(), fmt, M, K, Y.data_ptr(), _dtype(Y), ldy,
+                                 t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_dequant")
+
+
+def w4a8_mx_pack(W, blobs, stream=None) -> None:
+    """Quantize W [N, K] or [E, N, K] to MXFP4 and pack it into blobs, uint8 [w4a8_mx_packed_size] or [E, stride]."""
+    t = _torch()
+    dev = _on_device(t, W, blobs)
+    if W.dim() not in (2, 3) or blobs.dim() != W.dim() - 1 or blobs.dtype is not t.uint8 or not blobs.is_contiguous():
+        raise ValueError("W must be [N, K] or [E, N, K], and blobs a contiguous uint8 [bytes] or [E, bytes]")
+    one = W.dim() == 2
+    E, (N, K) = 1 if one else W.shape[0], W.shape[-2:]
+    if E == 0:
+        return
+    ldw = _row_stride(W if one else W[0], "W")
+    expert, stride = (0, 0) if one or E == 1 else (W.stride(0), blobs.stride(0))
+    if expert < 0 or (not one and blobs.shape[0] != E):
+        raise ValueError("W and blobs must have the same experts")
+    _check_mx_blobs(t, blobs, E, stride, K, N)
+    _check(lib().w4a8_mx_pack(W.data_ptr(), _dtype(W), E, N, K, ldw, expert, blobs.data_ptr(), stride,
+                              t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_pack")
+
+
+def w4a8_mx_pack_codes(codes, scales, blob, stream=None) -> None:
+    """Pack existing MXFP4 codes uint8 [N, K / 2] and scales uint8 [N, K / 32] (rows may be strided), K % 32 == 0."""
+    t = _torch()
+    dev = _on_device(t, codes, scales, blob)
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if codes.dtype is not t.uint8 or scales.dtype is not t.uint8 or scales.shape != (N, K // 32) or K % 32:
+        raise ValueError("codes and scales must be uint8 [N, K / 2] and [N, K / 32]")
+    ldc, lds = _row_stride(codes, "codes"), _row_stride(scales, "scales")
+    _check_mx_blobs(t, blob, 1, 0, K, N)
+    _check(lib().w4a8_mx_pack_codes(codes.data_ptr(), scales.data_ptr(), N, K, ldc, lds, blob.data_ptr(),
+                                    t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_pack_codes")
+
+
+def w4a8_mx_unpack_codes(blob, N: int, K: int, codes, scales, stream=None) -> None:
+    """The inverse, into the layout of activations: codes and scales of mx_empty(W4A8_MX_FP4, N, K)."""
+    t = _torch()
+    dev = _on_device(t, codes, scales, blob)
+    if _check_mx(t, codes, scales, W4A8_MX_FP4, K) != N:
+        raise ValueError("the codes must have N rows")
+    _check_mx_blobs(t, blob, 1, 0, K, N)
+    _check(lib().w4a8_mx_unpack_codes(blob.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(),
+                                      t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_unpack_codes")
+
+
+def w4a8_mx_gemm(Xq, sx, fmt: int, blob, K: int, N: int, Y, stream=None) -> None:
+    """Y [M, N] (bfloat16, float16 or float32, rows may be strided) = MX activations times packed MXFP4 weights [N, K]."""
+    t = _torch()
+    dev = _on_device(t, Xq, sx, blob, Y)
+    M = _check_mx(t, Xq, sx, fmt, K)
+    ldy = _row_stride(Y, "Y")
+    if Y.shape != (M, N):
+        raise ValueError("Y must be [M, N]")
+    _check_mx_blobs(t, blob, 1, 0, K, N)
+    _check(lib().w4a8_mx_gemm(Xq.data_ptr(), sx.data_ptr(), fmt, M, blob.data_ptr(), K, N, Y.data_ptr(), ldy, _dtype(Y),
+                              t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_gemm")
+
+
+def _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, others):
+    """Checked arguments of the grouped MX products, up to and including K; the current device."""
+    t = _torch()
+    dev = _on_device(t, Xq, sx, gather, expert_offsets, blobs, *others)
+    if expert_offsets.dtype is not t.int32 or (gather is not None and gather.dtype is not t.int32):
+        raise ValueError("gather and expert_offsets must be int32")
+    src_rows = _check_mx(t, Xq, sx, fmt, K)
+    if not (-_INT_MAX <= k <= _INT_MAX and 0 < E <= _INT_MAX) or rows > _INT_MAX:
+        raise ValueError("k, E and the rows must fit in 32 bits, and there must be an expert")
+    _check_rows(gather, expert_offsets, E, rows)
+    _check_mx_blobs(t, blobs, E, expert_stride, K, N)
+    return (Xq.data_ptr(), sx.data_ptr(), fmt, None if gather is None else gather.data_ptr(), int(k), expert_offsets.data_ptr(),
+            int(E), rows, src_rows, blobs.data_ptr(), int(expert_stride), K), t, dev
+
+
+def w4a8_moe_gemm_mx(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, Y,
+                     stream=None) -> None:
+    """Grouped product of MX activations with E packed MXFP4 matrices [N, K]; Y [rows, N]."""
+    rows, N = Y.shape
+    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, (Y,))
+    _check(lib().w4a8_moe_gemm_mx(*args, N, Y.data_ptr(), _row_stride(Y, "Y"), _dtype(Y),
+                                  t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_mx")
+
+
+def w4a8_moe_gemm_silu_mx(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, H,
+                          stream=None) -> None:
+    """Grouped gate/up product with silu(gate) * up in its epilogue: E packed [2I, K], H [rows, I] in bfloat16 or float16."""
+    rows, I = H.shape
+    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, (H,))
+    _check(lib().w4a8_moe_gemm_silu_mx(*args, I, H.data_ptr(), _row_stride(H, "H"), _dtype(H),
+                                       t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_silu_mx")
+
+
+def w4a8_moe_gemm_silu_mx_quant(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, I: int,
+                                h_fmt: int, Hq, sh, stream=None) -> None:
+    """The same with H quantized to h_fmt: codes and scales of mx_empty(h_fmt, rows, I)."""
+    t = _torch()
+    rows = _check_mx(t, Hq, sh, h_fmt, I)
+    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, (Hq, sh))
+    _check(lib().w4a8_moe_gemm_silu_mx_quant(*args, I, h_fmt, Hq.data_ptr(), sh.data_ptr(),
+                                             t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_silu_mx_quant")
+
+
+def w4a8_moe_mx_workspace_size(T: int, k: int, H: int, I: int, E: int, fmt: int) -> int:
+    _check_int32(T, k, H, I, E, fmt)
+    return int(lib().w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt))
+
+
+def w4a8_moe_forward_mx(X, topk_ids, topk_w, E: int, fmt: int, gu_blobs, gu_stride: int, d_blobs, d_stride: int, I: int, workspace,
+                        out, stream=None) -> None:
+    """One MoE layer on MXFP4 experts: gu_blobs E packed [2I, H], d_blobs E packed [H, I]; workspace of
+    w4a8_moe_mx_workspace_size bytes."""
+    _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
+    t = _torch()
+    (T, k), H = topk_ids.shape, X.shape[1]
+    _check_int32(E, fmt, I)
+    _check_mx_blobs(t, gu_blobs, E, gu_stride, H, 2 * I)
+    _check_mx_blobs(t, d_blobs, E, d_stride, I, H)
+    _check(lib().w4a8_moe_forward_mx(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, int(E), int(fmt), _ptr(gu_blobs), int(gu_stride),
+                                     _ptr(d_blobs), int(d_stride), H, int(I), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
+           "w4a8_moe_forward_mx")
+
+
+# ------------------------------------------------------------------------------ the norm around a block
+def _norm_args(X, residual, d: NormDesc, w, residual_out, post_w, gate, others):
+    """Checked arguments of the norm calls, up to and including the row stride of residual_out; the current device."""
+    t = _torch()
+    dev = _on_device(t, X, residual, w, residual_out, post_w, gate, *others)
+    M, H = X.shape
+    ldx = _row_stride(X, "X")
+    like = residual if residual is not None else residual_out
+    for r in (residual, residual_out):
+        if r is not None and (r.shape != X.shape or r.dtype is not like.dtype):
+            raise ValueError("residual and residual_out must have the shape of X and one type")
+    for v in (w, post_w):
+        if v is not None and (v.dtype is not t.float32 or v.numel() != H or not v.is_contiguous()):
+            raise ValueError("w and post_w must be contiguous float32 [H]")
+    ldg = 0
+    if gate is not None:
+        if gate.dtype is not X.dtype or gate.dim() != 2 or gate.shape[0] not in (1, M) or gate.shape[1] != H:
+            raise ValueError("gate must be [M, H] or [1, H] in the type of X")
+        ldg = _row_stride(gate, "gate") if gate.shape[0] == M and M > 1 else 0
+        if ldg == 0 and gate.stride(1) != 1 and H > 1:
+            raise ValueError("the rows of gate must be contiguous")
+    return (X.data_ptr(), _dtype(X), ldx, _ptr(residual), _dtype(like if like is not None else X),
+            H if residual is None else _row_stride(residual, "residual"), _ptr(gate), ldg, _ptr(post_w), _ptr(w), d, M, H,
+            _ptr(residual_out), H if residual_out is None else _row_stride(residual_out, "residual_out")), t, dev
+
+
+def w4a8_norm_residual(X, residual, d: NormDesc, w, residual_out, Y, post_w=None, gate=None, stream=None) -> None:
+    """r' = residual + alpha gate u, u = X or its RMS norm times post_w; Y = RMS norm of r' times w.  residual, residual_out, Y,
+    post_w and gate may be None."""
+    args, t, dev = _norm_args(X, residual, d, w, residual_out, post_w, gate, (Y,))
+    ldy = X.shape[1]
+    if Y is not None:
+        if Y.shape != X.shape or Y.dtype is not X.dtype:
+            raise ValueError("Y must have the shape and type of X")
+        ldy = _row_stride(Y, "Y")
+    _check(lib().w4a8_norm_residual(*args, _ptr(Y), ldy, t.raw_stream(dev) if stream is None else int(stream)), "w4a8_norm_residual")
+
+
+def w4a8_norm_residual_quant(X, residual, d: NormDesc, w, residual_out, fmt: int, Xq, sx, post_w=None, gate=None,
+                             stream=None) -> None:
+    """The same with h quantized: MX codes and scales (mx_empty), or int8 [M, H] and float32 [M] for W4A8_QUANT_INT8."""
+    args, t, dev = _norm_args(X, residual, d, w, residual_out, post_w, gate, (Xq, sx))
+    M, H = X.shape
+    if fmt == W4A8_QUANT_INT8:
+        if (Xq.dtype is not t.int8 or Xq.shape != (M, H) or sx.dtype is not t.float32 or sx.numel() != M or
+                not Xq.is_contiguous() or not sx.is_contiguous()):
+            raise ValueError("Xq and sx must be contiguous int8 [M, H] and float32 [M]")
+    elif _check_mx(t, Xq, sx, fmt, H) != M:
+        raise ValueError("X and its codes must have the same rows")
+    _check(lib().w4a8_norm_residual_quant(*args, fmt, _ptr(Xq), _ptr(sx), t.raw_stream(dev) if stream is None else int(stream)),
+           "w4a8_norm_residual_quant")
 
 
 # ------------------------------------------------------------------------------ helpers

@@ -1,0 +1,141 @@
+// Products of MX activations with packed MXFP4 weights: arguments, the scaled MFMA and the outputs, shared by the streaming and
+// the tile kernels (gfx950).
+#pragma once
+
+#include "w4a8_mx.h"
+#include "w4a8_moe_grouped.h"
+
+namespace w4a8 {
+
+struct MxArgs {
+    const uint8_t* X;         // activation codes, rows of rowb bytes
+    const uint8_t* sx;        // their scale bytes, rows of 4 K1
+    unsigned rowb;
+    const int32_t* gather;    // source row of routed row r: gather[r] / topk (NULL: r)
+    int topk;
+    int src_rows;
+    const int32_t* offsets;   // [E + 1] (NULL: one expert, all rows: the dense product)
+    int E;
+    int rows;
+    const uint8_t* W;         // packed weights of expert 0
+    size_t expert_stride;     // bytes between experts
+    size_t scales_off;
+    int K1;                   // steps of 128 k
+    int N;                    // columns of Y (paired form: of h; W then has 2 N, gate columns first)
+    void* Y;
+    size_t ldy;               // elements
+    int out;                  // w4a8_dtype of Y
+    uint8_t* Hq;              // paired form: codes and scales of h in place of Y (h_fmt; NULL: Y)
+    uint8_t* sh;
+    int h_fmt;
+    int lo, hi;               // this launch serves the experts with lo <= rows < hi
+};
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ int mx_row_first(const MxArgs& a, int e) {
+    return a.offsets ? min(max(a.offsets[e], 0), a.rows) : 0;
+}
+__device__ __forceinline__ int mx_row_last(const MxArgs& a, int e) {
+    return a.offsets ? min(max(a.offsets[e + 1], 0), a.rows) : a.rows;
+}
+
+// Source row of routed row r, or -1 (a gather entry that names no row of X: its output is zero).
+__device__ __forceinline__ int mx_src(const MxArgs& a, int r) {
+    if (!a.gather) return r;
+    const int g = a.gather[r];
+    if (g < 0) return -1;
+    const int t = int(unsigned(g) / unsigned(a.topk));
+    return t < a.src_rows ? t : -1;
+}
+
+// Activation operands of the kernels: fp4, fp8, and fp8 for float32 outputs (MX_FP8_EXACT).  Within 8 neighbouring k the MFMA
+// aligns the products of fp8 to the largest one and drops what lies 2^-13 and more below its power of two (measured: 2688
+// + 2^-3 is exact, 2^-4 is lost; 8 places further along K it is not).  On normal values that is 5e-6 normwise, 2e-5 with outliers:
+// nothing in 16 bits, but more than float32 should lose.  There each operand is multiplied in two parts, its elements of 2 and more
+// and the smaller ones: the products of a part then span no more than 14 bits, and nothing is dropped.
+enum { MX_FP8_EXACT = 2 };
+
+// Operand of one step of 128 k: 16 bytes of fp4 (a lane's block of 32), or two pieces of 16 fp8 values (k = 16 q and k = 64 + 16 q
+// of the step, where q = lane / 16).
+template <int FMT>
+struct MxOperand {
+    v4i p[FMT == W4A8_MX_FP4 ? 1 : 2];
+};
+
+// The elements of magnitude 2 and more (bit 6 of their byte, the high bit of the exponent, is set); the others are zero.
+__device__ __forceinline__ v4i mx_large(const v4i x) {
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = uint32_t(x[i]) & 0x40404040u;
+        r[i] = int(uint32_t(x[i]) & ((b << 2) - (b >> 6)));     // 255 times the bit, in every byte
+    }
+    return r;
+}
+
+// One step of a 16 x 16 tile: v_mfma_scale_f32_16x16x128_f8f6f4 multiplies blocks of 32 k with their scales and sums in float32
+// (fp4: exact where float32 holds the sum, else within 2^-23 of the sum of magnitudes).  The weights are the first operand, so
+// a lane's four sums are the columns 4 (lane / 16) .. + 3 of activation row lane % 16.  A lane's scale is that of block lane / 16:
+// byte WB of sw, byte 0 of sx.
+template <int FMT, int WB>
+__device__ __forceinline__ v4f mx_mfma(const v4i w, const MxOperand<FMT>& x, v4f c, const uint32_t sw, const uint32_t sx) {
+    const v8i a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+    if constexpr (FMT == W4A8_MX_FP4) {
+        const v8i b = __builtin_shufflevector(x.p[0], x.p[0], 0, 1, 2, 3, -1, -1, -1, -1);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, WB, int(sw), 0, int(sx));
+    } else {
+        v4i p0 = x.p[0], p1 = x.p[1];
+        if constexpr (FMT == MX_FP8_EXACT) {
+            const v4i l0 = mx_large(p0), l1 = mx_large(p1);
+            const v8i l = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, l, c, 4, 0, WB, int(sw), 0, int(sx));
+            p0 ^= l0, p1 ^= l1;
+        }
+        const v8i b = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, WB, int(sw), 0, int(sx));
+    }
+}
+
+// Four neighbouring outputs of one row, of which n (1..4) exist.
+__device__ __forceinline__ void mx_store(const MxArgs& a, const size_t at, const int n, const v4f y) {
+    GroupedArgs g;
+    g.Y = a.Y;
+    g.out = a.out;
+    grouped_store(g, at, n, y[0], y[1], y[2], y[3]);
+}
+
+// Blocks of h behind column N, up to whole steps of the product that reads h: zeros, written with the last block.
+__device__ __forceinline__ void mx_pad_blocks(const MxArgs& a, const int row, const int first, const int tid8) {
+    const int Ip = mx_kp(a.N), bytes = a.h_fmt == W4A8_MX_FP4 ? 16 : 32;
+    for (int b = first; b < Ip / 32; ++b) {
+        if (tid8 * 4 < bytes) *reinterpret_cast<uint32_t*>(a.Hq + (size_t(row) * size_t(Ip / 32) + size_t(b)) * bytes + tid8 * 4) = 0u;
+        if (tid8 == 0) a.sh[size_t(row) * size_t(Ip / 32) + b] = 0;
+    }
+}
+
+// Four neighbouring values y of one block of h, whose other values are with the 8 lanes around (lane ^ 1, ^ 2, ^ 4): codes and
+// scale.  All 8 lanes take part.
+__device__ __forceinline__ void mx_store_block(const MxArgs& a, const int row, const int block, const int j, const v4f y, const bool store) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+    m = mx_quad_max(m);
+    m = max(m, uint32_t(__shfl_xor(int(m), 4, 64)));
+    const bool fp4 = a.h_fmt == W4A8_MX_FP4;
+    const uint32_t byte = fp4 ? mx_scale_byte<W4A8_MX_FP4>(m) : mx_scale_byte<W4A8_MX_FP8>(m);
+    const float up = byte == 255u ? 0.0f : mx_up(byte);
+    const v4f v = y * up;
+    if (!store) return;
+    const size_t at = size_t(row) * size_t(mx_kp(a.N) / 32) + size_t(block);
+    if (fp4) {
+        const uint32_t q = byte == 255u ? 0u : mx_fp4x4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint16_t*>(a.Hq + at * 16 + j * 2) = uint16_t(q);
+    } else {
+        const uint32_t q = byte == 255u ? 0u : mx_fp8x4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint32_t*>(a.Hq + at * 32 + j * 4) = q;
+    }
+    if (j == 0) a.sh[at] = uint8_t(byte);
+}
+
+}  // namespace w4a8
