@@ -97,6 +97,13 @@ __device__ __forceinline__ v4f mx_mfma(const v4i w, const MxOperand<FMT>& x, v4f
     }
 }
 
+// silu(g) = g / (1 + exp(-g)) with v_exp_f32 and v_rcp_f32: the exponent's product is rounded once, which costs |g| 2^-24 of the
+// result (5e-6 at g = -80), well inside the half step of the 16-bit and the quantized outputs it goes to.  Past g = -88 the
+// exponential overflows and the result is 0.
+__device__ __forceinline__ float mx_silu(float g) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269502f));
+}
+
 // Four neighbouring outputs of one row, of which n (1..4) exist.
 __device__ __forceinline__ void mx_store(const MxArgs& a, const size_t at, const int n, const v4f y) {
     GroupedArgs g;
@@ -137,5 +144,10 @@ __device__ __forceinline__ void mx_store_block(const MxArgs& a, const int row, c
     }
     if (j == 0) a.sh[at] = uint8_t(byte);
 }
+
+// MFMA tiles (w4a8_mx_tile_kernels.hip) over the experts with a.lo <= rows < a.hi: 256 x 256, 128 x 128, 64 x 256 or
+// 32 x 256.
+enum MxTile { MX_TILE_256, MX_TILE_128, MX_TILE_64, MX_TILE_32 };
+void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s);
 
 }  // namespace w4a8

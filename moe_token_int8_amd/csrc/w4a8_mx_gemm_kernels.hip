@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -18,10 +19,10 @@ namespace w4a8 {
 // Streaming kernel: few rows, bound by the read of the weights.
 //
 // A workgroup of 8 waves owns one tile of up to 16 MS rows of one expert and CT MFMA tiles of 16 weight columns (paired form:
-// gate columns in half of them, the matching up columns in the others) over all of K.  The waves share K in units of U steps:
-// wave w takes the units w, w + 8, ...; weights and activations go from memory to registers in the layout of the MFMA operands
-// (a step of a weight tile is one contiguous KiB), with no LDS and no barrier in the loop, and the loads of a wave's next unit
-// are in flight while it multiplies.  The 8 partial sums are added in wave order through LDS, so a call repeats bit for bit.
+// gate columns in half of them, the matching up columns in the others) over all of K.  The waves share the steps of 128 k: wave
+// w takes w, w + 8, ...; weights and activations go from memory to registers in the layout of the MFMA operands (a step of a
+// weight tile is one contiguous KiB), with no LDS and no barrier in the loop, two of a wave's steps in flight.  The 8 partial
+// sums are added in wave order through LDS, so a call repeats bit for bit.
 constexpr int MXS_WAVES = 8;
 
 template <int MT>
@@ -67,14 +68,12 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
 
 template <int FMT, bool PAIR, int MS, int CT, bool NT>
 __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
-    constexpr int U = 2;                                        // steps of a unit
     constexpr int COLS = PAIR ? CT * 8 : CT * 16;
     constexpr bool QUADS = !PAIR && CT == 4;                    // the scales of the 4 tiles are one word
+    constexpr int STEP_BYTES = FMT == W4A8_MX_FP4 ? 64 : 128;   // of an activation row
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, c16 = lane & 15;
-    const int units = (a.K1 + U - 1) / U;
-    const unsigned tile_bytes = unsigned(a.K1) * 1024u, quad_bytes = unsigned(a.K1) * 256u;
     for (unsigned item = blockIdx.x;; item += gridDim.x) {
         const int slot = int(item / unsigned(ncb)), cb = int(item - unsigned(slot) * unsigned(ncb));
         const TileRows tr = mx_find<16 * MS>(a, slot, lane);
@@ -82,108 +81,95 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
         if (expert < 0) return;                                 // uniform over the workgroup; no later slot has a tile
         const int rbeg = __builtin_amdgcn_readfirstlane(tr.rbeg), nrows = __builtin_amdgcn_readfirstlane(tr.rend) - rbeg;
 
-        // weights and their scales: descriptors that end with the expert's; offsets past them load zeros, which is what tiles
-        // past the last column and steps past the last of K take
+        // weights and their scales: descriptors that end with the expert's; tiles past the last column and steps past the last of K
+        // are given an offset past them and load zeros (steps of the loop are loaded and multiplied without a branch, which
+        // would cost copies of the operands; the activations of such a step are those of step 0)
         const uint8_t* wexp = a.W + size_t(expert) * a.expert_stride;
         const int width = PAIR ? 2 * a.N : a.N, ntiles = (width + 15) / 16;
         const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wexp), 0,
-                                                                            int(unsigned(ntiles) * tile_bytes), 0x00020000);
+                                                                            int(unsigned(ntiles) * unsigned(a.K1) * 1024u), 0x00020000);
         const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(wexp + a.scales_off), 0, int(unsigned((width + 63) / 64) * quad_bytes), 0x00020000);
-        constexpr unsigned NONE = 0x80000000u;
-        int tile[CT];
+            const_cast<uint8_t*>(wexp + a.scales_off), 0, int(unsigned((ntiles + 3) / 4) * unsigned(a.K1) * 256u), 0x00020000);
+        constexpr unsigned NONE = 0x80000000u;                  // codes end below it, so that a sum with a valid offset does not wrap
+        unsigned woff[CT], soff[QUADS ? 1 : CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-            tile[t] = PAIR ? cb * (CT / 2) + t % (CT / 2) + (t >= CT / 2 ? a.N / 16 : 0) : cb * CT + t;
-        const uint8_t* xrow[MS];
-        const uint8_t* srow[MS];
-        struct Unit {
-            v4i w[U][CT];
-            uint32_t sw[U][QUADS ? 1 : CT];
-            MxOperand<FMT> x[U][MS];
-            uint32_t sx[U][MS];
+        for (int t = 0; t < CT; ++t) {
+            const int own = PAIR ? cb * (CT / 2) + t % (CT / 2) : cb * CT + t;      // among the gate, or all, tiles
+            const int tile = PAIR && t >= CT / 2 ? own + a.N / 16 : own;
+            const bool there = own < (PAIR ? a.N / 16 : ntiles);
+            woff[t] = there ? unsigned(tile) * unsigned(a.K1) * 1024u + unsigned(lane) * 16u : NONE;
+            if (!QUADS) soff[QUADS ? 0 : t] = there ? unsigned(tile >> 2) * unsigned(a.K1) * 256u + unsigned(lane) * 4u + unsigned(tile & 3) : NONE;
+        }
+        if (QUADS) soff[0] = unsigned(cb) * unsigned(a.K1) * 256u + unsigned(lane) * 4u;
+        struct Step {
+            v4i w[CT];
+            uint32_t sw[QUADS ? 1 : CT];
+            MxOperand<FMT> x[MS];
+            uint32_t sx[MS];
         };
         // NT: the non-temporal hint, for calls that read more weights than the Infinity Cache holds.
-        auto load_w = [&](Unit& b, const int u) __attribute__((always_inline)) {
+        auto load_w = [&](Step& b, const int step) __attribute__((always_inline)) {
+            const unsigned at = step < a.K1 ? unsigned(step) * 1024u : NONE, sat = step < a.K1 ? unsigned(step) * 256u : NONE;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int step = u * U + i;
-                const bool in = step < a.K1;
+            for (int t = 0; t < CT; ++t)
+                b.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[t] + at, 0, NT ? 2 : 0);
 #pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    const bool there = in && (PAIR ? cb * (CT / 2) + t % (CT / 2) < a.N / 16 : tile[t] < ntiles);
-                    b.w[i][t] = __builtin_amdgcn_raw_buffer_load_b128(
-                        wr, there ? unsigned(tile[t]) * tile_bytes + unsigned(step) * 1024u + unsigned(lane) * 16u : NONE, 0, NT ? 2 : 0);
-                    if (!QUADS)
-                        b.sw[i][QUADS ? 0 : t] = __builtin_amdgcn_raw_buffer_load_b8(
-                            sr, there ? unsigned(tile[t] >> 2) * quad_bytes + unsigned(step) * 256u + unsigned(lane) * 4u + unsigned(tile[t] & 3)
-                                      : NONE, 0, 0);
-                }
-                if (QUADS)
-                    b.sw[i][0] = __builtin_amdgcn_raw_buffer_load_b32(
-                        sr, in ? unsigned(cb) * quad_bytes + unsigned(step) * 256u + unsigned(lane) * 4u : NONE, 0, 0);
+            for (int t = 0; t < (QUADS ? 1 : CT); ++t)
+                b.sw[t] = QUADS ? uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, soff[t] + sat, 0, 0))
+                                : uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, soff[t] + sat, 0, 0));
+        };
+        const uint8_t* xrow[MS];
+        const uint8_t* srow[MS];
+        auto load_x = [&](Step& b, const int s) __attribute__((always_inline)) {
+            const int step = s < a.K1 ? s : 0;
+#pragma unroll
+            for (int ms = 0; ms < MS; ++ms) {
+                const uint8_t* p = xrow[ms] + unsigned(step) * unsigned(STEP_BYTES);
+                b.x[ms].p[0] = *reinterpret_cast<const v4i*>(p);
+                if constexpr (FMT != W4A8_MX_FP4) b.x[ms].p[1] = *reinterpret_cast<const v4i*>(p + 64);
+                b.sx[ms] = srow[ms][unsigned(step) * 4u];
             }
         };
-        auto load_x = [&](Unit& b, const int u) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const unsigned step = unsigned(min(u * U + i, a.K1 - 1));   // past the last step the weights are zero
-#pragma unroll
-                for (int ms = 0; ms < MS; ++ms) {
-                    if constexpr (FMT == W4A8_MX_FP4) {
-                        b.x[i][ms].p[0] = *reinterpret_cast<const v4i*>(xrow[ms] + step * 64u + unsigned(q) * 16u);
-                    } else {
-                        b.x[i][ms].p[0] = *reinterpret_cast<const v4i*>(xrow[ms] + step * 128u + unsigned(q) * 16u);
-                        b.x[i][ms].p[1] = *reinterpret_cast<const v4i*>(xrow[ms] + step * 128u + 64u + unsigned(q) * 16u);
-                    }
-                    b.sx[i][ms] = srow[ms][step * 4u + unsigned(q)];
-                }
-            }
-        };
+        Step s0, s1;
+        load_w(s0, wave);
+        load_w(s1, wave + MXS_WAVES);
         // activation rows of this lane; rows past the tile repeat its first row (their sums are not stored)
-        int src[MS];
 #pragma unroll
         for (int ms = 0; ms < MS; ++ms) {
-            const int row = ms * 16 + c16;
-            src[ms] = mx_src(a, rbeg + (row < nrows ? row : 0));
+            const int row = ms * 16 + c16, src = mx_src(a, rbeg + (row < nrows ? row : 0));
+            const size_t r = size_t(src < 0 ? 0 : src);
+            xrow[ms] = a.X + r * a.rowb + unsigned(q) * 16u;
+            srow[ms] = a.sx + r * (size_t(a.K1) * 4) + unsigned(q);
         }
-        Unit cur, next;
-        if (wave < units) load_w(cur, wave);
-#pragma unroll
-        for (int ms = 0; ms < MS; ++ms) {
-            const size_t r = size_t(src[ms] < 0 ? 0 : src[ms]);
-            xrow[ms] = a.X + r * a.rowb;
-            srow[ms] = a.sx + r * size_t(a.K1) * 4;
-        }
-        if (wave < units) load_x(cur, wave);
+        load_x(s0, wave);
+        load_x(s1, wave + MXS_WAVES);
 
         v4f acc[CT][MS];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
 #pragma unroll
             for (int ms = 0; ms < MS; ++ms) acc[t][ms] = v4f{};
-        for (int u = wave; u < units; u += MXS_WAVES) {
-            const bool more = u + MXS_WAVES < units;
-            if (more) {
-                load_w(next, u + MXS_WAVES);
-                load_x(next, u + MXS_WAVES);
-            }
+        auto multiply = [&](const Step& b) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+            for (int ms = 0; ms < MS; ++ms) {
+                if constexpr (QUADS) {
+                    acc[0][ms] = mx_mfma<FMT, 0>(b.w[0], b.x[ms], acc[0][ms], b.sw[0], b.sx[ms]);
+                    acc[1][ms] = mx_mfma<FMT, 1>(b.w[1], b.x[ms], acc[1][ms], b.sw[0], b.sx[ms]);
+                    acc[2][ms] = mx_mfma<FMT, 2>(b.w[2], b.x[ms], acc[2][ms], b.sw[0], b.sx[ms]);
+                    acc[3][ms] = mx_mfma<FMT, 3>(b.w[3], b.x[ms], acc[3][ms], b.sw[0], b.sx[ms]);
+                } else {
 #pragma unroll
-                for (int ms = 0; ms < MS; ++ms) {
-                    if constexpr (QUADS) {
-                        acc[0][ms] = mx_mfma<FMT, 0>(cur.w[i][0], cur.x[i][ms], acc[0][ms], cur.sw[i][0], cur.sx[i][ms]);
-                        acc[1][ms] = mx_mfma<FMT, 1>(cur.w[i][1], cur.x[i][ms], acc[1][ms], cur.sw[i][0], cur.sx[i][ms]);
-                        acc[2][ms] = mx_mfma<FMT, 2>(cur.w[i][2], cur.x[i][ms], acc[2][ms], cur.sw[i][0], cur.sx[i][ms]);
-                        acc[3][ms] = mx_mfma<FMT, 3>(cur.w[i][3], cur.x[i][ms], acc[3][ms], cur.sw[i][0], cur.sx[i][ms]);
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-                            acc[t][ms] = mx_mfma<FMT, 0>(cur.w[i][t], cur.x[i][ms], acc[t][ms], cur.sw[i][t], cur.sx[i][ms]);
-                    }
+                    for (int t = 0; t < CT; ++t) acc[t][ms] = mx_mfma<FMT, 0>(b.w[t], b.x[ms], acc[t][ms], b.sw[t], b.sx[ms]);
                 }
-            if (more) cur = next;
+            }
+        };
+        for (int s = wave; s < a.K1; s += 2 * MXS_WAVES) {
+            multiply(s0);
+            load_w(s0, s + 2 * MXS_WAVES);
+            load_x(s0, s + 2 * MXS_WAVES);
+            multiply(s1);
+            load_w(s1, s + 3 * MXS_WAVES);
+            load_x(s1, s + 3 * MXS_WAVES);
         }
 
         // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
@@ -215,7 +201,7 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
                     if (in && mx_src(a, rbeg + row) >= 0) {
                         const v4f g = total(at), u = total(at + ITEMS / 2);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) h[k] = silu_gate(g[k]) * u[k];
+                        for (int k = 0; k < 4; ++k) h[k] = mx_silu(g[k]) * u[k];
                     }
                     const bool there = o < OUT && row < nrows && cb * COLS + b * 32 < a.N;
                     mx_store_block(a, rbeg + row, (cb * COLS) / 32 + b, j, h, there);
@@ -230,7 +216,7 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
             if constexpr (PAIR) {
                 const v4f up = total(o + ITEMS / 2);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = silu_gate(y[k]) * up[k];
+                for (int k = 0; k < 4; ++k) y[k] = mx_silu(y[k]) * up[k];
             }
             if (mx_src(a, rbeg + row) < 0) y = v4f{};
             mx_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), y);
@@ -253,16 +239,63 @@ static void launch_stream_t(const MxArgs& a, long long slots, hipStream_t s) {
     mx_stream_kernel<FMT, PAIR, MS, CT, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
 }
 
+// Which kernel a call takes: the least of five estimates, in us.  The host knows rows and E, not the experts' rows: of E experts
+// about E (1 - exp(-rows / E)) have any, and each ends in a row tile that is half empty.  Streaming tiles: 512 workgroups at a time
+// take o and l a step.  MFMA tiles: `per` workgroups share a compute unit, a step takes l, or thr for each of them.  Either reads
+// the weights at bw TB/s.  Fitted to 282 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, K 768 .. 14336), of
+// which the choice loses 5 % in the mean against the best of all, 38 % at worst.  Measured, us, streams of 16 and 32 rows / tiles of
+// 32 / 64 / 256 rows: 16 x 4096 x 14336 fp8 9.0, 9.9 / 19.6 / 19.0 / 27.7; 128 x 14336 x 4096 fp4 26, 21 / 40 / 45 / 58; 2 rows for each
+// of 256 experts, 2048 x 7168 fp8 397, 335 / 278 / 277 / 374; 64 rows for each of 64, 4096 x 2816 fp8 299, 254 / 133 / 125 / 135;
+// 8192 x 4096 x 14336 fp4 257 with 256 rows.
+enum MxKernel { MXK_STREAM16, MXK_STREAM32, MXK_TILE32, MXK_TILE64, MXK_TILE256, MXK_KERNELS };
+
+static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
+    struct Rate {
+        int rows, cols, per;
+        double o, l, thr, bw;
+    };
+    static const Rate rates[2][MXK_KERNELS] = {
+        {{16, 64, 2, 6.3, 0.098, 0, 4.1}, {32, 64, 2, 5.2, 0.196, 0, 3.8}, {32, 256, 4, 1.2, 0.43, 0.41, 5.1}, {64, 256, 3, 1.1, 0.47, 0.475, 4.8}, {256, 256, 1, 6.0, 0.73, 0, 3.8}},
+        {{16, 64, 2, 5.6, 0.079, 0, 3.9}, {32, 64, 2, 4.1, 0.151, 0, 3.9}, {32, 256, 4, 1.0, 0.12, 0.31, 5.2}, {64, 256, 3, 1.7, 0.14, 0.35, 4.9}, {256, 256, 1, 5.9, 0.54, 0, 4.3}}};
+    const double rows = a.rows, E = a.E, width = pair ? 2.0 * a.N : a.N, steps = a.K1;
+    const double active = E > 1 ? std::min(rows, E * (1 - std::exp(-rows / E))) : 1;
+    const double bytes = active * width * steps * 68;           // 128 k of a column
+    MxKernel best = MXK_STREAM16;
+    double least = 1e300;
+    for (int v = 0; v < MXK_KERNELS; ++v) {
+        const Rate& r = rates[fp4][v];
+        const double rt = E > 1 ? std::max(active, rows / r.rows + 0.5 * active) : std::ceil(rows / r.rows), n = rt * std::ceil(width / r.cols);
+        double us;
+        if (v <= MXK_STREAM32) {
+            us = std::max(1.0, n / 512) * (r.o + r.l * steps);
+        } else {
+            const double co = n / 256, full = co / r.per;
+            const double rounds = full < 1 ? 1 : full < 4 ? std::ceil(full) : full + 0.5;
+            us = 4 + rounds * (r.o + steps * std::max(r.l, r.thr * std::min(std::max(co, 1.0), double(r.per))));
+        }
+        us = std::max(us, 4 + bytes / (r.bw * 1e6));
+        if (us < least) least = us, best = MxKernel(v);
+    }
+    return best;
+}
+
 template <int FMT, bool PAIR>
 static const char* launch_mx(MxArgs a, hipStream_t s) {
     const long long rows = a.rows, E = a.E;
     a.lo = 1, a.hi = 0x7fffffff;
-    if (rows <= 16) {
-        launch_stream_t<FMT, PAIR, 1, 4, false>(a, std::min(E, rows), s);
+    // the tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
+    const bool near = !a.gather || (long long)a.src_rows * a.rowb < 0xe0000000ll;
+    const MxKernel v = choose_mx(a, FMT == W4A8_MX_FP4, PAIR);
+    if (v == MXK_STREAM16) {
+        launch_stream_t<FMT, PAIR, 1, 4, false>(a, rows / 16 + std::min(E, rows), s);
         return "mx_stream_kernel (16-row tiles)";
     }
-    launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);
-    return "mx_stream_kernel (32-row tiles)";
+    if (v == MXK_STREAM32 || !near) {
+        launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);
+        return "mx_stream_kernel (32-row tiles)";
+    }
+    launch_mx_tile(a, FMT, PAIR, v == MXK_TILE32 ? MX_TILE_32 : v == MXK_TILE64 ? MX_TILE_64 : MX_TILE_256, s);
+    return v == MXK_TILE32 ? "mx_tile_kernel (32 x 256)" : v == MXK_TILE64 ? "mx_tile_kernel (64 x 256)" : "mx_tile_kernel (256 x 256)";
 }
 
 // out[t] = sum_j w[t, j] Yd[inv[t, j]] in float32, j ascending, rounded once: the experts' outputs stay in float32 (rounded to

@@ -1,0 +1,490 @@
+// Products of MX activations with packed MXFP4 weights: the kernel for many rows (MFMA tiles), dense and by expert.
+//
+// Source: P1 "Kimi 2.7 MoE: from 4-bit storage to INT8 (W4A8)" (pwwt.cn), section 4.4 step 4 (the grouped expert GEMM over
+// router-sorted rows, "the performance key") and section 5.1 (tiles matched to the MFMA operands).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "w4a8_mx_gemm.h"
+
+namespace w4a8 {
+
+// Persistent workgroups of WM x WN waves walk over tiles of 16 MT WM rows x 64 WN weight columns (paired form: half of them gate,
+// the matching half up columns).  Wave (wm, wn) owns 16 MT rows and 64 columns: 4 MT accumulators of 4 a lane.
+//
+// The packed weights are in operand order, so they go from memory straight to registers, 4 KiB a wave and step of 128 k, two
+// steps ahead.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4, one of fp8), copied
+// without registers (buffer_load ... lds), three stages deep, with a stage's scale bytes behind its codes.  LDS then carries a
+// third of what it would with both operands (64 + 16 KiB of the 128 a CU moves in the 1024 cycles of a 256 x 256 step of fp4).
+//
+// vmcnt counts in the order of issue, so what is issued when is fixed: a step requests the weights of the step after the next;
+// the first step of a stage then requests the activations of the stage after the next.  One barrier a stage, before the last
+// group of MFMAs, when the stage's last operands are in registers: behind it the next stage is whole and this one is free.
+constexpr int MXT_ROW = 128;                                    // bytes of a row in a stage
+constexpr int MXT_MAX_E = 1024;
+constexpr int MXT_PANEL = 4;                                    // row tiles of a panel of consecutive tiles
+
+#define LDS __attribute__((address_space(3)))
+using lds_ptr = LDS uint8_t*;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_buffer(const uint8_t* base, size_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, int(unsigned(bytes < 0xffffffffu ? bytes : 0xffffffffu)),
+                                             0x00020000);
+}
+
+// 16 or 4 bytes a lane from memory to LDS, lane after lane from dst on.  (The whole offset is in the register operand: a scalar
+// offset is not part of the range check.)
+__device__ __forceinline__ void mx_copy16(__amdgpu_buffer_rsrc_t src, unsigned off, lds_ptr dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LDS void*)dst, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void mx_copy4(__amdgpu_buffer_rsrc_t src, unsigned off, lds_ptr dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LDS void*)dst, 4, off, 0, 0, 0);
+}
+
+// Waits until at most NEWER memory operations of this wave are in flight and its LDS reads are done, then for every wave.
+template <int NEWER>
+__device__ __forceinline__ void mx_barrier() {
+    static_assert(NEWER < 64, "the counter has 6 bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((NEWER & 15) | ((NEWER >> 4) << 14) | (7 << 4) | (0 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// v, without what the compiler knows of it: what is derived from it is computed there and not kept across the MFMA loop.
+__device__ __forceinline__ int mx_opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Chunk c (16 bytes) of row r sits at position c ^ mx_swizzle(r): 16 rows read at one chunk lie in distinct banks.
+__device__ __forceinline__ int mx_swizzle(int r) { return (r >> 1) & 7; }
+
+// Exchanges the odd 16-lane rows of a with the even ones of b.
+__device__ __forceinline__ void mx_swap16(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0], b = r[1];
+}
+// Maximum over the four lanes l % 16, 16 + l % 16, ...
+__device__ __forceinline__ uint32_t mx_max_rows(uint32_t m) {
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max(uint32_t(a[0]), uint32_t(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max(uint32_t(b[0]), uint32_t(b[1]));
+}
+
+template <int FMT, bool PAIR, int WM, int WN, int MT>
+__global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FMT != W4A8_MX_FP4) && FMT != MX_FP8_EXACT ? 4 : 3) void mx_tile_kernel(MxArgs a) {
+    constexpr bool FP4 = FMT == W4A8_MX_FP4;
+    constexpr int THREADS = 64 * WM * WN, BM = 16 * MT * WM;
+    constexpr int COLS = PAIR ? 32 * WN : 64 * WN;              // columns of Y
+    constexpr int SPS = FP4 ? 2 : 1;                            // steps of a stage
+    constexpr int CODES = BM * MXT_ROW, STAGE = CODES + THREADS * 4;
+    constexpr int SB = 4 * SPS;                                 // scale bytes of a row in a stage
+    constexpr int COPIES = BM * 8 / THREADS;                    // 16-byte copies of a thread in a stage
+    constexpr int G = FP4 ? MT / 2 : MT == 8 ? 2 : 1, NG = MT / G;      // row tiles of a group, groups of a step
+    constexpr int FILL = COPIES + 1, WL = PAIR ? 8 : 5;         // memory operations of a stage's copies, of a step's weights
+    constexpr int LIST = 64;                                    // tiles looked up at a time
+    static_assert(NG % 2 == 0 && COPIES * THREADS == BM * 8 && BM * SB <= THREADS * 4, "shapes");
+    __shared__ __align__(1024) uint8_t stage0[STAGE];
+    __shared__ __align__(1024) uint8_t stage1[STAGE];
+    __shared__ __align__(1024) uint8_t stage2[STAGE];
+    __shared__ int4 list[LIST];                                 // tiles of this workgroup: expert, first row, rows, column block
+    __shared__ int first[MXT_MAX_E + 1];                        // row tiles before expert e
+    __shared__ int entries[BM];                                 // gather entries of the next tile's rows
+    __shared__ int wsum[WM * WN];
+    const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int q = lane >> 4, c16 = lane & 15, wm = wave / WN, wn = wave % WN;
+    const int ncb = (a.N + COLS - 1) / COLS;
+    const int stages = (a.K1 + SPS - 1) / SPS;
+    const bool f32 = !PAIR && a.out == W4A8_F32;
+
+    // row tiles of every expert of this launch, as a prefix sum
+    {
+        constexpr int EPT = MXT_MAX_E / THREADS;
+        const int tid = threadIdx.x;
+        int t[EPT], incl = 0;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int e = EPT * tid + i;
+            const int cnt = e < a.E ? mx_row_last(a, e) - mx_row_first(a, e) : 0;
+            t[i] = cnt >= a.lo && cnt < a.hi ? (cnt + BM - 1) / BM : 0;
+            incl += t[i];
+        }
+        int excl = -incl;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int y = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 63) wsum[wave] = incl;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) incl += wsum[w];
+        excl += incl;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            if (EPT * tid + i <= a.E) first[EPT * tid + i] = excl;
+            excl += t[i];
+        }
+        if (a.E == MXT_MAX_E && tid == THREADS - 1) first[MXT_MAX_E] = incl;
+        __syncthreads();
+    }
+    const long long total = (long long)first[a.E] * ncb;
+    // blocks go to the 8 XCDs in turn: the blocks of one XCD take neighbouring tiles, which share rows or columns in its L2
+    const int nblk = int(gridDim.x), per = nblk / 8;
+    const int rank = nblk % 8 ? int(blockIdx.x) : (int(blockIdx.x) % 8) * per + int(blockIdx.x) / 8;
+    const int mine = rank < total ? int((total - rank + nblk - 1) / nblk) : 0;      // tiles of this workgroup
+    if (mine == 0) return;
+
+    // the tiles from k0 on of this workgroup; all threads, between barriers
+    auto look_up = [&](const int k0) __attribute__((always_inline)) {
+        const int tid = mx_opaque(int(threadIdx.x));
+        if (tid < LIST && k0 + tid < mine) {
+            const long long t = rank + (long long)(k0 + tid) * nblk;
+            const int trow = int(t / ncb);
+            int lo = 0, hi = a.E;                               // expert: the last one whose first tile is not after trow
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= trow) lo = mid;
+                else hi = mid;
+            }
+            const int f0 = first[lo], rt = first[lo + 1] - f0, in_e = int(t - (long long)f0 * ncb);
+            const int panel = in_e / (MXT_PANEL * ncb), j = in_e - panel * MXT_PANEL * ncb;
+            const int rp = min(MXT_PANEL, rt - panel * MXT_PANEL);
+            const int cb = j / rp, r0 = mx_row_first(a, lo) + (panel * MXT_PANEL + j - cb * rp) * BM;
+            list[tid] = make_int4(lo, r0, min(BM, mx_row_last(a, lo) - r0), cb);
+        }
+        __syncthreads();
+    };
+
+    // What a tile reads.  Descriptors end with the data: rows past the tile's last and weight tiles past the last column are given
+    // an offset past everything and load zeros.  The step goes into the weights' scalar offset, which the range check leaves
+    // out: steps past the last one, which are requested but not used, repeat it.
+    constexpr unsigned NONE = 0xf0000000u;
+    unsigned xoff[COPIES], soff, woff[4], wsoff[PAIR ? 4 : 1];
+    __amdgpu_buffer_rsrc_t xr, sr, wr, wsr;
+    v4i w[3][4];
+    uint32_t sw[3][PAIR ? 4 : 1];
+
+    auto load_w_part = [&](const int set, const int step, const int part) __attribute__((always_inline)) {
+        const int k = min(step, a.K1 - 1);
+        if (part < 4) w[set][part & 3] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[part & 3], k * 1024, 0);
+        else sw[set][PAIR ? part & 3 : 0] =
+                 PAIR ? uint32_t(__builtin_amdgcn_raw_buffer_load_b8(wsr, wsoff[PAIR ? part & 3 : 0], k * 256, 0))
+                      : uint32_t(__builtin_amdgcn_raw_buffer_load_b32(wsr, wsoff[0], k * 256, 0));
+    };
+    auto load_w = [&](const int set, const int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int part = 0; part < WL; ++part) load_w_part(set, step, part);
+    };
+    auto copy_part = [&](const lds_ptr st, const int s, const int part) __attribute__((always_inline)) {
+        const bool in = s < stages;
+        if (part < COPIES)
+            mx_copy16(xr, xoff[part < COPIES ? part : 0] + (in ? unsigned(s) * MXT_ROW : 0xc0000000u),
+                      st + (part * (THREADS / 8) + wave * 8) * MXT_ROW);
+        else
+            mx_copy4(sr, soff + (in ? unsigned(s) * SB : 0xc0000000u), st + CODES + wave * 256);
+    };
+    auto copies = [&](const lds_ptr st, const int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int part = 0; part < FILL; ++part) copy_part(st, s, part);
+    };
+    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1, st2 = (lds_ptr)stage2;
+
+    // gather entries of a tile's rows, copied to LDS a tile ahead
+    auto request_rows = [&](const int4 g) __attribute__((always_inline)) {
+        if (a.gather && wave < (BM + 63) / 64)
+            mx_copy4(mx_buffer(reinterpret_cast<const uint8_t*>(a.gather + g.y), size_t(g.z) * 4),
+                     unsigned(mx_opaque(int(threadIdx.x))) * 4u, (lds_ptr)((LDS int*)entries + wave * 64));
+    };
+    auto source = [&](const int g) __attribute__((always_inline)) {    // row of X, or -1
+        if (!a.gather) return g;
+        const int t = g < 0 ? -1 : int(unsigned(g) / unsigned(a.topk));
+        return t < a.src_rows ? t : -1;
+    };
+    // bit m of dead: this lane's row 16 m + c16 of the wave has a gather entry that names no row (its outputs are zeros)
+    unsigned dead = 0, next_dead = 0;
+    auto begin = [&](const int4 g) __attribute__((always_inline)) {
+        const int tid = mx_opaque(int(threadIdx.x)), lane = tid & 63;
+        const uint8_t* wexp = a.W + size_t(g.x) * a.expert_stride;
+        const int width = PAIR ? 2 * a.N : a.N, ntiles = (width + 15) / 16;
+        wr = mx_buffer(wexp, size_t(ntiles) * size_t(a.K1) * 1024);
+        wsr = mx_buffer(wexp + a.scales_off, size_t((ntiles + 3) / 4) * size_t(a.K1) * 256);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int own = PAIR ? g.w * 2 * WN + wn * 2 + (n & 1) : g.w * 4 * WN + wn * 4 + n;  // among the gate, or all, tiles
+            const int t = PAIR && n >= 2 ? own + a.N / 16 : own;
+            const bool there = own < (PAIR ? a.N / 16 : ntiles);
+            woff[n] = there ? unsigned(t) * (unsigned(a.K1) * 1024u) + unsigned(lane) * 16u : NONE;
+            if (PAIR) wsoff[PAIR ? n : 0] = there ? unsigned(t >> 2) * (unsigned(a.K1) * 256u) + unsigned(lane) * 4u + unsigned(t & 3) : NONE;
+            else if (n == 0) wsoff[0] = there ? unsigned(t >> 2) * (unsigned(a.K1) * 256u) + unsigned(lane) * 4u : NONE;
+        }
+        const size_t srow = size_t(a.K1) * 4, base = a.gather ? 0 : size_t(g.y), nrow = size_t(a.gather ? a.src_rows : g.z);
+        xr = mx_buffer(a.X + base * a.rowb, nrow * a.rowb);
+        sr = mx_buffer(a.sx + base * srow, nrow * srow);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            const int row = i * (THREADS / 8) + (tid >> 3), chunk = (lane & 7) ^ mx_swizzle(row);
+            const int src = max(source(a.gather ? entries[row] : row), 0);
+            xoff[i] = row < g.z ? unsigned(src) * a.rowb + unsigned(chunk) * 16u : NONE;
+        }
+        {
+            const int row = FP4 ? tid >> 1 : tid;
+            const int src = row < BM ? max(source(a.gather ? entries[min(row, BM - 1)] : row), 0) : 0;
+            soff = row < g.z ? unsigned(src) * unsigned(srow) + (FP4 ? unsigned(tid & 1) * 4u : 0u) : NONE;
+        }
+        if (a.gather) {
+            next_dead = 0;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int row = wm * (16 * MT) + m * 16 + (lane & 15);
+                if (row < g.z && source(entries[row]) < 0) next_dead |= 1u << m;
+            }
+        }
+        // in this order, which the waits below count on
+        __builtin_amdgcn_sched_barrier(0);
+        if (!FP4) load_w(0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        copies(st0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (FP4) load_w(0, 0);
+        else load_w(1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        copies(st1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (FP4) load_w(1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int NEWER_FIRST = FP4 ? 2 * WL + FILL : WL + FILL;     // operations behind the copies of stage 0 at the start
+    // behind those of stage s + 1 at the barrier of stage s, which stands before the last group of its last step
+    constexpr int OPS = FP4 ? WL : WL + FILL;                       // of that step, spread over its row tiles
+    constexpr int NEWER = (FP4 ? 2 * WL + FILL : 0) + (MT - G) * OPS / MT;
+
+    // operands in LDS: byte offsets of this lane in a stage, for the halves of 64 bytes
+    int xat[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) xat[h] = mx_opaque((wm * (16 * MT) + c16) * MXT_ROW + ((4 * h + q) ^ mx_swizzle(c16)) * 16);
+    const int sat = mx_opaque(CODES + (wm * (16 * MT) + c16) * SB + q);
+    MxOperand<FMT> x[2][G];
+    uint32_t sx[2][G];
+    auto read_tile = [&](const int buf, const lds_ptr st, const int h, const int m) __attribute__((always_inline)) {
+        const int i = m % G;
+        if constexpr (FP4) {
+            x[buf][i].p[0] = *(const LDS v4i*)(st + xat[h] + m * 2048);
+        } else {
+            x[buf][i].p[0] = *(const LDS v4i*)(st + xat[0] + m * 2048);
+            x[buf][i].p[FP4 ? 0 : 1] = *(const LDS v4i*)(st + xat[1] + m * 2048);
+        }
+        sx[buf][i] = *(const LDS uint8_t*)(st + sat + m * 16 * SB + (FP4 ? 4 * h : 0));
+    };
+
+    constexpr int STORES16 = PAIR ? MT : 2 * MT;                // of a wave's regular tile in 16 bits
+    bool behind_stores = false;
+
+    look_up(0);
+    auto uniform = [&](int4 v) __attribute__((always_inline)) {
+        return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                         __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+    };
+    int4 g = uniform(list[0]);
+    request_rows(g);
+    mx_barrier<0>();
+    begin(g);
+    for (int k = 0;;) {
+        const int4 cur = g;
+        dead = next_dead;
+        if (behind_stores) mx_barrier<NEWER_FIRST + STORES16>();
+        else mx_barrier<NEWER_FIRST>();
+        // the next tile, and its gather entries: requested here, first needed at the end of this tile
+        if (++k < mine) {
+            if (k % LIST == 0) look_up(k);
+            g = uniform(list[k % LIST]);
+            request_rows(g);
+        }
+        if (wm * (16 * MT) < cur.z) {
+            v4f acc[4][MT];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[n][m] = v4f{};
+#pragma unroll
+            for (int m = 0; m < G; ++m) read_tile(0, st0, 0, m);
+            for (int s3 = 0;; s3 += 3) {
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    const lds_ptr st = u == 0 ? st0 : u == 1 ? st1 : st2, next = u == 0 ? st1 : u == 1 ? st2 : st0,
+                                  far = u == 0 ? st2 : u == 1 ? st0 : st1;
+#pragma unroll
+                    for (int h = 0; h < SPS; ++h) {
+                        // A step: for each row tile the operands of a row tile of the next group are read, a share of the step's memory
+                        // operations is issued, and 4 MFMAs follow.  (Issued together at the start of the step, the memory operations
+                        // of all waves meet: 4096 x 14336 x 4096 in fp4 113 us in place of 104.)
+                        const int step = (s3 + u) * SPS + h, set = (u * SPS + h) % 3;
+                        const int ops = h == 0 ? WL + FILL : WL;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int gr = m / G, i = m % G, b = gr & 1;
+                            const bool last = gr == NG - 1 && h == SPS - 1;
+                            if (last && i == 0) mx_barrier<NEWER>();
+                            if (gr < NG - 1) read_tile(b ^ 1, st, h, m + G);
+                            else if (!last) read_tile(0, st, 1, i);
+                            else read_tile(0, next, 0, i);
+#pragma unroll
+                            for (int op = m * ops / MT; op < (m + 1) * ops / MT; ++op) {
+                                if (op < WL) load_w_part((set + 2) % 3, step + 2, op);
+                                else copy_part(far, s3 + u + 2, op - WL);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                            if constexpr (PAIR) {
+#pragma unroll
+                                for (int n = 0; n < 4; ++n)
+                                    acc[n][m] = mx_mfma<FMT, 0>(w[set][n], x[b][i], acc[n][m], sw[set][PAIR ? n : 0], sx[b][i]);
+                            } else {
+                                acc[0][m] = mx_mfma<FMT, 0>(w[set][0], x[b][i], acc[0][m], sw[set][0], sx[b][i]);
+                                acc[1][m] = mx_mfma<FMT, 1>(w[set][1], x[b][i], acc[1][m], sw[set][0], sx[b][i]);
+                                acc[2][m] = mx_mfma<FMT, 2>(w[set][2], x[b][i], acc[2][m], sw[set][0], sx[b][i]);
+                                acc[3][m] = mx_mfma<FMT, 3>(w[set][3], x[b][i], acc[3][m], sw[set][0], sx[b][i]);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if (step + 1 >= a.K1) goto done;
+                    }
+                }
+            }
+        done:;
+            const int l = mx_opaque(lane), c16 = l & 15, q = l >> 4;
+            // every stage has been read, and what was requested past the last step (nothing is read there) has ended: the next
+            // tile's copies start before this one's outputs are stored
+            mx_barrier<0>();
+            if (k < mine) begin(g);
+            const int r0 = wm * (16 * MT);
+            const unsigned gone = dead;
+            auto value = [&](const int n, const int m) __attribute__((always_inline)) {
+                v4f y = acc[n][m];
+                if constexpr (PAIR) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = mx_silu(y[i]) * acc[n + (PAIR ? 2 : 0)][m][i];
+                }
+                return gone >> m & 1 ? v4f{} : y;
+            };
+            const unsigned es = f32 ? 4u : 2u;
+            const bool regular = !(PAIR && a.Hq) && a.ldy < (size_t(1) << 21) && ((a.N & (f32 ? 3 : 7)) == 0 || (cur.w + 1) * COLS <= a.N);
+            const unsigned pitch = unsigned(a.ldy) * es;
+            const int colw = cur.w * COLS + wn * (PAIR ? 32 : 64);  // first column of the wave
+            if (PAIR && a.Hq) {
+                const size_t bpr = size_t(mx_kp(a.N) / 32), block = size_t(colw / 32);
+                const bool have = colw < a.N, last = have && colw + 32 >= a.N, fp4 = a.h_fmt == W4A8_MX_FP4;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    v4f h0 = value(0, m), h1 = value(1, m);
+                    if (colw + 16 >= a.N) h1 = v4f{};           // a last block of 16 columns
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = max(top, max(__float_as_uint(h0[i]) & 0x7fffffffu, __float_as_uint(h1[i]) & 0x7fffffffu));
+                    top = mx_max_rows(top);
+                    const uint32_t byte = fp4 ? mx_scale_byte<W4A8_MX_FP4>(top) : mx_scale_byte<W4A8_MX_FP8>(top);
+                    const float up = byte == 255u ? 0.0f : mx_up(byte);
+                    uint32_t c0, c1;
+                    if (fp4) c0 = mx_fp4x4(h0[0] * up, h0[1] * up, h0[2] * up, h0[3] * up), c1 = mx_fp4x4(h1[0] * up, h1[1] * up, h1[2] * up, h1[3] * up);
+                    else c0 = mx_fp8x4(h0[0] * up, h0[1] * up, h0[2] * up, h0[3] * up), c1 = mx_fp8x4(h1[0] * up, h1[1] * up, h1[2] * up, h1[3] * up);
+                    if (byte == 255u) c0 = 0u, c1 = 0u;
+                    mx_swap16(c0, c1);                          // 8 neighbouring columns: tile q % 2, half q / 2
+                    const int row = r0 + m * 16 + c16, at8 = (q & 1) * 2 + (q >> 1);
+                    if (row >= cur.z || !have) continue;
+                    const size_t at = size_t(cur.y + row) * bpr + block;
+                    if (fp4) *reinterpret_cast<uint32_t*>(a.Hq + at * 16 + at8 * 4) = c0 | (c1 << 16);
+                    else *reinterpret_cast<uint2*>(a.Hq + at * 32 + at8 * 8) = make_uint2(c0, c1);
+                    if (q == 0) a.sh[at] = uint8_t(byte);
+                    if (last) {
+                        const int bytes = fp4 ? 16 : 32;
+                        for (size_t b = block + 1; b < bpr; ++b) {
+                            uint8_t* p = a.Hq + (size_t(cur.y + row) * bpr + b) * bytes + q * (bytes / 4);
+                            *reinterpret_cast<uint32_t*>(p) = 0u;
+                            if (!fp4) *reinterpret_cast<uint32_t*>(p + 4) = 0u;
+                            if (q == 0) a.sh[size_t(cur.y + row) * bpr + b] = 0;
+                        }
+                    }
+                }
+            } else if (!regular) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int row = r0 + m * 16 + c16;
+#pragma unroll
+                    for (int n = 0; n < (PAIR ? 2 : 4); ++n) {
+                        const int col = colw + n * 16 + 4 * q;
+                        const v4f y = value(n, m);
+                        if (row < cur.z && col < a.N) mx_store(a, size_t(cur.y + row) * a.ldy + col, min(4, a.N - col), y);
+                    }
+                }
+            } else {
+                // stores of 16 bytes that exist whole or not at all: one each, dropped by the descriptor where they do not
+                const __amdgpu_buffer_rsrc_t yr = mx_buffer(static_cast<const uint8_t*>(a.Y) + size_t(cur.y) * a.ldy * es,
+                                                            size_t(cur.z - 1) * pitch + size_t(a.N) * es);
+                if (f32) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int n = 0; n < (PAIR ? 2 : 4); ++n) {
+                            const int col = colw + n * 16 + 4 * q;
+                            const unsigned off = col < a.N ? unsigned(r0 + m * 16 + c16) * pitch + unsigned(col) * 4u : NONE;
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, value(n, m)), yr, off, 0, 0);
+                        }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int n = 0; n < (PAIR ? 2 : 4); n += 2) {
+                            const v4f y0 = value(n, m), y1 = value(n + 1, m);
+                            const bool h = a.out == W4A8_F16;
+                            uint32_t a0 = h ? f32_to_f16_pair(y0[0], y0[1]) : f32_to_bf16_pair(y0[0], y0[1]);
+                            uint32_t a1 = h ? f32_to_f16_pair(y0[2], y0[3]) : f32_to_bf16_pair(y0[2], y0[3]);
+                            uint32_t b0 = h ? f32_to_f16_pair(y1[0], y1[1]) : f32_to_bf16_pair(y1[0], y1[1]);
+                            uint32_t b1 = h ? f32_to_f16_pair(y1[2], y1[3]) : f32_to_bf16_pair(y1[2], y1[3]);
+                            mx_swap16(a0, b0);                  // 8 neighbouring columns: tile n + q % 2, half q / 2
+                            mx_swap16(a1, b1);
+                            const int col = colw + (n + (q & 1)) * 16 + (q >> 1) * 8;
+                            const unsigned off = col < a.N ? unsigned(r0 + m * 16 + c16) * pitch + unsigned(col) * 2u : NONE;
+                            __builtin_amdgcn_raw_buffer_store_b128(v4i{int(a0), int(a1), int(b0), int(b1)}, yr, off, 0, 0);
+                        }
+                }
+            }
+            if (k == mine) break;
+            behind_stores = regular && !f32;
+        } else {                                                // a wave below the last row only copies
+            for (int s = 0; s < stages; ++s) {
+                const int f = (s + 2) % 3;
+                copies(f == 0 ? st0 : f == 1 ? st1 : st2, s + 2);
+                // the barriers of the waves that compute; the last stage of an odd number of steps ends before its barrier
+                if (s < stages - 1 || a.K1 % SPS == 0) mx_barrier<FILL>();
+            }
+            mx_barrier<0>();
+            if (k == mine) break;
+            begin(g);
+            behind_stores = false;
+        }
+    }
+}
+
+template <int FMT, bool PAIR, int WM, int WN, int MT>
+static void launch_tile_t(const MxArgs& a, int per_cu, hipStream_t s) {
+    constexpr long long BM = 16 * MT * WM, cols = PAIR ? 32 * WN : 64 * WN;
+    const long long tiles = (a.rows / BM + std::min<long long>(a.E, a.rows / a.lo)) * ((a.N + cols - 1) / cols);    // an upper bound
+    mx_tile_kernel<FMT, PAIR, WM, WN, MT><<<dim3(unsigned(std::min<long long>(256 * per_cu, tiles))), dim3(64 * WM * WN), 0, s>>>(a);
+}
+
+template <int FMT, bool PAIR>
+static void launch_tile_v(const MxArgs& a, MxTile v, hipStream_t s) {
+    if (v == MX_TILE_256) launch_tile_t<FMT, PAIR, 2, 4, 8>(a, 1, s);
+    else if (v == MX_TILE_128) launch_tile_t<FMT, PAIR, 2, 2, 4>(a, 2, s);
+    else if (v == MX_TILE_64) launch_tile_t<FMT, PAIR, 1, 4, 4>(a, 3, s);
+    else launch_tile_t<FMT, PAIR, 1, 4, 2>(a, 4, s);
+}
+
+void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s) {
+    if (fmt == W4A8_MX_FP4) pair ? launch_tile_v<W4A8_MX_FP4, true>(a, v, s) : launch_tile_v<W4A8_MX_FP4, false>(a, v, s);
+    else if (fmt == MX_FP8_EXACT) launch_tile_v<MX_FP8_EXACT, false>(a, v, s);
+    else pair ? launch_tile_v<W4A8_MX_FP8, true>(a, v, s) : launch_tile_v<W4A8_MX_FP8, false>(a, v, s);
+}
+
+}  // namespace w4a8
