@@ -201,7 +201,8 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.int32, self.int8, self.float32, self.uint8 = torch.int32, torch.int8, torch.float32, torch.uint8
+        self.int32, self.int8, self.float32 = torch.int32, torch.int8, torch.float32
+        self.uint8, self.bfloat16 = torch.uint8, torch.bfloat16
         self.initialized, self.device = torch.cuda.is_initialized, torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.types = {torch.bfloat16: W4A8_BF16, torch.float32: W4A8_F32, torch.float16: W4A8_F16}
@@ -676,15 +677,6 @@ def mx_empty(fmt: int, M: int, K: int, device="cuda"):
             torch.empty((M, -(-K // 128) * 4), dtype=torch.uint8, device=device))
 
 
-def _on_device(t, *tensors) -> int:
-    """The current device, on which all the tensors (or None) are."""
-    dev = t.current()
-    for x in tensors:
-        if x is not None and x.get_device() != dev:
-            _require_current([y for y in tensors if y is not None])         # says which
-    return dev
-
-
 def _row_stride(x, what: str) -> int:
     """Elements between the rows of a matrix whose rows are contiguous; that of a single row says nothing."""
     (M, N), (ld, step) = x.shape, x.stride()
@@ -697,27 +689,47 @@ def _row_stride(x, what: str) -> int:
     return ld
 
 
-def _check_mx(t, Xq, sx, fmt: int, K: int) -> int:
-    """Codes and scales as w4a8_mx_quant leaves them; their rows."""
-    if fmt != W4A8_MX_FP4 and fmt != W4A8_MX_FP8:
-        raise ValueError("fmt must be W4A8_MX_FP4 or W4A8_MX_FP8")
-    if not 0 < K <= _INT_MAX:
-        raise ValueError("K must be positive and fit in 32 bits")
-    Kp = -(-K // 128) * 128
-    M = Xq.shape[0]
-    if (Xq.dtype is not t.uint8 or sx.dtype is not t.uint8 or Xq.shape != (M, Kp // 2 if fmt == W4A8_MX_FP4 else Kp) or
-            sx.shape != (M, Kp // 32) or not Xq.is_contiguous() or not sx.is_contiguous()):
-        raise ValueError("the codes and scales must be contiguous uint8 [M, K rounded up to 128 (MXFP4: / 2)] and [M, the same / 32]")
-    if M > _INT_MAX:
-        _check_int32(M)
-    return M
+def _ld(x, N: int, what: str) -> int:
+    """_row_stride of a matrix of N columns, which is N if it is contiguous."""
+    return N if x.is_contiguous() else _row_stride(x, what)
+
+
+def _kind(t, x) -> int:
+    """_dtype, without the calls in between."""
+    kind = t.types.get(x.dtype)
+    return _dtype(x) if kind is None else kind
+
+
+# The calls below test all of their arguments in one expression, cheapest first (half of a small call's host time otherwise), and
+# say what is wrong with them only where it is false.
+def _mx_rows(t, dev: int, Xq, sx, fmt: int, M: int, K: int) -> bool:
+    """Whether Xq and sx are codes and scales of M rows of K as w4a8_mx_quant leaves them, on device dev."""
+    Kp = (K + 127) & -128
+    return (Xq.get_device() == dev and sx.get_device() == dev and Xq.dtype is t.uint8 and sx.dtype is t.uint8 and
+            (fmt == W4A8_MX_FP8 and Xq.numel() == M * Kp or fmt == W4A8_MX_FP4 and 2 * Xq.numel() == M * Kp) and
+            32 * sx.numel() == M * Kp and Xq.is_contiguous() and sx.is_contiguous() and 0 < K <= _INT_MAX and M <= _INT_MAX)
+
+
+def _refuse(tensors, mx=(), what: str = "the tensors do not match") -> None:
+    """Raises for a call whose test failed: tensors elsewhere, codes (Xq, sx, fmt, M, K) of another shape, or `what`."""
+    _require_current([x for x in tensors if x is not None])
+    t = _torch()
+    for Xq, sx, fmt, M, K in mx:
+        if fmt != W4A8_MX_FP4 and fmt != W4A8_MX_FP8:
+            raise ValueError("fmt must be W4A8_MX_FP4 or W4A8_MX_FP8")
+        if not 0 < K <= _INT_MAX or M > _INT_MAX:
+            raise ValueError("K must be positive, and it and the rows fit in 32 bits")
+        if not _mx_rows(t, t.current(), Xq, sx, fmt, M, K):
+            raise ValueError("the codes and scales must be contiguous uint8 [M, K rounded up to 128 (MXFP4: / 2)] and "
+                             "[M, the same / 32]")
+    raise ValueError(what)
 
 
 _mx_packed_sizes: dict = {}
 
 
 def w4a8_mx_packed_size(K: int, N: int) -> int:
-    """Bytes of packed MXFP4 weights [N, K]."""
+    """Bytes of packed MXFP4 weights [N, K]; 0 if there are none of that size."""
     size = _mx_packed_sizes.get((K, N))
     if size is None:
         _check_int32(K, N)
@@ -727,66 +739,74 @@ def w4a8_mx_packed_size(K: int, N: int) -> int:
     return size
 
 
-def _check_mx_blobs(t, blobs, E: int, stride: int, K: int, N: int) -> None:
-    size = w4a8_mx_packed_size(K, N)
+def _mx_blobs(t, dev: int, blobs, E: int, stride: int, K: int, N: int) -> bool:
+    """Whether blobs holds E packed [N, K], stride bytes apart, on device dev."""
+    size = _mx_packed_sizes.get((K, N)) or w4a8_mx_packed_size(K, N)
     if size == 0:
-        raise W4A8Error(W4A8_EINVAL, "w4a8_mx_packed_size")
-    if E < 1 or stride < 0 or blobs.dtype is not t.uint8 or not blobs.is_contiguous() or blobs.numel() < (E - 1) * stride + size:
-        raise ValueError("the packed weights must be contiguous uint8 and hold E matrices at their stride")
+        raise W4A8Error(W4A8_EUNSUPPORTED if K > 0 and N > 0 else W4A8_EINVAL, "w4a8_mx_packed_size")
+    return (blobs.get_device() == dev and blobs.dtype is t.uint8 and 0 < E <= _INT_MAX and stride >= 0 and
+            blobs.numel() >= (E - 1) * stride + size and blobs.is_contiguous())
+
+
+_NO_BLOBS = "the packed weights must be contiguous uint8 and hold the matrices at their stride"
 
 
 def w4a8_mx_quant(X, fmt: int, Xq, sx, stream=None) -> None:
     """X [M, K] (bfloat16, float16 or float32, rows may be strided) -> MX codes and scales (mx_empty)."""
-    t = _torch()
-    dev = _on_device(t, X, Xq, sx)
+    t = _torch_of_calls or _torch()
+    dev = X.get_device()
     M, K = X.shape
-    ldx = _row_stride(X, "X")
-    if _check_mx(t, Xq, sx, fmt, K) != M:
-        raise ValueError("X and its codes must have the same rows")
-    _check(lib().w4a8_mx_quant(X.data_ptr(), _dtype(X), M, K, ldx, fmt, Xq.data_ptr(), sx.data_ptr(),
-                               t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_quant")
+    if dev != (t.device() if dev >= 0 else t.current()) or not _mx_rows(t, dev, Xq, sx, fmt, M, K):
+        _refuse((X, Xq, sx), ((Xq, sx, fmt, M, K),))
+    st = lib().w4a8_mx_quant(X.data_ptr(), _kind(t, X), M, K, _ld(X, K, "X"), fmt, Xq.data_ptr(), sx.data_ptr(),
+                             t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_mx_quant")
 
 
 def w4a8_mx_dequant(Xq, sx, fmt: int, Y, stream=None) -> None:
     """The values of MX codes and scales: Y [M, K] in bfloat16, float16 or float32, rows may be strided."""
-    t = _torch()
-    dev = _on_device(t, Y, Xq, sx)
+    t = _torch_of_calls or _torch()
+    dev = Y.get_device()
     M, K = Y.shape
-    ldy = _row_stride(Y, "Y")
-    if _check_mx(t, Xq, sx, fmt, K) != M:
-        raise ValueError("Y and its codes must have the same rows")
-    _check(lib().w4a8_mx_dequant(Xq.data_ptr(), sx.data_ptr(), fmt, M, K, Y.data_ptr(), _dtype(Y), ldy,
-                                 t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_dequant")
+    if dev != (t.device() if dev >= 0 else t.current()) or not _mx_rows(t, dev, Xq, sx, fmt, M, K):
+        _refuse((Y, Xq, sx), ((Xq, sx, fmt, M, K),))
+    st = lib().w4a8_mx_dequant(Xq.data_ptr(), sx.data_ptr(), fmt, M, K, Y.data_ptr(), _kind(t, Y), _ld(Y, K, "Y"),
+                               t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_mx_dequant")
 
 
 def w4a8_mx_pack(W, blobs, stream=None) -> None:
     """Quantize W [N, K] or [E, N, K] to MXFP4 and pack it into blobs, uint8 [w4a8_mx_packed_size] or [E, stride]."""
     t = _torch()
-    dev = _on_device(t, W, blobs)
-    if W.dim() not in (2, 3) or blobs.dim() != W.dim() - 1 or blobs.dtype is not t.uint8 or not blobs.is_contiguous():
-        raise ValueError("W must be [N, K] or [E, N, K], and blobs a contiguous uint8 [bytes] or [E, bytes]")
+    dev = t.current()
+    if W.dim() not in (2, 3) or blobs.dim() != W.dim() - 1:
+        raise ValueError("W must be [N, K] or [E, N, K], and blobs uint8 [bytes] or [E, bytes]")
     one = W.dim() == 2
     E, (N, K) = 1 if one else W.shape[0], W.shape[-2:]
     if E == 0:
         return
-    ldw = _row_stride(W if one else W[0], "W")
-    expert, stride = (0, 0) if one or E == 1 else (W.stride(0), blobs.stride(0))
-    if expert < 0 or (not one and blobs.shape[0] != E):
+    if not one and blobs.shape[0] != E:
         raise ValueError("W and blobs must have the same experts")
-    _check_mx_blobs(t, blobs, E, stride, K, N)
+    ldw = _row_stride(W if one else W[0], "W")
+    expert, stride = (0, 0) if E == 1 else (W.stride(0), blobs.stride(0))
+    if W.get_device() != dev or expert < 0 or not _mx_blobs(t, dev, blobs, E, stride, K, N):
+        _refuse((W, blobs), what=_NO_BLOBS)
     _check(lib().w4a8_mx_pack(W.data_ptr(), _dtype(W), E, N, K, ldw, expert, blobs.data_ptr(), stride,
                               t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_pack")
 
 
 def w4a8_mx_pack_codes(codes, scales, blob, stream=None) -> None:
-    """Pack existing MXFP4 codes uint8 [N, K / 2] and scales uint8 [N, K / 32] (rows may be strided), K % 32 == 0."""
+    """Pack existing MXFP4 codes uint8 [N, K / 2] (row stride a multiple of 16) and scales uint8 [N, K / 32], K % 32 == 0."""
     t = _torch()
-    dev = _on_device(t, codes, scales, blob)
+    dev = t.current()
     N, K = codes.shape[0], 2 * codes.shape[1]
     if codes.dtype is not t.uint8 or scales.dtype is not t.uint8 or scales.shape != (N, K // 32) or K % 32:
         raise ValueError("codes and scales must be uint8 [N, K / 2] and [N, K / 32]")
     ldc, lds = _row_stride(codes, "codes"), _row_stride(scales, "scales")
-    _check_mx_blobs(t, blob, 1, 0, K, N)
+    if codes.get_device() != dev or scales.get_device() != dev or not _mx_blobs(t, dev, blob, 1, 0, K, N):
+        _refuse((codes, scales, blob), what=_NO_BLOBS)
     _check(lib().w4a8_mx_pack_codes(codes.data_ptr(), scales.data_ptr(), N, K, ldc, lds, blob.data_ptr(),
                                     t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_pack_codes")
 
@@ -794,68 +814,82 @@ def w4a8_mx_pack_codes(codes, scales, blob, stream=None) -> None:
 def w4a8_mx_unpack_codes(blob, N: int, K: int, codes, scales, stream=None) -> None:
     """The inverse, into the layout of activations: codes and scales of mx_empty(W4A8_MX_FP4, N, K)."""
     t = _torch()
-    dev = _on_device(t, codes, scales, blob)
-    if _check_mx(t, codes, scales, W4A8_MX_FP4, K) != N:
-        raise ValueError("the codes must have N rows")
-    _check_mx_blobs(t, blob, 1, 0, K, N)
+    dev = t.current()
+    if not _mx_rows(t, dev, codes, scales, W4A8_MX_FP4, N, K) or not _mx_blobs(t, dev, blob, 1, 0, K, N):
+        _refuse((codes, scales, blob), ((codes, scales, W4A8_MX_FP4, N, K),), _NO_BLOBS)
     _check(lib().w4a8_mx_unpack_codes(blob.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(),
                                       t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_unpack_codes")
 
 
 def w4a8_mx_gemm(Xq, sx, fmt: int, blob, K: int, N: int, Y, stream=None) -> None:
     """Y [M, N] (bfloat16, float16 or float32, rows may be strided) = MX activations times packed MXFP4 weights [N, K]."""
-    t = _torch()
-    dev = _on_device(t, Xq, sx, blob, Y)
-    M = _check_mx(t, Xq, sx, fmt, K)
-    ldy = _row_stride(Y, "Y")
-    if Y.shape != (M, N):
-        raise ValueError("Y must be [M, N]")
-    _check_mx_blobs(t, blob, 1, 0, K, N)
-    _check(lib().w4a8_mx_gemm(Xq.data_ptr(), sx.data_ptr(), fmt, M, blob.data_ptr(), K, N, Y.data_ptr(), ldy, _dtype(Y),
-                              t.raw_stream(dev) if stream is None else int(stream)), "w4a8_mx_gemm")
+    t = _torch_of_calls or _torch()
+    dev = Y.get_device()
+    M, width = Y.shape
+    if (width != N or dev != (t.device() if dev >= 0 else t.current()) or not _mx_rows(t, dev, Xq, sx, fmt, M, K) or
+            not _mx_blobs(t, dev, blob, 1, 0, K, N)):
+        _refuse((Xq, sx, blob, Y), ((Xq, sx, fmt, M, K),), _NO_BLOBS if width == N else "Y must be [M, N]")
+    st = lib().w4a8_mx_gemm(Xq.data_ptr(), sx.data_ptr(), fmt, M, blob.data_ptr(), K, N, Y.data_ptr(), _ld(Y, N, "Y"),
+                            _kind(t, Y), t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_mx_gemm")
 
 
-def _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, others):
-    """Checked arguments of the grouped MX products, up to and including K; the current device."""
-    t = _torch()
-    dev = _on_device(t, Xq, sx, gather, expert_offsets, blobs, *others)
-    if expert_offsets.dtype is not t.int32 or (gather is not None and gather.dtype is not t.int32):
-        raise ValueError("gather and expert_offsets must be int32")
-    src_rows = _check_mx(t, Xq, sx, fmt, K)
-    if not (-_INT_MAX <= k <= _INT_MAX and 0 < E <= _INT_MAX) or rows > _INT_MAX:
-        raise ValueError("k, E and the rows must fit in 32 bits, and there must be an expert")
-    _check_rows(gather, expert_offsets, E, rows)
-    _check_mx_blobs(t, blobs, E, expert_stride, K, N)
-    return (Xq.data_ptr(), sx.data_ptr(), fmt, None if gather is None else gather.data_ptr(), int(k), expert_offsets.data_ptr(),
-            int(E), rows, src_rows, blobs.data_ptr(), int(expert_stride), K), t, dev
+def _mx_moe_args(t, dev: int, Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, other):
+    """Checked arguments of the grouped MX products, up to and including K.  dev: where `other`, an output, is."""
+    src_rows = Xq.shape[0]
+    if not (dev == (t.device() if dev >= 0 else t.current()) and _mx_rows(t, dev, Xq, sx, fmt, src_rows, K) and
+            _mx_blobs(t, dev, blobs, E, expert_stride, K, N) and expert_offsets.get_device() == dev and
+            expert_offsets.dtype is t.int32 and expert_offsets.numel() == E + 1 and expert_offsets.is_contiguous() and
+            (gather is None or gather.get_device() == dev and gather.dtype is t.int32 and gather.numel() >= rows and
+             gather.is_contiguous()) and -_INT_MAX <= k <= _INT_MAX and rows <= _INT_MAX):
+        _require_current((Xq, sx, blobs, other), int32=(gather, expert_offsets))
+        _check_rows(gather, expert_offsets, E, rows)
+        _check_int32(k, E, rows)
+        _refuse((), ((Xq, sx, fmt, src_rows, K),), _NO_BLOBS)
+    return (Xq.data_ptr(), sx.data_ptr(), fmt, None if gather is None else gather.data_ptr(), k, expert_offsets.data_ptr(),
+            E, rows, src_rows, blobs.data_ptr(), expert_stride, K)
 
 
 def w4a8_moe_gemm_mx(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, Y,
                      stream=None) -> None:
     """Grouped product of MX activations with E packed MXFP4 matrices [N, K]; Y [rows, N]."""
+    t = _torch_of_calls or _torch()
+    dev = Y.get_device()
     rows, N = Y.shape
-    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, (Y,))
-    _check(lib().w4a8_moe_gemm_mx(*args, N, Y.data_ptr(), _row_stride(Y, "Y"), _dtype(Y),
-                                  t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_mx")
+    args = _mx_moe_args(t, dev, Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, N, Y)
+    st = lib().w4a8_moe_gemm_mx(*args, N, Y.data_ptr(), _ld(Y, N, "Y"), _kind(t, Y),
+                                t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_moe_gemm_mx")
 
 
 def w4a8_moe_gemm_silu_mx(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, H,
                           stream=None) -> None:
     """Grouped gate/up product with silu(gate) * up in its epilogue: E packed [2I, K], H [rows, I] in bfloat16 or float16."""
+    t = _torch_of_calls or _torch()
+    dev = H.get_device()
     rows, I = H.shape
-    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, (H,))
-    _check(lib().w4a8_moe_gemm_silu_mx(*args, I, H.data_ptr(), _row_stride(H, "H"), _dtype(H),
-                                       t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_silu_mx")
+    args = _mx_moe_args(t, dev, Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, H)
+    st = lib().w4a8_moe_gemm_silu_mx(*args, I, H.data_ptr(), _ld(H, I, "H"), _kind(t, H),
+                                     t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_moe_gemm_silu_mx")
 
 
 def w4a8_moe_gemm_silu_mx_quant(Xq, sx, fmt: int, gather, k: int, expert_offsets, E: int, blobs, expert_stride: int, K: int, I: int,
                                 h_fmt: int, Hq, sh, stream=None) -> None:
     """The same with H quantized to h_fmt: codes and scales of mx_empty(h_fmt, rows, I)."""
-    t = _torch()
-    rows = _check_mx(t, Hq, sh, h_fmt, I)
-    args, t, dev = _mx_moe_args(Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, (Hq, sh))
-    _check(lib().w4a8_moe_gemm_silu_mx_quant(*args, I, h_fmt, Hq.data_ptr(), sh.data_ptr(),
-                                             t.raw_stream(dev) if stream is None else int(stream)), "w4a8_moe_gemm_silu_mx_quant")
+    t = _torch_of_calls or _torch()
+    dev = Hq.get_device()
+    rows = Hq.shape[0]
+    if not _mx_rows(t, dev, Hq, sh, h_fmt, rows, I):
+        _refuse((Hq, sh), ((Hq, sh, h_fmt, rows, I),))
+    args = _mx_moe_args(t, dev, Xq, sx, fmt, gather, k, expert_offsets, E, blobs, expert_stride, K, rows, 2 * I, Hq)
+    st = lib().w4a8_moe_gemm_silu_mx_quant(*args, I, h_fmt, Hq.data_ptr(), sh.data_ptr(),
+                                           t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_moe_gemm_silu_mx_quant")
 
 
 def w4a8_moe_mx_workspace_size(T: int, k: int, H: int, I: int, E: int, fmt: int) -> int:
@@ -867,69 +901,95 @@ def w4a8_moe_forward_mx(X, topk_ids, topk_w, E: int, fmt: int, gu_blobs, gu_stri
                         out, stream=None) -> None:
     """One MoE layer on MXFP4 experts: gu_blobs E packed [2I, H], d_blobs E packed [H, I]; workspace of
     w4a8_moe_mx_workspace_size bytes."""
-    _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
-    t = _torch()
-    (T, k), H = topk_ids.shape, X.shape[1]
-    _check_int32(E, fmt, I)
-    _check_mx_blobs(t, gu_blobs, E, gu_stride, H, 2 * I)
-    _check_mx_blobs(t, d_blobs, E, d_stride, I, H)
-    _check(lib().w4a8_moe_forward_mx(_ptr(X), _ptr(topk_ids), _ptr(topk_w), T, k, int(E), int(fmt), _ptr(gu_blobs), int(gu_stride),
-                                     _ptr(d_blobs), int(d_stride), H, int(I), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
-           "w4a8_moe_forward_mx")
+    t = _torch_of_calls or _torch()
+    dev = X.get_device()
+    (T, H), (rows, k) = X.shape, topk_ids.shape
+    if not (dev == (t.device() if dev >= 0 else t.current()) and topk_ids.get_device() == dev and topk_w.get_device() == dev and
+            workspace.get_device() == dev and out.get_device() == dev and _mx_blobs(t, dev, gu_blobs, E, gu_stride, H, 2 * I) and
+            _mx_blobs(t, dev, d_blobs, E, d_stride, I, H) and T | H | k <= _INT_MAX):
+        _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
+        _check_int32(E, I, T, H, k)
+        raise ValueError(_NO_BLOBS)
+    if not (X.dtype is t.bfloat16 and out.dtype is t.bfloat16 and topk_ids.dtype is t.int32 and topk_w.dtype is t.float32 and
+            rows == T and topk_w.shape == (T, k) and out.shape == (T, H) and X.is_contiguous() and out.is_contiguous() and
+            topk_ids.is_contiguous() and topk_w.is_contiguous() and workspace.is_contiguous()):
+        _check_layer(X, topk_ids, topk_w, workspace, out, gu_blobs, d_blobs)
+    st = lib().w4a8_moe_forward_mx(X.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), T, k, E, fmt, gu_blobs.data_ptr(),
+                                   gu_stride, d_blobs.data_ptr(), d_stride, H, I, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), out.data_ptr(),
+                                   t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_moe_forward_mx")
 
 
 # ------------------------------------------------------------------------------ the norm around a block
-def _norm_args(X, residual, d: NormDesc, w, residual_out, post_w, gate, others):
-    """Checked arguments of the norm calls, up to and including the row stride of residual_out; the current device."""
-    t = _torch()
-    dev = _on_device(t, X, residual, w, residual_out, post_w, gate, *others)
-    M, H = X.shape
-    ldx = _row_stride(X, "X")
-    like = residual if residual is not None else residual_out
-    for r in (residual, residual_out):
-        if r is not None and (r.shape != X.shape or r.dtype is not like.dtype):
-            raise ValueError("residual and residual_out must have the shape of X and one type")
-    for v in (w, post_w):
-        if v is not None and (v.dtype is not t.float32 or v.numel() != H or not v.is_contiguous()):
-            raise ValueError("w and post_w must be contiguous float32 [H]")
+def _norm_row(t, dev: int, v, H: int) -> bool:
+    return v is None or v.get_device() == dev and v.dtype is t.float32 and v.numel() == H and v.is_contiguous()
+
+
+def _norm_args(t, dev: int, X, residual, d: NormDesc, w, residual_out, post_w, gate):
+    """Checked arguments of the norm calls, up to and including the row stride of residual_out."""
+    shape = X.shape
+    M, H = shape
+    if dev != (t.device() if dev >= 0 else t.current()) or not _norm_row(t, dev, w, H) or not _norm_row(t, dev, post_w, H):
+        _refuse((X, w, post_w), what="w and post_w must be contiguous float32 [H]")
+    res, ldr, out, ldo, kind = None, H, None, H, X
+    if residual is not None:
+        if residual.get_device() != dev or residual.shape != shape:
+            _refuse((X, residual), what="residual must have the shape of X")
+        res, ldr, kind = residual.data_ptr(), _ld(residual, H, "residual"), residual
+    if residual_out is residual:
+        out, ldo = res, ldr
+    elif residual_out is not None:
+        if (residual_out.get_device() != dev or residual_out.shape != shape or
+                residual is not None and residual_out.dtype is not residual.dtype):
+            _refuse((X, residual_out), what="residual_out must have the shape of X and the type of residual")
+        out, ldo, kind = residual_out.data_ptr(), _ld(residual_out, H, "residual_out"), residual_out
     ldg = 0
     if gate is not None:
-        if gate.dtype is not X.dtype or gate.dim() != 2 or gate.shape[0] not in (1, M) or gate.shape[1] != H:
-            raise ValueError("gate must be [M, H] or [1, H] in the type of X")
-        ldg = _row_stride(gate, "gate") if gate.shape[0] == M and M > 1 else 0
-        if ldg == 0 and gate.stride(1) != 1 and H > 1:
-            raise ValueError("the rows of gate must be contiguous")
-    return (X.data_ptr(), _dtype(X), ldx, _ptr(residual), _dtype(like if like is not None else X),
-            H if residual is None else _row_stride(residual, "residual"), _ptr(gate), ldg, _ptr(post_w), _ptr(w), d, M, H,
-            _ptr(residual_out), H if residual_out is None else _row_stride(residual_out, "residual_out")), t, dev
+        if (gate.get_device() != dev or gate.dtype is not X.dtype or gate.dim() != 2 or gate.shape[0] not in (1, M) or
+                gate.shape[1] != H):
+            _refuse((X, gate), what="gate must be [M, H] or [1, H] in the type of X")
+        ldg = _row_stride(gate, "gate")
+        if gate.shape[0] != M or M == 1:
+            ldg = 0
+    return (X.data_ptr(), _kind(t, X), _ld(X, H, "X"), res, _kind(t, kind), ldr, None if gate is None else gate.data_ptr(), ldg,
+            None if post_w is None else post_w.data_ptr(), None if w is None else w.data_ptr(), d, M, H, out, ldo)
 
 
 def w4a8_norm_residual(X, residual, d: NormDesc, w, residual_out, Y, post_w=None, gate=None, stream=None) -> None:
     """r' = residual + alpha gate u, u = X or its RMS norm times post_w; Y = RMS norm of r' times w.  residual, residual_out, Y,
     post_w and gate may be None."""
-    args, t, dev = _norm_args(X, residual, d, w, residual_out, post_w, gate, (Y,))
-    ldy = X.shape[1]
+    t = _torch_of_calls or _torch()
+    dev = X.get_device()
+    args = _norm_args(t, dev, X, residual, d, w, residual_out, post_w, gate)
+    y, ldy = None, args[12]
     if Y is not None:
-        if Y.shape != X.shape or Y.dtype is not X.dtype:
-            raise ValueError("Y must have the shape and type of X")
-        ldy = _row_stride(Y, "Y")
-    _check(lib().w4a8_norm_residual(*args, _ptr(Y), ldy, t.raw_stream(dev) if stream is None else int(stream)), "w4a8_norm_residual")
+        if Y.get_device() != dev or Y.shape != X.shape or Y.dtype is not X.dtype:
+            _refuse((X, Y), what="Y must have the shape and type of X")
+        y, ldy = Y.data_ptr(), _ld(Y, ldy, "Y")
+    st = lib().w4a8_norm_residual(*args, y, ldy, t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_norm_residual")
 
 
 def w4a8_norm_residual_quant(X, residual, d: NormDesc, w, residual_out, fmt: int, Xq, sx, post_w=None, gate=None,
                              stream=None) -> None:
     """The same with h quantized: MX codes and scales (mx_empty), or int8 [M, H] and float32 [M] for W4A8_QUANT_INT8."""
-    args, t, dev = _norm_args(X, residual, d, w, residual_out, post_w, gate, (Xq, sx))
-    M, H = X.shape
+    t = _torch_of_calls or _torch()
+    dev = X.get_device()
+    args = _norm_args(t, dev, X, residual, d, w, residual_out, post_w, gate)
+    M, H = args[11], args[12]
     if fmt == W4A8_QUANT_INT8:
-        if (Xq.dtype is not t.int8 or Xq.shape != (M, H) or sx.dtype is not t.float32 or sx.numel() != M or
-                not Xq.is_contiguous() or not sx.is_contiguous()):
-            raise ValueError("Xq and sx must be contiguous int8 [M, H] and float32 [M]")
-    elif _check_mx(t, Xq, sx, fmt, H) != M:
-        raise ValueError("X and its codes must have the same rows")
-    _check(lib().w4a8_norm_residual_quant(*args, fmt, _ptr(Xq), _ptr(sx), t.raw_stream(dev) if stream is None else int(stream)),
-           "w4a8_norm_residual_quant")
+        if not (Xq.get_device() == dev and sx.get_device() == dev and Xq.dtype is t.int8 and sx.dtype is t.float32 and
+                Xq.shape == X.shape and sx.numel() == M and Xq.is_contiguous() and sx.is_contiguous()):
+            _refuse((X, Xq, sx), what="Xq and sx must be contiguous int8 [M, H] and float32 [M]")
+    elif not _mx_rows(t, dev, Xq, sx, fmt, M, H):
+        _refuse((X, Xq, sx), ((Xq, sx, fmt, M, H),))
+    st = lib().w4a8_norm_residual_quant(*args, fmt, Xq.data_ptr(), sx.data_ptr(),
+                                        t.raw_stream(dev) if stream is None else int(stream))
+    if st:
+        _check(st, "w4a8_norm_residual_quant")
 
 
 # ------------------------------------------------------------------------------ helpers

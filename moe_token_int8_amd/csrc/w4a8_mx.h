@@ -13,6 +13,7 @@
 namespace w4a8 {
 
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 // K of a stored row: padded with zeros to whole MFMA steps of 128.
 constexpr int MX_STEP = 128;
@@ -80,6 +81,28 @@ __device__ __forceinline__ uint32_t mx_amax8(const float* v) {
 __device__ __forceinline__ uint32_t mx_quad_max(uint32_t m) {
     m = max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0xB1, 0xF, 0xF, true)));
     return max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x4E, 0xF, 0xF, true)));
+}
+
+// f over all 64 lanes, in every lane: exchanges within rows of 16 by DPP (quad permutes, half and whole row mirrored), between
+// rows by v_permlane{16,32}_swap; no LDS.
+template <class F>
+__device__ __forceinline__ uint32_t wave_all(uint32_t m, F f) {
+    m = f(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0xB1, 0xF, 0xF, true)));
+    m = f(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x4E, 0xF, 0xF, true)));
+    m = f(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x141, 0xF, 0xF, true)));
+    m = f(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x140, 0xF, 0xF, true)));
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = f(uint32_t(a[0]), uint32_t(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return f(uint32_t(b[0]), uint32_t(b[1]));
+}
+__device__ __forceinline__ float wave_sum(float s) {
+    return __uint_as_float(wave_all(__float_as_uint(s), [](uint32_t x, uint32_t y) __attribute__((always_inline)) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+    }));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
+    return wave_all(m, [](uint32_t x, uint32_t y) __attribute__((always_inline)) { return max(x, y); });
 }
 
 // 8 neighbouring elements at p, of which n exist (the others are 0), as float32.  Any alignment of whole elements.

@@ -11,8 +11,9 @@ struct MxArgs {
     const uint8_t* X;         // activation codes, rows of rowb bytes
     const uint8_t* sx;        // their scale bytes, rows of 4 K1
     unsigned rowb;
-    const int32_t* gather;    // source row of routed row r: gather[r] / topk (NULL: r)
-    int topk;
+    const int32_t* gather;    // source row of routed row r: gather[r] / k (NULL: r)
+    unsigned div_mul;         // x / k = (umulhi(x, div_mul) + x) >> div_shift for x < 2^31
+    int div_shift;
     int src_rows;
     const int32_t* offsets;   // [E + 1] (NULL: one expert, all rows: the dense product)
     int E;
@@ -28,7 +29,6 @@ struct MxArgs {
     uint8_t* Hq;              // paired form: codes and scales of h in place of Y (h_fmt; NULL: Y)
     uint8_t* sh;
     int h_fmt;
-    int lo, hi;               // this launch serves the experts with lo <= rows < hi
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -40,13 +40,16 @@ __device__ __forceinline__ int mx_row_last(const MxArgs& a, int e) {
     return a.offsets ? min(max(a.offsets[e + 1], 0), a.rows) : a.rows;
 }
 
+// Token of a gather entry, or -1 if it names no row of X.
+__device__ __forceinline__ int mx_token(const MxArgs& a, int g) {
+    const int t = int((__umulhi(unsigned(g), a.div_mul) + unsigned(g)) >> a.div_shift);
+    return g >= 0 && t < a.src_rows ? t : -1;
+}
+
 // Source row of routed row r, or -1 (a gather entry that names no row of X: its output is zero).
 __device__ __forceinline__ int mx_src(const MxArgs& a, int r) {
     if (!a.gather) return r;
-    const int g = a.gather[r];
-    if (g < 0) return -1;
-    const int t = int(unsigned(g) / unsigned(a.topk));
-    return t < a.src_rows ? t : -1;
+    return mx_token(a, a.gather[r]);
 }
 
 // Activation operands of the kernels: fp4, fp8, and fp8 for float32 outputs (MX_FP8_EXACT).  Within 8 neighbouring k the MFMA
@@ -145,9 +148,8 @@ __device__ __forceinline__ void mx_store_block(const MxArgs& a, const int row, c
     if (j == 0) a.sh[at] = uint8_t(byte);
 }
 
-// MFMA tiles (w4a8_mx_tile_kernels.hip) over the experts with a.lo <= rows < a.hi: 256 x 256, 128 x 128, 64 x 256 or
-// 32 x 256.
-enum MxTile { MX_TILE_256, MX_TILE_128, MX_TILE_64, MX_TILE_32 };
+// MFMA tiles (w4a8_mx_tile_kernels.hip): 128 x 512, 128 x 256, 64 x 256 or 32 x 256.
+enum MxTile { MX_TILE_WIDE, MX_TILE_128, MX_TILE_64, MX_TILE_32 };
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s);
 
 }  // namespace w4a8

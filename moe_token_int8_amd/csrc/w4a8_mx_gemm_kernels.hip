@@ -16,20 +16,21 @@
 
 namespace w4a8 {
 
-// Streaming kernel: few rows, bound by the read of the weights.
+// Streaming kernel: few rows, bound by the read of the weights and, in small calls, by its latency.
 //
-// A workgroup of 8 waves owns one tile of up to 16 MS rows of one expert and CT MFMA tiles of 16 weight columns (paired form:
-// gate columns in half of them, the matching up columns in the others) over all of K.  The waves share the steps of 128 k: wave
-// w takes w, w + 8, ...; weights and activations go from memory to registers in the layout of the MFMA operands (a step of a
-// weight tile is one contiguous KiB), with no LDS and no barrier in the loop, two of a wave's steps in flight.  The 8 partial
-// sums are added in wave order through LDS, so a call repeats bit for bit.
-constexpr int MXS_WAVES = 8;
+// A workgroup of 8 waves owns one tile of up to 16 rows of one expert and 4 MFMA tiles of 16 weight columns (paired form: 2 of gate
+// columns, then the 2 matching ones of up columns) over all of K.  The waves share the steps of 128 k: wave w takes w, w + 8, ...;
+// weights and activations go from memory to registers in the layout of the MFMA operands (a step of a weight tile is one
+// contiguous KiB), with no LDS and no barrier in the loop, two of a wave's steps in flight.  The 8 partial sums are added in wave
+// order through LDS, so a call repeats bit for bit.  (Two row tiles a workgroup read the weights once for 32 rows, but the tile
+// kernel does that faster: 32 rows for each of 64 experts, 1408 x 4096 fp4 73 against 51 us.)
+constexpr int MXS_WAVES = 8, MXS_ROWS = 16, MXS_TILES = 4;
 
-template <int MT>
+// The slot-th row tile over the experts, in their order; every wave finds it alone.  expert is -1 past the last one.
 __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane) {
     TileRows tr{0, 0, -1};
     if (!a.offsets) {
-        if ((long long)slot * MT < a.rows) tr = {slot * MT, min(a.rows, slot * MT + MT), 0};
+        if ((long long)slot * MXS_ROWS < a.rows) tr = {slot * MXS_ROWS, min(a.rows, slot * MXS_ROWS + MXS_ROWS), 0};
         return tr;
     }
     int base = 0;
@@ -45,7 +46,7 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
         for (int j = 0; j < 4; ++j) {
             // malformed offsets cannot move a tile outside the rows of the call
             const int e0 = min(max(b[j], 0), a.rows), e1 = min(max(e[j], e0), a.rows), cnt = e1 - e0;
-            const int t = cnt >= a.lo && cnt < a.hi ? (cnt + MT - 1) / MT : 0;
+            const int t = (cnt + MXS_ROWS - 1) / MXS_ROWS;
             int incl = t;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -56,8 +57,8 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
             if (hit) {
                 const int src = __ffsll((long long)hit) - 1;
                 tr.expert = c0 + j * 64 + src;
-                tr.rbeg = __builtin_amdgcn_readlane(e0 + (slot - base - (incl - t)) * MT, src);
-                tr.rend = min(__builtin_amdgcn_readlane(e1, src), tr.rbeg + MT);
+                tr.rbeg = __builtin_amdgcn_readlane(e0 + (slot - base - (incl - t)) * MXS_ROWS, src);
+                tr.rend = min(__builtin_amdgcn_readlane(e1, src), tr.rbeg + MXS_ROWS);
                 return tr;
             }
             base += __builtin_amdgcn_readlane(incl, 63);
@@ -66,17 +67,16 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
     return tr;
 }
 
-template <int FMT, bool PAIR, int MS, int CT, bool NT>
+template <int FMT, bool PAIR>
 __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
-    constexpr int COLS = PAIR ? CT * 8 : CT * 16;
-    constexpr bool QUADS = !PAIR && CT == 4;                    // the scales of the 4 tiles are one word
+    constexpr int CT = MXS_TILES, COLS = PAIR ? CT * 8 : CT * 16;
     constexpr int STEP_BYTES = FMT == W4A8_MX_FP4 ? 64 : 128;   // of an activation row
-    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ v4f red[MXS_WAVES * CT * 64];                    // partial sums: [wave][tile][lane]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, c16 = lane & 15;
     for (unsigned item = blockIdx.x;; item += gridDim.x) {
         const int slot = int(item / unsigned(ncb)), cb = int(item - unsigned(slot) * unsigned(ncb));
-        const TileRows tr = mx_find<16 * MS>(a, slot, lane);
+        const TileRows tr = mx_find(a, slot, lane);
         const int expert = __builtin_amdgcn_readfirstlane(tr.expert);
         if (expert < 0) return;                                 // uniform over the workgroup; no later slot has a tile
         const int rbeg = __builtin_amdgcn_readfirstlane(tr.rbeg), nrows = __builtin_amdgcn_readfirstlane(tr.rend) - rbeg;
@@ -91,76 +91,63 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
         const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint8_t*>(wexp + a.scales_off), 0, int(unsigned((ntiles + 3) / 4) * unsigned(a.K1) * 256u), 0x00020000);
         constexpr unsigned NONE = 0x80000000u;                  // codes end below it, so that a sum with a valid offset does not wrap
-        unsigned woff[CT], soff[QUADS ? 1 : CT];
+        unsigned woff[CT], soff[PAIR ? CT : 1];                 // (unpaired: the scales of the 4 tiles are one word)
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             const int own = PAIR ? cb * (CT / 2) + t % (CT / 2) : cb * CT + t;      // among the gate, or all, tiles
             const int tile = PAIR && t >= CT / 2 ? own + a.N / 16 : own;
             const bool there = own < (PAIR ? a.N / 16 : ntiles);
             woff[t] = there ? unsigned(tile) * unsigned(a.K1) * 1024u + unsigned(lane) * 16u : NONE;
-            if (!QUADS) soff[QUADS ? 0 : t] = there ? unsigned(tile >> 2) * unsigned(a.K1) * 256u + unsigned(lane) * 4u + unsigned(tile & 3) : NONE;
+            if (PAIR) soff[PAIR ? t : 0] = there ? unsigned(tile >> 2) * unsigned(a.K1) * 256u + unsigned(lane) * 4u + unsigned(tile & 3) : NONE;
         }
-        if (QUADS) soff[0] = unsigned(cb) * unsigned(a.K1) * 256u + unsigned(lane) * 4u;
+        if (!PAIR) soff[0] = unsigned(cb) * unsigned(a.K1) * 256u + unsigned(lane) * 4u;
         struct Step {
             v4i w[CT];
-            uint32_t sw[QUADS ? 1 : CT];
-            MxOperand<FMT> x[MS];
-            uint32_t sx[MS];
+            uint32_t sw[PAIR ? CT : 1];
+            MxOperand<FMT> x;
+            uint32_t sx;
         };
-        // NT: the non-temporal hint, for calls that read more weights than the Infinity Cache holds.
         auto load_w = [&](Step& b, const int step) __attribute__((always_inline)) {
             const unsigned at = step < a.K1 ? unsigned(step) * 1024u : NONE, sat = step < a.K1 ? unsigned(step) * 256u : NONE;
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-                b.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[t] + at, 0, NT ? 2 : 0);
+            for (int t = 0; t < CT; ++t) b.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[t] + at, 0, 0);
 #pragma unroll
-            for (int t = 0; t < (QUADS ? 1 : CT); ++t)
-                b.sw[t] = QUADS ? uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, soff[t] + sat, 0, 0))
-                                : uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, soff[t] + sat, 0, 0));
+            for (int t = 0; t < (PAIR ? CT : 1); ++t)
+                b.sw[t] = PAIR ? uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, soff[t] + sat, 0, 0))
+                               : uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, soff[t] + sat, 0, 0));
         };
-        const uint8_t* xrow[MS];
-        const uint8_t* srow[MS];
+        const uint8_t *xrow, *srow;
         auto load_x = [&](Step& b, const int s) __attribute__((always_inline)) {
             const int step = s < a.K1 ? s : 0;
-#pragma unroll
-            for (int ms = 0; ms < MS; ++ms) {
-                const uint8_t* p = xrow[ms] + unsigned(step) * unsigned(STEP_BYTES);
-                b.x[ms].p[0] = *reinterpret_cast<const v4i*>(p);
-                if constexpr (FMT != W4A8_MX_FP4) b.x[ms].p[1] = *reinterpret_cast<const v4i*>(p + 64);
-                b.sx[ms] = srow[ms][unsigned(step) * 4u];
-            }
+            const uint8_t* p = xrow + unsigned(step) * unsigned(STEP_BYTES);
+            b.x.p[0] = *reinterpret_cast<const v4i*>(p);
+            if constexpr (FMT != W4A8_MX_FP4) b.x.p[1] = *reinterpret_cast<const v4i*>(p + 64);
+            b.sx = srow[unsigned(step) * 4u];
         };
         Step s0, s1;
         load_w(s0, wave);
         load_w(s1, wave + MXS_WAVES);
-        // activation rows of this lane; rows past the tile repeat its first row (their sums are not stored)
-#pragma unroll
-        for (int ms = 0; ms < MS; ++ms) {
-            const int row = ms * 16 + c16, src = mx_src(a, rbeg + (row < nrows ? row : 0));
+        {   // the activation row of this lane; rows past the tile repeat its first row (their sums are not stored)
+            const int src = mx_src(a, rbeg + (c16 < nrows ? c16 : 0));
             const size_t r = size_t(src < 0 ? 0 : src);
-            xrow[ms] = a.X + r * a.rowb + unsigned(q) * 16u;
-            srow[ms] = a.sx + r * (size_t(a.K1) * 4) + unsigned(q);
+            xrow = a.X + r * a.rowb + unsigned(q) * 16u;
+            srow = a.sx + r * (size_t(a.K1) * 4) + unsigned(q);
         }
         load_x(s0, wave);
         load_x(s1, wave + MXS_WAVES);
 
-        v4f acc[CT][MS];
+        v4f acc[CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int ms = 0; ms < MS; ++ms) acc[t][ms] = v4f{};
+        for (int t = 0; t < CT; ++t) acc[t] = v4f{};
         auto multiply = [&](const Step& b) __attribute__((always_inline)) {
+            if constexpr (PAIR) {
 #pragma unroll
-            for (int ms = 0; ms < MS; ++ms) {
-                if constexpr (QUADS) {
-                    acc[0][ms] = mx_mfma<FMT, 0>(b.w[0], b.x[ms], acc[0][ms], b.sw[0], b.sx[ms]);
-                    acc[1][ms] = mx_mfma<FMT, 1>(b.w[1], b.x[ms], acc[1][ms], b.sw[0], b.sx[ms]);
-                    acc[2][ms] = mx_mfma<FMT, 2>(b.w[2], b.x[ms], acc[2][ms], b.sw[0], b.sx[ms]);
-                    acc[3][ms] = mx_mfma<FMT, 3>(b.w[3], b.x[ms], acc[3][ms], b.sw[0], b.sx[ms]);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) acc[t][ms] = mx_mfma<FMT, 0>(b.w[t], b.x[ms], acc[t][ms], b.sw[t], b.sx[ms]);
-                }
+                for (int t = 0; t < CT; ++t) acc[t] = mx_mfma<FMT, 0>(b.w[t], b.x, acc[t], b.sw[PAIR ? t : 0], b.sx);
+            } else {
+                acc[0] = mx_mfma<FMT, 0>(b.w[0], b.x, acc[0], b.sw[0], b.sx);
+                acc[1] = mx_mfma<FMT, 1>(b.w[1], b.x, acc[1], b.sw[0], b.sx);
+                acc[2] = mx_mfma<FMT, 2>(b.w[2], b.x, acc[2], b.sw[0], b.sx);
+                acc[3] = mx_mfma<FMT, 3>(b.w[3], b.x, acc[3], b.sw[0], b.sx);
             }
         };
         for (int s = wave; s < a.K1; s += 2 * MXS_WAVES) {
@@ -172,13 +159,9 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
             load_x(s1, s + 3 * MXS_WAVES);
         }
 
-        // the 8 partial sums: planes of 16 bytes a lane, [wave][tile][row block][lane]
-        v4f* red = reinterpret_cast<v4f*>(smem);
-        constexpr int ITEMS = CT * MS * 64, OUT = PAIR ? ITEMS / 2 : ITEMS;
+        constexpr int ITEMS = CT * 64, OUT = PAIR ? ITEMS / 2 : ITEMS;
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int ms = 0; ms < MS; ++ms) red[wave * ITEMS + (t * MS + ms) * 64 + lane] = acc[t][ms];
+        for (int t = 0; t < CT; ++t) red[wave * ITEMS + t * 64 + lane] = acc[t];
         lds_barrier();
         auto total = [&](const int o) __attribute__((always_inline)) {
             v4f s = red[o];
@@ -186,68 +169,53 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
             for (int w = 1; w < MXS_WAVES; ++w) s += red[w * ITEMS + o];
             return s;
         };
-        constexpr int PER = (OUT + 511) / 512;
+        if (tid < OUT) {                                        // whole waves
+            if (PAIR && a.Hq) {                                 // 8 neighbouring lanes take a row's block of 32 columns
+                const int j = tid & 7, row = tid >> 3, at = (j >> 2) * 64 + (j & 3) * 16 + row, block = cb * (COLS / 32);
+                v4f h{};
+                if (row < nrows && cb * COLS + j * 4 < a.N && mx_src(a, rbeg + row) >= 0) {
+                    const v4f g = total(at), u = total(at + ITEMS / 2);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int o = tid + i * 512;
-            if constexpr (PAIR && CT >= 4) {
-                if (a.Hq) {                                     // 8 neighbouring lanes take a row's block of 32 columns
-                    constexpr int BL = CT / 4;                  // blocks of a row
-                    const int j = o & 7, b = (o >> 3) % BL, row = (o >> 3) / BL, t = b * 2 + (j >> 2);
-                    const int at = (t * MS + row / 16) * 64 + (j & 3) * 16 + (row & 15);
-                    const int col = cb * COLS + b * 32 + j * 4;
-                    const bool in = o < OUT && row < nrows && col < a.N;
-                    v4f h{};
-                    if (in && mx_src(a, rbeg + row) >= 0) {
-                        const v4f g = total(at), u = total(at + ITEMS / 2);
+                    for (int k = 0; k < 4; ++k) h[k] = mx_silu(g[k]) * u[k];
+                }
+                mx_store_block(a, rbeg + row, block, j, h, row < nrows);
+                if (row < nrows && cb * COLS + COLS >= a.N) mx_pad_blocks(a, rbeg + row, block + 1, j);
+            } else {
+                const int row = c16, col = cb * COLS + (tid >> 6) * 16 + 4 * q;
+                if (row < nrows && col < a.N) {
+                    v4f y = total(tid);
+                    if constexpr (PAIR) {
+                        const v4f up = total(tid + ITEMS / 2);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) h[k] = mx_silu(g[k]) * u[k];
+                        for (int k = 0; k < 4; ++k) y[k] = mx_silu(y[k]) * up[k];
                     }
-                    const bool there = o < OUT && row < nrows && cb * COLS + b * 32 < a.N;
-                    mx_store_block(a, rbeg + row, (cb * COLS) / 32 + b, j, h, there);
-                    if (there && cb * COLS + b * 32 + 32 >= a.N) mx_pad_blocks(a, rbeg + row, (cb * COLS) / 32 + b + 1, j);
-                    continue;
+                    if (mx_src(a, rbeg + row) < 0) y = v4f{};
+                    mx_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), y);
                 }
             }
-            const int l = o & 63, row = ((o >> 6) % MS) * 16 + (l & 15);
-            const int col = cb * COLS + ((o >> 6) / MS) * 16 + 4 * (l >> 4);
-            if (o >= OUT || row >= nrows || col >= a.N) continue;
-            v4f y = total(o);
-            if constexpr (PAIR) {
-                const v4f up = total(o + ITEMS / 2);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = mx_silu(y[k]) * up[k];
-            }
-            if (mx_src(a, rbeg + row) < 0) y = v4f{};
-            mx_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), y);
         }
-        lds_barrier();                                          // the planes are written again by the next tile
+        lds_barrier();                                          // the sums are written again by the next tile
     }
 }
 
-// Workgroups of a launch: all tiles up to a bound, beyond which they go round in a grid that is resident at once (two
-// workgroups a compute unit).
-constexpr long long MXS_GRID = 512;
-
-template <int FMT, bool PAIR, int MS, int CT, bool NT>
-static void launch_stream_t(const MxArgs& a, long long slots, hipStream_t s) {
-    constexpr size_t lds = size_t(MXS_WAVES) * CT * MS * 64 * 16;
-    static_assert(lds <= 65536, "two workgroups share a compute unit");
-    constexpr int cols = PAIR ? CT * 8 : CT * 16;
+// All tiles up to a bound that keeps a launch's work-items below 2^32; beyond it workgroups go round.
+template <int FMT, bool PAIR>
+static void launch_stream(const MxArgs& a, hipStream_t s) {
+    constexpr int cols = PAIR ? MXS_TILES * 8 : MXS_TILES * 16;
     const int ncb = (a.N + cols - 1) / cols;
-    const long long blocks = MS == 1 ? std::min(slots * ncb, 1ll << 22) : std::min(slots * ncb, MXS_GRID);
-    mx_stream_kernel<FMT, PAIR, MS, CT, NT><<<dim3(unsigned(blocks)), dim3(512), lds, s>>>(a, ncb);
+    const long long slots = a.rows / MXS_ROWS + std::min(a.E, a.rows);          // an upper bound of the row tiles
+    mx_stream_kernel<FMT, PAIR><<<dim3(unsigned(std::min(slots * ncb, 1ll << 22))), dim3(512), 0, s>>>(a, ncb);
 }
 
 // Which kernel a call takes: the least of five estimates, in us.  The host knows rows and E, not the experts' rows: of E experts
 // about E (1 - exp(-rows / E)) have any, and each ends in a row tile that is half empty.  Streaming tiles: 512 workgroups at a time
 // take o and l a step.  MFMA tiles: `per` workgroups share a compute unit, a step takes l, or thr for each of them.  Either reads
-// the weights at bw TB/s.  Fitted to 282 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, K 768 .. 14336), of
-// which the choice loses 5 % in the mean against the best of all, 38 % at worst.  Measured, us, streams of 16 and 32 rows / tiles of
-// 32 / 64 / 256 rows: 16 x 4096 x 14336 fp8 9.0, 9.9 / 19.6 / 19.0 / 27.7; 128 x 14336 x 4096 fp4 26, 21 / 40 / 45 / 58; 2 rows for each
-// of 256 experts, 2048 x 7168 fp8 397, 335 / 278 / 277 / 374; 64 rows for each of 64, 4096 x 2816 fp8 299, 254 / 133 / 125 / 135;
-// 8192 x 4096 x 14336 fp4 257 with 256 rows.
-enum MxKernel { MXK_STREAM16, MXK_STREAM32, MXK_TILE32, MXK_TILE64, MXK_TILE256, MXK_KERNELS };
+// the weights at bw TB/s.  Fitted to 352 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, K 300 .. 14336), of
+// which the choice loses 5 % in the mean against the best of all, 60 % at worst.  Measured, us, streaming / tiles of 32, 64, 128 x
+// 256 and 128 x 512: 16 x 4096 x 14336 fp8 9 / 19, 19, 26, 38; 128 x 14336 x 4096 fp4 26 / 39, 44, 54, 78; 512 x 4096 x 4096 fp4 - / 19, 16,
+// 20, 27; 2048 x 4096 x 14336 fp8 - / 150, 117, 103, 95; 2 rows for each of 256 experts, 2048 x 7168 fp8 393 / 276, 276, 298, 301; 64
+// rows for each of 64, gate/up 4096 x 1408 fp8 299 / 129, 123, 114, 103; 32 rows for each of 64, 1408 x 4096 fp4 114 / 53, 51, 52, 57.
+enum MxKernel { MXK_STREAM, MXK_TILE32, MXK_TILE64, MXK_TILE128, MXK_WIDE, MXK_KERNELS };
 
 static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
     struct Rate {
@@ -255,18 +223,18 @@ static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
         double o, l, thr, bw;
     };
     static const Rate rates[2][MXK_KERNELS] = {
-        {{16, 64, 2, 6.3, 0.098, 0, 4.1}, {32, 64, 2, 5.2, 0.196, 0, 3.8}, {32, 256, 4, 1.2, 0.43, 0.41, 5.1}, {64, 256, 3, 1.1, 0.47, 0.475, 4.8}, {256, 256, 1, 6.0, 0.73, 0, 3.8}},
-        {{16, 64, 2, 5.6, 0.079, 0, 3.9}, {32, 64, 2, 4.1, 0.151, 0, 3.9}, {32, 256, 4, 1.0, 0.12, 0.31, 5.2}, {64, 256, 3, 1.7, 0.14, 0.35, 4.9}, {256, 256, 1, 5.9, 0.54, 0, 4.3}}};
+        {{16, 64, 2, 3.6, 0.132, 0, 3.5}, {32, 256, 4, 0.3, 0.48, 0.41, 5.1}, {64, 256, 3, 1.2, 0.47, 0.51, 5.2}, {128, 256, 2, 3.3, 0, 0.68, 4.8}, {128, 512, 1, 4.3, 0.09, 1.12, 4.4}},
+        {{16, 64, 2, 3.4, 0.102, 0, 3.8}, {32, 256, 4, 0.5, 0.11, 0.34, 5.3}, {64, 256, 3, 1.1, 0.40, 0.40, 5.0}, {128, 256, 2, 3.5, 0.38, 0.44, 4.5}, {128, 512, 1, 3.8, 0.65, 0.78, 4.7}}};
     const double rows = a.rows, E = a.E, width = pair ? 2.0 * a.N : a.N, steps = a.K1;
     const double active = E > 1 ? std::min(rows, E * (1 - std::exp(-rows / E))) : 1;
     const double bytes = active * width * steps * 68;           // 128 k of a column
-    MxKernel best = MXK_STREAM16;
+    MxKernel best = MXK_STREAM;
     double least = 1e300;
     for (int v = 0; v < MXK_KERNELS; ++v) {
         const Rate& r = rates[fp4][v];
         const double rt = E > 1 ? std::max(active, rows / r.rows + 0.5 * active) : std::ceil(rows / r.rows), n = rt * std::ceil(width / r.cols);
         double us;
-        if (v <= MXK_STREAM32) {
+        if (v == MXK_STREAM) {
             us = std::max(1.0, n / 512) * (r.o + r.l * steps);
         } else {
             const double co = n / 256, full = co / r.per;
@@ -280,22 +248,16 @@ static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
 }
 
 template <int FMT, bool PAIR>
-static const char* launch_mx(MxArgs a, hipStream_t s) {
-    const long long rows = a.rows, E = a.E;
-    a.lo = 1, a.hi = 0x7fffffff;
+static const char* launch_mx(const MxArgs& a, hipStream_t s) {
     // the tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     const bool near = !a.gather || (long long)a.src_rows * a.rowb < 0xe0000000ll;
-    const MxKernel v = choose_mx(a, FMT == W4A8_MX_FP4, PAIR);
-    if (v == MXK_STREAM16) {
-        launch_stream_t<FMT, PAIR, 1, 4, false>(a, rows / 16 + std::min(E, rows), s);
-        return "mx_stream_kernel (16-row tiles)";
+    switch (near ? choose_mx(a, FMT == W4A8_MX_FP4, PAIR) : MXK_STREAM) {
+        case MXK_TILE32: launch_mx_tile(a, FMT, PAIR, MX_TILE_32, s); return "mx_tile_kernel (32 x 256)";
+        case MXK_TILE64: launch_mx_tile(a, FMT, PAIR, MX_TILE_64, s); return "mx_tile_kernel (64 x 256)";
+        case MXK_TILE128: launch_mx_tile(a, FMT, PAIR, MX_TILE_128, s); return "mx_tile_kernel (128 x 256)";
+        case MXK_WIDE: launch_mx_tile(a, FMT, PAIR, MX_TILE_WIDE, s); return "mx_tile_kernel (128 x 512)";
+        default: launch_stream<FMT, PAIR>(a, s); return "mx_stream_kernel";
     }
-    if (v == MXK_STREAM32 || !near) {
-        launch_stream_t<FMT, PAIR, 2, 4, false>(a, rows / 32 + std::min(E, rows), s);
-        return "mx_stream_kernel (32-row tiles)";
-    }
-    launch_mx_tile(a, FMT, PAIR, v == MXK_TILE32 ? MX_TILE_32 : v == MXK_TILE64 ? MX_TILE_64 : MX_TILE_256, s);
-    return v == MXK_TILE32 ? "mx_tile_kernel (32 x 256)" : v == MXK_TILE64 ? "mx_tile_kernel (64 x 256)" : "mx_tile_kernel (256 x 256)";
 }
 
 // out[t] = sum_j w[t, j] Yd[inv[t, j]] in float32, j ascending, rounded once: the experts' outputs stay in float32 (rounded to
@@ -369,7 +331,9 @@ static MxArgs mx_args(const void* Xq, const uint8_t* sx, int fmt, const int32_t*
     a.sx = sx;
     a.rowb = unsigned(mx_row_bytes(fmt, K));
     a.gather = gather;
-    a.topk = k;
+    // s = ceil(log2 k), 2^32 (2^s - k) / k + 1: exact for dividends below 2^32, of which the sum takes those below 2^31
+    while ((1ll << a.div_shift) < k) ++a.div_shift;
+    a.div_mul = gather ? unsigned(((1ull << 32) * ((1ull << a.div_shift) - unsigned(k))) / unsigned(k) + 1) : 0;
     a.src_rows = src_rows;
     a.offsets = offsets;
     a.E = E;

@@ -10,20 +10,25 @@
 
 namespace w4a8 {
 
-// Persistent workgroups of WM x WN waves walk over tiles of 16 MT WM rows x 64 WN weight columns (paired form: half of them gate,
-// the matching half up columns).  Wave (wm, wn) owns 16 MT rows and 64 columns: 4 MT accumulators of 4 a lane.
+// Persistent workgroups of WN waves walk over tiles of 16 MT rows x 64 WN weight columns (paired form: half of them gate, the
+// matching half up columns).  Each wave owns all rows and 64 columns: 4 MT accumulators of 4 a lane.
 //
 // The packed weights are in operand order, so they go from memory straight to registers, 4 KiB a wave and step of 128 k, two
-// steps ahead.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4, one of fp8), copied
-// without registers (buffer_load ... lds), three stages deep, with a stage's scale bytes behind its codes.  LDS then carries a
-// third of what it would with both operands (64 + 16 KiB of the 128 a CU moves in the 1024 cycles of a 256 x 256 step of fp4).
+// steps ahead, each to one wave.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4, one of
+// fp8), copied without registers (buffer_load ... lds), three stages deep, with a stage's scale bytes behind its codes.
+//
+// What bounds it: the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
+// cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 104 us (4.6 PFLOP/s; MFMAs alone on
+// registers reach 6.2), 83 without the memory operations in the loop, 99 without the copies, 94 without the weights, unchanged with
+// half the LDS reads.  256 x 256 tiles, where two waves load the same weights, took 108; touching the weights' lines 8 steps ahead,
+// one load of 64 lines, 115 to 130 (64 cycles of the same path); another order of steps for workgroups that share data, no change.
 //
 // vmcnt counts in the order of issue, so what is issued when is fixed: a step requests the weights of the step after the next;
 // the first step of a stage then requests the activations of the stage after the next.  One barrier a stage, before the last
 // group of MFMAs, when the stage's last operands are in registers: behind it the next stage is whole and this one is free.
 constexpr int MXT_ROW = 128;                                    // bytes of a row in a stage
 constexpr int MXT_MAX_E = 1024;
-constexpr int MXT_PANEL = 4;                                    // row tiles of a panel of consecutive tiles
+constexpr unsigned MXT_PANEL = 8;                               // row tiles of a panel of consecutive tiles
 
 #define LDS __attribute__((address_space(3)))
 using lds_ptr = LDS uint8_t*;
@@ -74,10 +79,10 @@ __device__ __forceinline__ uint32_t mx_max_rows(uint32_t m) {
     return max(uint32_t(b[0]), uint32_t(b[1]));
 }
 
-template <int FMT, bool PAIR, int WM, int WN, int MT>
-__global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FMT != W4A8_MX_FP4) && FMT != MX_FP8_EXACT ? 4 : 3) void mx_tile_kernel(MxArgs a) {
+template <int FMT, bool PAIR, int WN, int MT>
+__global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != W4A8_MX_FP4) && FMT != MX_FP8_EXACT ? 4 : 3) void mx_tile_kernel(MxArgs a) {
     constexpr bool FP4 = FMT == W4A8_MX_FP4;
-    constexpr int THREADS = 64 * WM * WN, BM = 16 * MT * WM;
+    constexpr int THREADS = 64 * WN, BM = 16 * MT;
     constexpr int COLS = PAIR ? 32 * WN : 64 * WN;              // columns of Y
     constexpr int SPS = FP4 ? 2 : 1;                            // steps of a stage
     constexpr int CODES = BM * MXT_ROW, STAGE = CODES + THREADS * 4;
@@ -93,14 +98,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
     __shared__ int4 list[LIST];                                 // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[MXT_MAX_E + 1];                        // row tiles before expert e
     __shared__ int entries[BM];                                 // gather entries of the next tile's rows
-    __shared__ int wsum[WM * WN];
+    __shared__ int wsum[WN];
     const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int q = lane >> 4, c16 = lane & 15, wm = wave / WN, wn = wave % WN;
+    const int q = lane >> 4, c16 = lane & 15, wn = wave;
     const int ncb = (a.N + COLS - 1) / COLS;
     const int stages = (a.K1 + SPS - 1) / SPS;
     const bool f32 = !PAIR && a.out == W4A8_F32;
 
-    // row tiles of every expert of this launch, as a prefix sum
+    // row tiles of every expert, as a prefix sum
     {
         constexpr int EPT = MXT_MAX_E / THREADS;
         const int tid = threadIdx.x;
@@ -108,8 +113,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             const int e = EPT * tid + i;
-            const int cnt = e < a.E ? mx_row_last(a, e) - mx_row_first(a, e) : 0;
-            t[i] = cnt >= a.lo && cnt < a.hi ? (cnt + BM - 1) / BM : 0;
+            const int cnt = e < a.E ? max(mx_row_last(a, e) - mx_row_first(a, e), 0) : 0;
+            t[i] = (cnt + BM - 1) / BM;
             incl += t[i];
         }
         int excl = -incl;
@@ -130,29 +135,31 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
         if (a.E == MXT_MAX_E && tid == THREADS - 1) first[MXT_MAX_E] = incl;
         __syncthreads();
     }
-    const long long total = (long long)first[a.E] * ncb;
+    // Workgroups take the tiles in turn.  Within an expert, panels of MXT_PANEL row tiles go through all columns together.  (In 32
+    // bits: 2^24 rows in tiles of 32, and one more for each of 1024 experts, by 2^20 columns in blocks of 128 or more.)  Consecutive
+    // tiles for a workgroup, which keep its weights from one to the next, share less in L2: 4153 tokens x 6 of 64 experts, 4096 x
+    // 2815 320 us in place of 270.
+    const unsigned total = unsigned(first[a.E]) * unsigned(ncb);
     // blocks go to the 8 XCDs in turn: the blocks of one XCD take neighbouring tiles, which share rows or columns in its L2
-    const int nblk = int(gridDim.x), per = nblk / 8;
-    const int rank = nblk % 8 ? int(blockIdx.x) : (int(blockIdx.x) % 8) * per + int(blockIdx.x) / 8;
-    const int mine = rank < total ? int((total - rank + nblk - 1) / nblk) : 0;      // tiles of this workgroup
+    const unsigned nblk = gridDim.x, per = nblk / 8;
+    const unsigned rank = nblk % 8 ? blockIdx.x : blockIdx.x % 8 * per + blockIdx.x / 8;
+    const int mine = rank < total ? int((total - rank - 1) / nblk + 1) : 0;         // tiles of this workgroup
     if (mine == 0) return;
 
     // the tiles from k0 on of this workgroup; all threads, between barriers
     auto look_up = [&](const int k0) __attribute__((always_inline)) {
         const int tid = mx_opaque(int(threadIdx.x));
         if (tid < LIST && k0 + tid < mine) {
-            const long long t = rank + (long long)(k0 + tid) * nblk;
-            const int trow = int(t / ncb);
+            const unsigned t = rank + unsigned(k0 + tid) * nblk, trow = t / unsigned(ncb);
             int lo = 0, hi = a.E;                               // expert: the last one whose first tile is not after trow
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (first[mid] <= trow) lo = mid;
+                if (unsigned(first[mid]) <= trow) lo = mid;
                 else hi = mid;
             }
-            const int f0 = first[lo], rt = first[lo + 1] - f0, in_e = int(t - (long long)f0 * ncb);
-            const int panel = in_e / (MXT_PANEL * ncb), j = in_e - panel * MXT_PANEL * ncb;
-            const int rp = min(MXT_PANEL, rt - panel * MXT_PANEL);
-            const int cb = j / rp, r0 = mx_row_first(a, lo) + (panel * MXT_PANEL + j - cb * rp) * BM;
+            const unsigned in_e = t - unsigned(first[lo]) * unsigned(ncb), panel = in_e / (MXT_PANEL * unsigned(ncb));
+            const unsigned j = in_e - panel * (MXT_PANEL * unsigned(ncb)), rp = min(MXT_PANEL, unsigned(first[lo + 1] - first[lo]) - panel * MXT_PANEL);
+            const int cb = int(j / rp), r0 = mx_row_first(a, lo) + int(panel * MXT_PANEL + j - unsigned(cb) * rp) * BM;
             list[tid] = make_int4(lo, r0, min(BM, mx_row_last(a, lo) - r0), cb);
         }
         __syncthreads();
@@ -199,9 +206,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
                      unsigned(mx_opaque(int(threadIdx.x))) * 4u, (lds_ptr)((LDS int*)entries + wave * 64));
     };
     auto source = [&](const int g) __attribute__((always_inline)) {    // row of X, or -1
-        if (!a.gather) return g;
-        const int t = g < 0 ? -1 : int(unsigned(g) / unsigned(a.topk));
-        return t < a.src_rows ? t : -1;
+        return a.gather ? mx_token(a, g) : g;
     };
     // bit m of dead: this lane's row 16 m + c16 of the wave has a gather entry that names no row (its outputs are zeros)
     unsigned dead = 0, next_dead = 0;
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
             next_dead = 0;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int row = wm * (16 * MT) + m * 16 + (lane & 15);
+                const int row = m * 16 + (lane & 15);
                 if (row < g.z && source(entries[row]) < 0) next_dead |= 1u << m;
             }
         }
@@ -264,8 +269,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
     // operands in LDS: byte offsets of this lane in a stage, for the halves of 64 bytes
     int xat[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) xat[h] = mx_opaque((wm * (16 * MT) + c16) * MXT_ROW + ((4 * h + q) ^ mx_swizzle(c16)) * 16);
-    const int sat = mx_opaque(CODES + (wm * (16 * MT) + c16) * SB + q);
+    for (int h = 0; h < 2; ++h) xat[h] = mx_opaque(c16 * MXT_ROW + ((4 * h + q) ^ mx_swizzle(c16)) * 16);
+    const int sat = mx_opaque(CODES + c16 * SB + q);
     MxOperand<FMT> x[2][G];
     uint32_t sx[2][G];
     auto read_tile = [&](const int buf, const lds_ptr st, const int h, const int m) __attribute__((always_inline)) {
@@ -279,8 +284,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
         sx[buf][i] = *(const LDS uint8_t*)(st + sat + m * 16 * SB + (FP4 ? 4 * h : 0));
     };
 
-    constexpr int STORES16 = PAIR ? MT : 2 * MT;                // of a wave's regular tile in 16 bits
-    bool behind_stores = false;
+    // Stores that a wave issues at the end of a tile, behind the next one's first copies: FEW of a regular tile in 16 bits, twice as
+    // many in float32 or of quantized h, or a number that is not known (0), which the first barrier waits for.
+    constexpr int FEW = PAIR ? MT : 2 * MT;
+    int stores = 0;
 
     look_up(0);
     auto uniform = [&](int4 v) __attribute__((always_inline)) {
@@ -294,7 +301,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
     for (int k = 0;;) {
         const int4 cur = g;
         dead = next_dead;
-        if (behind_stores) mx_barrier<NEWER_FIRST + STORES16>();
+        if (stores == FEW) mx_barrier<NEWER_FIRST + FEW>();
+        else if (stores == 2 * FEW) mx_barrier<NEWER_FIRST + 2 * FEW>();
         else mx_barrier<NEWER_FIRST>();
         // the next tile, and its gather entries: requested here, first needed at the end of this tile
         if (++k < mine) {
@@ -302,7 +310,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
             g = uniform(list[k % LIST]);
             request_rows(g);
         }
-        if (wm * (16 * MT) < cur.z) {
+        {
             v4f acc[4][MT];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -358,7 +366,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
             // tile's copies start before this one's outputs are stored
             mx_barrier<0>();
             if (k < mine) begin(g);
-            const int r0 = wm * (16 * MT);
             const unsigned gone = dead;
             auto value = [&](const int n, const int m) __attribute__((always_inline)) {
                 v4f y = acc[n][m];
@@ -372,9 +379,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
             const bool regular = !(PAIR && a.Hq) && a.ldy < (size_t(1) << 21) && ((a.N & (f32 ? 3 : 7)) == 0 || (cur.w + 1) * COLS <= a.N);
             const unsigned pitch = unsigned(a.ldy) * es;
             const int colw = cur.w * COLS + wn * (PAIR ? 32 : 64);  // first column of the wave
+            stores = !regular ? 0 : f32 ? 2 * FEW : FEW;
             if (PAIR && a.Hq) {
-                const size_t bpr = size_t(mx_kp(a.N) / 32), block = size_t(colw / 32);
-                const bool have = colw < a.N, last = have && colw + 32 >= a.N, fp4 = a.h_fmt == W4A8_MX_FP4;
+                const unsigned bpr = unsigned(mx_kp(a.N) / 32), block = unsigned(colw) / 32u;
+                const bool have = colw < a.N, fp4 = a.h_fmt == W4A8_MX_FP4;
+                const unsigned bytes = fp4 ? 16u : 32u;
+                // rows past the tile's last lie behind its descriptors: their stores are dropped
+                const __amdgpu_buffer_rsrc_t hr = mx_buffer(a.Hq + size_t(cur.y) * bpr * bytes, size_t(cur.z) * bpr * bytes);
+                const __amdgpu_buffer_rsrc_t br = mx_buffer(a.sh + size_t(cur.y) * bpr, size_t(cur.z) * bpr);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     v4f h0 = value(0, m), h1 = value(1, m);
@@ -390,26 +402,27 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
                     else c0 = mx_fp8x4(h0[0] * up, h0[1] * up, h0[2] * up, h0[3] * up), c1 = mx_fp8x4(h1[0] * up, h1[1] * up, h1[2] * up, h1[3] * up);
                     if (byte == 255u) c0 = 0u, c1 = 0u;
                     mx_swap16(c0, c1);                          // 8 neighbouring columns: tile q % 2, half q / 2
-                    const int row = r0 + m * 16 + c16, at8 = (q & 1) * 2 + (q >> 1);
-                    if (row >= cur.z || !have) continue;
-                    const size_t at = size_t(cur.y + row) * bpr + block;
-                    if (fp4) *reinterpret_cast<uint32_t*>(a.Hq + at * 16 + at8 * 4) = c0 | (c1 << 16);
-                    else *reinterpret_cast<uint2*>(a.Hq + at * 32 + at8 * 8) = make_uint2(c0, c1);
-                    if (q == 0) a.sh[at] = uint8_t(byte);
-                    if (last) {
-                        const int bytes = fp4 ? 16 : 32;
-                        for (size_t b = block + 1; b < bpr; ++b) {
-                            uint8_t* p = a.Hq + (size_t(cur.y + row) * bpr + b) * bytes + q * (bytes / 4);
-                            *reinterpret_cast<uint32_t*>(p) = 0u;
-                            if (!fp4) *reinterpret_cast<uint32_t*>(p + 4) = 0u;
-                            if (q == 0) a.sh[size_t(cur.y + row) * bpr + b] = 0;
+                    const unsigned at = unsigned(m * 16 + c16) * bpr + block, at8 = unsigned((q & 1) * 2 + (q >> 1));
+                    if (fp4) __builtin_amdgcn_raw_buffer_store_b32(int(c0 | (c1 << 16)), hr, have ? at * 16u + at8 * 4u : NONE, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b64(v2i{int(c0), int(c1)}, hr, have ? at * 32u + at8 * 8u : NONE, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b8(uint8_t(byte), br, have && q == 0 ? at : NONE, 0, 0);
+                }
+                stores = 2 * FEW;
+                if (have && colw + 32 >= a.N && block + 1 < bpr) {  // blocks behind the last column, up to whole steps of the next product
+                    stores = 0;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        for (unsigned b = block + 1; b < bpr; ++b) {
+                            const unsigned at = unsigned(m * 16 + c16) * bpr + b;
+                            __builtin_amdgcn_raw_buffer_store_b32(0, hr, at * bytes + unsigned(q) * (bytes / 4), 0, 0);
+                            if (!fp4) __builtin_amdgcn_raw_buffer_store_b32(0, hr, at * bytes + unsigned(q) * 8u + 4u, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b8(uint8_t(0), br, q == 0 ? at : NONE, 0, 0);
                         }
-                    }
                 }
             } else if (!regular) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const int row = r0 + m * 16 + c16;
+                    const int row = m * 16 + c16;
 #pragma unroll
                     for (int n = 0; n < (PAIR ? 2 : 4); ++n) {
                         const int col = colw + n * 16 + 4 * q;
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
 #pragma unroll
                         for (int n = 0; n < (PAIR ? 2 : 4); ++n) {
                             const int col = colw + n * 16 + 4 * q;
-                            const unsigned off = col < a.N ? unsigned(r0 + m * 16 + c16) * pitch + unsigned(col) * 4u : NONE;
+                            const unsigned off = col < a.N ? unsigned(m * 16 + c16) * pitch + unsigned(col) * 4u : NONE;
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, value(n, m)), yr, off, 0, 0);
                         }
                 } else {
@@ -444,41 +457,29 @@ __global__ __launch_bounds__(64 * WM * WN, WM == 2 ? 2 : MT == 2 && !(PAIR && FM
                             mx_swap16(a0, b0);                  // 8 neighbouring columns: tile n + q % 2, half q / 2
                             mx_swap16(a1, b1);
                             const int col = colw + (n + (q & 1)) * 16 + (q >> 1) * 8;
-                            const unsigned off = col < a.N ? unsigned(r0 + m * 16 + c16) * pitch + unsigned(col) * 2u : NONE;
+                            const unsigned off = col < a.N ? unsigned(m * 16 + c16) * pitch + unsigned(col) * 2u : NONE;
                             __builtin_amdgcn_raw_buffer_store_b128(v4i{int(a0), int(a1), int(b0), int(b1)}, yr, off, 0, 0);
                         }
                 }
             }
             if (k == mine) break;
-            behind_stores = regular && !f32;
-        } else {                                                // a wave below the last row only copies
-            for (int s = 0; s < stages; ++s) {
-                const int f = (s + 2) % 3;
-                copies(f == 0 ? st0 : f == 1 ? st1 : st2, s + 2);
-                // the barriers of the waves that compute; the last stage of an odd number of steps ends before its barrier
-                if (s < stages - 1 || a.K1 % SPS == 0) mx_barrier<FILL>();
-            }
-            mx_barrier<0>();
-            if (k == mine) break;
-            begin(g);
-            behind_stores = false;
         }
     }
 }
 
-template <int FMT, bool PAIR, int WM, int WN, int MT>
+template <int FMT, bool PAIR, int WN, int MT>
 static void launch_tile_t(const MxArgs& a, int per_cu, hipStream_t s) {
-    constexpr long long BM = 16 * MT * WM, cols = PAIR ? 32 * WN : 64 * WN;
-    const long long tiles = (a.rows / BM + std::min<long long>(a.E, a.rows / a.lo)) * ((a.N + cols - 1) / cols);    // an upper bound
-    mx_tile_kernel<FMT, PAIR, WM, WN, MT><<<dim3(unsigned(std::min<long long>(256 * per_cu, tiles))), dim3(64 * WM * WN), 0, s>>>(a);
+    constexpr long long BM = 16 * MT, cols = PAIR ? 32 * WN : 64 * WN;
+    const long long tiles = (a.rows / BM + std::min<long long>(a.E, a.rows)) * ((a.N + cols - 1) / cols);   // an upper bound
+    mx_tile_kernel<FMT, PAIR, WN, MT><<<dim3(unsigned(std::min<long long>(256 * per_cu, tiles))), dim3(64 * WN), 0, s>>>(a);
 }
 
 template <int FMT, bool PAIR>
 static void launch_tile_v(const MxArgs& a, MxTile v, hipStream_t s) {
-    if (v == MX_TILE_256) launch_tile_t<FMT, PAIR, 2, 4, 8>(a, 1, s);
-    else if (v == MX_TILE_128) launch_tile_t<FMT, PAIR, 2, 2, 4>(a, 2, s);
-    else if (v == MX_TILE_64) launch_tile_t<FMT, PAIR, 1, 4, 4>(a, 3, s);
-    else launch_tile_t<FMT, PAIR, 1, 4, 2>(a, 4, s);
+    if (v == MX_TILE_WIDE) launch_tile_t<FMT, PAIR, 8, 8>(a, 1, s);
+    else if (v == MX_TILE_128) launch_tile_t<FMT, PAIR, 4, 8>(a, 2, s);
+    else if (v == MX_TILE_64) launch_tile_t<FMT, PAIR, 4, 4>(a, 3, s);
+    else launch_tile_t<FMT, PAIR, 4, 2>(a, 4, s);
 }
 
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s) {

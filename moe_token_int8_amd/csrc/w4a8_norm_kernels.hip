@@ -51,24 +51,20 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_residual_kerne
     if (WPR == 1 && row >= a.M) return;
     const int Kp = mx_kp(a.H);
 
-    auto across = [&](float s, const int which, const bool maximum) __attribute__((always_inline)) {
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const float y = __shfl_xor(s, o, 64);
-            s = maximum ? __uint_as_float(max(__float_as_uint(s), __float_as_uint(y))) : s + y;
-        }
+    auto sum = [&](float s, const int which) __attribute__((always_inline)) {
+        s = wave_sum(s);
         if constexpr (WPR > 1) {
             if (lane == 0) part[which][wave] = s;
             __syncthreads();
             s = part[which][0];
 #pragma unroll
-            for (int w = 1; w < WPR; ++w) {
-                const float y = part[which][w];
-                s = maximum ? __uint_as_float(max(__float_as_uint(s), __float_as_uint(y))) : s + y;
-            }
+            for (int w = 1; w < WPR; ++w) s += part[which][w];
         }
         return s;
     };
+    // few values a lane: the weights are requested with everything else, and not after the sums that they wait for
+    constexpr bool EARLY = R <= 2;
+    float w[EARLY ? R : 1][8], p[EARLY ? R : 1][8], g[EARLY ? R : 1][8];
 
     float v[R][8], r[R][8];
 #pragma unroll
@@ -86,20 +82,29 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_residual_kerne
             for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
         }
     }
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int k = (i * T + t) * 8, n = a.H - k;
+            if (a.gate) mx_load8<DT>(a.gate + (size_t(row) * size_t(a.ldg) + size_t(min(k, a.H))) * ES, n, g[i]);
+            if (a.post_w) mx_load8<W4A8_F32>(a.post_w + min(k, a.H), n, p[i]);
+            if (a.fmt != NORM_NONE) mx_load8<W4A8_F32>(a.w + min(k, a.H), n, w[i]);
+        }
+    }
     if (a.post_w) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = fmaf(v[i][j], v[i][j], s);
-        const float rs = 1.0f / sqrtf(across(s, 0, false) / float(a.H) + a.eps_post);
+        const float rs = 1.0f / sqrtf(sum(s, 0) / float(a.H) + a.eps_post);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int k = (i * T + t) * 8, n = a.H - k;
-            float p[8];
-            mx_load8<W4A8_F32>(a.post_w + min(k, a.H), n, p);
+            const int at = EARLY ? i : 0;
+            if (!EARLY) mx_load8<W4A8_F32>(a.post_w + min(k, a.H), n, p[at]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rs * p[j];
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rs * p[at][j];
         }
     }
     float s = 0.0f;
@@ -107,10 +112,10 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_residual_kerne
     for (int i = 0; i < R; ++i) {
         const int k = (i * T + t) * 8, n = a.H - k;
         if (a.gate) {
-            float g[8];
-            mx_load8<DT>(a.gate + (size_t(row) * size_t(a.ldg) + size_t(min(k, a.H))) * ES, n, g);
+            const int at = EARLY ? i : 0;
+            if (!EARLY) mx_load8<DT>(a.gate + (size_t(row) * size_t(a.ldg) + size_t(min(k, a.H))) * ES, n, g[at]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
+            for (int j = 0; j < 8; ++j) v[i][j] *= g[at][j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[i][j] = round_to<RT>(fmaf(a.alpha, v[i][j], r[i][j]));
@@ -119,15 +124,15 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_residual_kerne
         for (int j = 0; j < 8; ++j) s = fmaf(r[i][j], r[i][j], s);
     }
     if (a.fmt == NORM_NONE) return;
-    const float rs = 1.0f / sqrtf(across(s, 1, false) / float(a.H) + a.eps);
+    const float rs = 1.0f / sqrtf(sum(s, 1) / float(a.H) + a.eps);
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int k = (i * T + t) * 8, n = a.H - k;
-        float p[8];
-        mx_load8<W4A8_F32>(a.w + min(k, a.H), n, p);
+        const int at = EARLY ? i : 0;
+        if (!EARLY) mx_load8<W4A8_F32>(a.w + min(k, a.H), n, w[at]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * rs * p[j];
+        for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * rs * w[at][j];
         if (a.fmt == NORM_H) {
             if (n > 0) mx_store8<DT>(a.Y + (size_t(row) * size_t(a.ldy) + size_t(k)) * ES, n, r[i]);
             continue;
@@ -154,7 +159,14 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_residual_kerne
         }
     }
     if (a.fmt != W4A8_QUANT_INT8) return;
-    const RowScale q = row_scale(__float_as_uint(across(__uint_as_float(amax), 2, true)));
+    amax = wave_max(amax);
+    if constexpr (WPR > 1) {
+        if (lane == 0) part[2][wave] = __uint_as_float(amax);
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < WPR; ++x) amax = max(amax, __float_as_uint(part[2][x]));
+    }
+    const RowScale q = row_scale(amax);
     if (t == 0) reinterpret_cast<float*>(a.sx)[row] = q.s;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -172,8 +184,11 @@ template <int DT, int RT>
 static void launch_norm(const NormArgs& a, hipStream_t s) {
     const int units = (mx_kp(a.H) + 511) / 512;                 // rounds of one wave
     const unsigned M = unsigned(a.M);
+    // few rows: as many waves a row as it has rounds, so that a row is one trip to memory and one sum (8 rows of
+    // 4096: 5.4 -> 4.5 us)
     if (units <= 1) norm_residual_kernel<DT, RT, 1, 1><<<dim3((M + 3) / 4), dim3(256), 0, s>>>(a);
     else if (units <= 4) norm_residual_kernel<DT, RT, 4, 1><<<dim3(M), dim3(256), 0, s>>>(a);
+    else if (units <= 16 && M <= 512) norm_residual_kernel<DT, RT, 16, 1><<<dim3(M), dim3(1024), 0, s>>>(a);
     else if (units <= 8) norm_residual_kernel<DT, RT, 4, 2><<<dim3(M), dim3(256), 0, s>>>(a);
     else if (units <= 16) norm_residual_kernel<DT, RT, 4, 4><<<dim3(M), dim3(256), 0, s>>>(a);
     else if (units <= 32) norm_residual_kernel<DT, RT, 16, 2><<<dim3(M), dim3(1024), 0, s>>>(a);
