@@ -40,6 +40,31 @@ __device__ __forceinline__ int mx_row_last(const MxArgs& a, int e) {
     return a.offsets ? min(max(a.offsets[e + 1], 0), a.rows) : a.rows;
 }
 
+// Scales of the two gate and the two up tiles of a wave in the paired form, where the first gate tile is even.  The gate tiles' bytes
+// are in one word, the up tiles' in one or two (in the second, b, only if the first up tile is the last of its four).
+struct MxPairScales {
+    unsigned gate, up, up2;   // byte offsets of the words in the scales of step 0; NONE: not needed
+    int gshift, ubyte;        // where the two bytes are
+};
+template <unsigned NONE>
+__device__ __forceinline__ MxPairScales mx_pair_scales(const MxArgs& a, const int tile, const bool there, const int lane) {
+    const int up = tile + a.N / 16;
+    const unsigned quad = unsigned(a.K1) * 256u, l = unsigned(lane) * 4u;
+    return {there ? unsigned(tile >> 2) * quad + l : NONE, there ? unsigned(up >> 2) * quad + l : NONE,
+            there && (up & 3) == 3 && tile + 1 < a.N / 16 ? unsigned((up >> 2) + 1) * quad + l : NONE, (tile & 2) * 8, up & 3};
+}
+
+// Inclusive sum over the lanes up to this one: shifts within rows of 16 by DPP, then the rows' last lanes passed on.
+__device__ __forceinline__ int wave_prefix(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+
 // Token of a gather entry, or -1 if it names no row of X.
 __device__ __forceinline__ int mx_token(const MxArgs& a, int g) {
     const int t = int((__umulhi(unsigned(g), a.div_mul) + unsigned(g)) >> a.div_shift);

@@ -44,15 +44,11 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            if (c0 + j * 64 >= a.E) break;
             // malformed offsets cannot move a tile outside the rows of the call
             const int e0 = min(max(b[j], 0), a.rows), e1 = min(max(e[j], e0), a.rows), cnt = e1 - e0;
             const int t = (cnt + MXS_ROWS - 1) / MXS_ROWS;
-            int incl = t;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_up(incl, o, 64);
-                if (lane >= o) incl += y;
-            }
+            const int incl = wave_prefix(t);
             const unsigned long long hit = __ballot(slot >= base + incl - t && slot < base + incl);
             if (hit) {
                 const int src = __ffsll((long long)hit) - 1;
@@ -68,14 +64,14 @@ __device__ __forceinline__ TileRows mx_find(const MxArgs& a, int slot, int lane)
 }
 
 template <int FMT, bool PAIR>
-__global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
+__global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb, int slots) {
     constexpr int CT = MXS_TILES, COLS = PAIR ? CT * 8 : CT * 16;
     constexpr int STEP_BYTES = FMT == W4A8_MX_FP4 ? 64 : 128;   // of an activation row
     __shared__ v4f red[MXS_WAVES * CT * 64];                    // partial sums: [wave][tile][lane]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, c16 = lane & 15;
-    for (unsigned item = blockIdx.x;; item += gridDim.x) {
-        const int slot = int(item / unsigned(ncb)), cb = int(item - unsigned(slot) * unsigned(ncb));
+    const int first = int(blockIdx.x / unsigned(ncb)), cb = int(blockIdx.x - unsigned(first) * unsigned(ncb));
+    for (int slot = first; slot < slots; slot += int(gridDim.x / unsigned(ncb))) {
         const TileRows tr = mx_find(a, slot, lane);
         const int expert = __builtin_amdgcn_readfirstlane(tr.expert);
         if (expert < 0) return;                                 // uniform over the workgroup; no later slot has a tile
@@ -91,19 +87,20 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
         const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint8_t*>(wexp + a.scales_off), 0, int(unsigned((ntiles + 3) / 4) * unsigned(a.K1) * 256u), 0x00020000);
         constexpr unsigned NONE = 0x80000000u;                  // codes end below it, so that a sum with a valid offset does not wrap
-        unsigned woff[CT], soff[PAIR ? CT : 1];                 // (unpaired: the scales of the 4 tiles are one word)
+        unsigned woff[CT];
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             const int own = PAIR ? cb * (CT / 2) + t % (CT / 2) : cb * CT + t;      // among the gate, or all, tiles
             const int tile = PAIR && t >= CT / 2 ? own + a.N / 16 : own;
             const bool there = own < (PAIR ? a.N / 16 : ntiles);
             woff[t] = there ? unsigned(tile) * unsigned(a.K1) * 1024u + unsigned(lane) * 16u : NONE;
-            if (PAIR) soff[PAIR ? t : 0] = there ? unsigned(tile >> 2) * unsigned(a.K1) * 256u + unsigned(lane) * 4u + unsigned(tile & 3) : NONE;
         }
-        if (!PAIR) soff[0] = unsigned(cb) * unsigned(a.K1) * 256u + unsigned(lane) * 4u;
+        // the scales of the 4 tiles are one word (paired form: see MxPairScales)
+        const MxPairScales ps = mx_pair_scales<NONE>(a, cb * 2, cb * 2 < a.N / 16, lane);
+        const unsigned soff = unsigned(cb) * unsigned(a.K1) * 256u + unsigned(lane) * 4u;
         struct Step {
             v4i w[CT];
-            uint32_t sw[PAIR ? CT : 1];
+            uint32_t sw[PAIR ? 3 : 1];
             MxOperand<FMT> x;
             uint32_t sx;
         };
@@ -111,10 +108,11 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
             const unsigned at = step < a.K1 ? unsigned(step) * 1024u : NONE, sat = step < a.K1 ? unsigned(step) * 256u : NONE;
 #pragma unroll
             for (int t = 0; t < CT; ++t) b.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[t] + at, 0, 0);
-#pragma unroll
-            for (int t = 0; t < (PAIR ? CT : 1); ++t)
-                b.sw[t] = PAIR ? uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, soff[t] + sat, 0, 0))
-                               : uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, soff[t] + sat, 0, 0));
+            b.sw[0] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, (PAIR ? ps.gate : soff) + sat, 0, 0));
+            if constexpr (PAIR) {
+                b.sw[1] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, ps.up + sat, 0, 0));
+                b.sw[2] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(sr, ps.up2 + sat, 0, 0));
+            }
         };
         const uint8_t *xrow, *srow;
         auto load_x = [&](Step& b, const int s) __attribute__((always_inline)) {
@@ -127,8 +125,9 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
         Step s0, s1;
         load_w(s0, wave);
         load_w(s1, wave + MXS_WAVES);
-        {   // the activation row of this lane; rows past the tile repeat its first row (their sums are not stored)
-            const int src = mx_src(a, rbeg + (c16 < nrows ? c16 : 0));
+        // the activation row of this lane; rows past the tile repeat its first row (their sums are not stored)
+        const int src = mx_src(a, rbeg + (c16 < nrows ? c16 : 0));
+        {
             const size_t r = size_t(src < 0 ? 0 : src);
             xrow = a.X + r * a.rowb + unsigned(q) * 16u;
             srow = a.sx + r * (size_t(a.K1) * 4) + unsigned(q);
@@ -141,8 +140,11 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
         for (int t = 0; t < CT; ++t) acc[t] = v4f{};
         auto multiply = [&](const Step& b) __attribute__((always_inline)) {
             if constexpr (PAIR) {
-#pragma unroll
-                for (int t = 0; t < CT; ++t) acc[t] = mx_mfma<FMT, 0>(b.w[t], b.x, acc[t], b.sw[PAIR ? t : 0], b.sx);
+                const uint32_t g = b.sw[0] >> ps.gshift, u = __builtin_amdgcn_alignbyte(b.sw[2], b.sw[1], ps.ubyte);
+                acc[0] = mx_mfma<FMT, 0>(b.w[0], b.x, acc[0], g, b.sx);
+                acc[1] = mx_mfma<FMT, 1>(b.w[1], b.x, acc[1], g, b.sx);
+                acc[2] = mx_mfma<FMT, 0>(b.w[2], b.x, acc[2], u, b.sx);
+                acc[3] = mx_mfma<FMT, 1>(b.w[3], b.x, acc[3], u, b.sx);
             } else {
                 acc[0] = mx_mfma<FMT, 0>(b.w[0], b.x, acc[0], b.sw[0], b.sx);
                 acc[1] = mx_mfma<FMT, 1>(b.w[1], b.x, acc[1], b.sw[0], b.sx);
@@ -173,7 +175,8 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
             if (PAIR && a.Hq) {                                 // 8 neighbouring lanes take a row's block of 32 columns
                 const int j = tid & 7, row = tid >> 3, at = (j >> 2) * 64 + (j & 3) * 16 + row, block = cb * (COLS / 32);
                 v4f h{};
-                if (row < nrows && cb * COLS + j * 4 < a.N && mx_src(a, rbeg + row) >= 0) {
+                const bool dead = __shfl(src, row & 15, 64) < 0;
+                if (row < nrows && cb * COLS + j * 4 < a.N && !dead) {
                     const v4f g = total(at), u = total(at + ITEMS / 2);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[k] = mx_silu(g[k]) * u[k];
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) y[k] = mx_silu(y[k]) * up[k];
                     }
-                    if (mx_src(a, rbeg + row) < 0) y = v4f{};
+                    if (src < 0) y = v4f{};
                     mx_store(a, size_t(rbeg + row) * a.ldy + col, min(4, a.N - col), y);
                 }
             }
@@ -198,13 +201,13 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb) {
     }
 }
 
-// All tiles up to a bound that keeps a launch's work-items below 2^32; beyond it workgroups go round.
+// A workgroup for each tile, up to a number that keeps a launch's work-items below 2^32; beyond it they go round.
 template <int FMT, bool PAIR>
 static void launch_stream(const MxArgs& a, hipStream_t s) {
     constexpr int cols = PAIR ? MXS_TILES * 8 : MXS_TILES * 16;
-    const int ncb = (a.N + cols - 1) / cols;
-    const long long slots = a.rows / MXS_ROWS + std::min(a.E, a.rows);          // an upper bound of the row tiles
-    mx_stream_kernel<FMT, PAIR><<<dim3(unsigned(std::min(slots * ncb, 1ll << 22))), dim3(512), 0, s>>>(a, ncb);
+    const int ncb = (a.N + cols - 1) / cols;                    // at most 2^14
+    const int slots = a.rows / MXS_ROWS + std::min(a.E, a.rows);                // an upper bound of the row tiles
+    mx_stream_kernel<FMT, PAIR><<<dim3(unsigned(std::min(slots, (1 << 22) / ncb) * ncb)), dim3(512), 0, s>>>(a, ncb, slots);
 }
 
 // Which kernel a call takes: the least of five estimates, in us.  The host knows rows and E, not the experts' rows: of E experts

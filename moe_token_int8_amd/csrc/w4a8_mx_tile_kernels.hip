@@ -89,7 +89,7 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
     constexpr int SB = 4 * SPS;                                 // scale bytes of a row in a stage
     constexpr int COPIES = BM * 8 / THREADS;                    // 16-byte copies of a thread in a stage
     constexpr int G = FP4 ? MT / 2 : MT == 8 ? 2 : 1, NG = MT / G;      // row tiles of a group, groups of a step
-    constexpr int FILL = COPIES + 1, WL = PAIR ? 8 : 5;         // memory operations of a stage's copies, of a step's weights
+    constexpr int FILL = COPIES + 1, WL = PAIR ? 7 : 5;         // memory operations of a stage's copies, of a step's weights
     constexpr int LIST = 64;                                    // tiles looked up at a time
     static_assert(NG % 2 == 0 && COPIES * THREADS == BM * 8 && BM * SB <= THREADS * 4, "shapes");
     __shared__ __align__(1024) uint8_t stage0[STAGE];
@@ -118,11 +118,7 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
             incl += t[i];
         }
         int excl = -incl;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int y = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += y;
-        }
+        incl = wave_prefix(incl);
         if (lane == 63) wsum[wave] = incl;
         __syncthreads();
         for (int w = 0; w < wave; ++w) incl += wsum[w];
@@ -169,17 +165,17 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
     // an offset past everything and load zeros.  The step goes into the weights' scalar offset, which the range check leaves
     // out: steps past the last one, which are requested but not used, repeat it.
     constexpr unsigned NONE = 0xf0000000u;
-    unsigned xoff[COPIES], soff, woff[4], wsoff[PAIR ? 4 : 1];
+    unsigned xoff[COPIES], soff, woff[4], wsoff = NONE;
+    MxPairScales ps{NONE, NONE, NONE, 0, 0};                    // paired form
     __amdgpu_buffer_rsrc_t xr, sr, wr, wsr;
     v4i w[3][4];
-    uint32_t sw[3][PAIR ? 4 : 1];
+    uint32_t sw[3][PAIR ? 3 : 1];
 
     auto load_w_part = [&](const int set, const int step, const int part) __attribute__((always_inline)) {
         const int k = min(step, a.K1 - 1);
         if (part < 4) w[set][part & 3] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[part & 3], k * 1024, 0);
-        else sw[set][PAIR ? part & 3 : 0] =
-                 PAIR ? uint32_t(__builtin_amdgcn_raw_buffer_load_b8(wsr, wsoff[PAIR ? part & 3 : 0], k * 256, 0))
-                      : uint32_t(__builtin_amdgcn_raw_buffer_load_b32(wsr, wsoff[0], k * 256, 0));
+        else sw[set][PAIR ? part - 4 : 0] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(
+                 wsr, !PAIR ? wsoff : part == 4 ? ps.gate : part == 5 ? ps.up : ps.up2, k * 256, 0));
     };
     auto load_w = [&](const int set, const int step) __attribute__((always_inline)) {
 #pragma unroll
@@ -222,8 +218,13 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
             const int t = PAIR && n >= 2 ? own + a.N / 16 : own;
             const bool there = own < (PAIR ? a.N / 16 : ntiles);
             woff[n] = there ? unsigned(t) * (unsigned(a.K1) * 1024u) + unsigned(lane) * 16u : NONE;
-            if (PAIR) wsoff[PAIR ? n : 0] = there ? unsigned(t >> 2) * (unsigned(a.K1) * 256u) + unsigned(lane) * 4u + unsigned(t & 3) : NONE;
-            else if (n == 0) wsoff[0] = there ? unsigned(t >> 2) * (unsigned(a.K1) * 256u) + unsigned(lane) * 4u : NONE;
+        }
+        if (PAIR) {
+            const int tile = (g.w * WN + wn) * 2;
+            ps = mx_pair_scales<NONE>(a, tile, tile < a.N / 16, lane);
+        } else {
+            const int quad = g.w * WN + wn;
+            wsoff = quad * 4 < ntiles ? unsigned(quad) * (unsigned(a.K1) * 256u) + unsigned(lane) * 4u : NONE;
         }
         const size_t srow = size_t(a.K1) * 4, base = a.gather ? 0 : size_t(g.y), nrow = size_t(a.gather ? a.src_rows : g.z);
         xr = mx_buffer(a.X + base * a.rowb, nrow * a.rowb);
@@ -345,9 +346,14 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
                             }
                             __builtin_amdgcn_sched_barrier(0);
                             if constexpr (PAIR) {
-#pragma unroll
-                                for (int n = 0; n < 4; ++n)
-                                    acc[n][m] = mx_mfma<FMT, 0>(w[set][n], x[b][i], acc[n][m], sw[set][PAIR ? n : 0], sx[b][i]);
+                                if (m == 0) {                   // the bytes in place, once a step
+                                    sw[set][0] >>= ps.gshift;
+                                    sw[set][PAIR ? 1 : 0] = __builtin_amdgcn_alignbyte(sw[set][PAIR ? 2 : 0], sw[set][PAIR ? 1 : 0], ps.ubyte);
+                                }
+                                acc[0][m] = mx_mfma<FMT, 0>(w[set][0], x[b][i], acc[0][m], sw[set][0], sx[b][i]);
+                                acc[1][m] = mx_mfma<FMT, 1>(w[set][1], x[b][i], acc[1][m], sw[set][0], sx[b][i]);
+                                acc[2][m] = mx_mfma<FMT, 0>(w[set][2], x[b][i], acc[2][m], sw[set][PAIR ? 1 : 0], sx[b][i]);
+                                acc[3][m] = mx_mfma<FMT, 1>(w[set][3], x[b][i], acc[3][m], sw[set][PAIR ? 1 : 0], sx[b][i]);
                             } else {
                                 acc[0][m] = mx_mfma<FMT, 0>(w[set][0], x[b][i], acc[0][m], sw[set][0], sx[b][i]);
                                 acc[1][m] = mx_mfma<FMT, 1>(w[set][1], x[b][i], acc[1][m], sw[set][0], sx[b][i]);
