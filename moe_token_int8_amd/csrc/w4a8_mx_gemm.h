@@ -177,4 +177,8 @@ __device__ __forceinline__ void mx_store_block(const MxArgs& a, const int row, c
 enum MxTile { MX_TILE_WIDE, MX_TILE_128, MX_TILE_64, MX_TILE_32 };
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s);
 
+// Routing (the results of w4a8_moe_align) and the codes of the M bfloat16 rows of X in one launch (w4a8_mx_quant_kernels.hip).
+void launch_route_quant(const int32_t* ids, int R, int E, int32_t* rows, int32_t* offs, int32_t* inv, const void* X, int M, int K,
+                        int fmt, uint8_t* Xq, uint8_t* sx, hipStream_t s);
+
 }  // namespace w4a8

@@ -16,11 +16,10 @@ namespace w4a8 {
 // Rows -> codes and scales.  A lane takes 8 neighbours along K (16 or 32 bytes in, 4 or 8 out), 4 lanes a block, a wave 512
 // of a row; the block's maximum is two quad permutes.  Bound by the copy: 2 bytes in and 17/32 or 33/32 out an element.
 template <int DT, int FMT>
-__global__ __launch_bounds__(256) void mx_quant_kernel(const uint8_t* X, long long M, int K, long long ldx, int chunks,
-                                                       uint8_t* Xq, uint8_t* sx) {
+__device__ __forceinline__ void quant_chunk(const uint8_t* X, const long long M, const int K, const long long ldx, const int chunks,
+                                            uint8_t* Xq, uint8_t* sx, const long long w, const int lane) {
     constexpr int ES = DT == W4A8_F32 ? 4 : 2;
-    const int lane = int(threadIdx.x) & 63, Kp = mx_kp(K);
-    const long long w = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int Kp = mx_kp(K);
     const long long row = w / chunks;
     const int k = int(w - row * chunks) * 512 + lane * 8;
     if (row >= M || k >= Kp) return;                            // whole blocks of 4 lanes: Kp is a multiple of 128
@@ -31,6 +30,70 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(const uint8_t* X, long lo
     if constexpr (FMT == W4A8_MX_FP4) *reinterpret_cast<uint32_t*>(Xq + size_t(row) * size_t(Kp / 2) + k / 2) = q.x;
     else *reinterpret_cast<uint2*>(Xq + size_t(row) * size_t(Kp) + k) = q;
     if ((lane & 3) == 0) sx[size_t(row) * size_t(Kp / 32) + k / 32] = uint8_t(byte);
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(256) void mx_quant_kernel(const uint8_t* X, long long M, int K, long long ldx, int chunks,
+                                                       uint8_t* Xq, uint8_t* sx) {
+    const long long w = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    quant_chunk<DT, FMT>(X, M, K, ldx, chunks, Xq, sx, w, int(threadIdx.x) & 63);
+}
+
+// One expert's part of the order of the routed rows, by one wave: ids below e count towards the expert's first place, ids equal to
+// e take the next places in their order, and each wave reads all ids for itself, so that no wave waits for another.  (The same
+// results as a counting sort in one workgroup, which is the quicker way for many ids.)
+__device__ __forceinline__ void route_expert(const int* ids, const int R, const int E, const int e, int* rows, int* offs, int* inv,
+                                             const int lane) {
+    int below = 0, mine = 0;
+    for (int c = 0; c < R; c += 1024) {                         // 16 loads in flight
+        int id[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int r = c + j * 64 + lane;
+            id[j] = r < R ? ids[r] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            below += __popcll(__ballot(id[j] >= 0 && id[j] < e));
+            mine += __popcll(__ballot(id[j] == e));
+        }
+    }
+    if (lane == 0) {
+        offs[e] = below;
+        if (e == E - 1) offs[E] = below + mine;
+    }
+    if (!mine && e != 0) return;
+    for (int c = 0; c < R; c += 1024) {
+        int id[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int r = c + j * 64 + lane;
+            id[j] = r < R ? ids[r] : E;
+            if (e == 0 && r < R && (id[j] < 0 || id[j] >= E)) inv[r] = -1;      // counted nowhere
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const unsigned long long hit = __ballot(id[j] == e);
+            const int at = below + __popcll(hit & ((1ull << lane) - 1)), r = c + j * 64 + lane;
+            if (id[j] == e) rows[at] = r, inv[r] = at;
+            below += __popcll(hit);
+        }
+    }
+}
+
+// The first steps of an expert layer in one launch: the order of the routed rows, by the first workgroups (a wave an expert), and
+// the codes of the tokens, by the others.
+template <int FMT>
+__global__ __launch_bounds__(256) void mx_route_quant_kernel(const int* ids, int R, int E, int* rows, int* offs, int* inv,
+                                                             const uint8_t* X, int M, int K, int chunks, uint8_t* Xq, uint8_t* sx) {
+    const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int routing = (E + 3) / 4;
+    if (int(blockIdx.x) < routing) {
+        const int e = int(blockIdx.x) * 4 + wave;
+        if (e < E) route_expert(ids, R, E, e, rows, offs, inv, lane);
+    } else {
+        quant_chunk<W4A8_BF16, FMT>(X, M, K, K, chunks, Xq, sx, (long long)(int(blockIdx.x) - routing) * 4 + wave, lane);
+    }
 }
 
 // Codes and scales -> values: 8 a lane.
@@ -137,6 +200,15 @@ static void launch_quant(const void* X, int M, int K, int ldx, int fmt, void* Xq
     uint8_t* q = static_cast<uint8_t*>(Xq);
     if (fmt == W4A8_MX_FP4) mx_quant_kernel<DT, W4A8_MX_FP4><<<grid, dim3(256), 0, s>>>(x, M, K, ldx, chunks, q, sx);
     else mx_quant_kernel<DT, W4A8_MX_FP8><<<grid, dim3(256), 0, s>>>(x, M, K, ldx, chunks, q, sx);
+}
+
+void launch_route_quant(const int32_t* ids, int R, int E, int32_t* rows, int32_t* offs, int32_t* inv, const void* X, int M, int K,
+                        int fmt, uint8_t* Xq, uint8_t* sx, hipStream_t s) {
+    const int chunks = (mx_kp(K) + 511) / 512;
+    const dim3 grid(unsigned((E + 3) / 4 + ((long long)M * chunks + 3) / 4));
+    const uint8_t* x = static_cast<const uint8_t*>(X);
+    if (fmt == W4A8_MX_FP4) mx_route_quant_kernel<W4A8_MX_FP4><<<grid, dim3(256), 0, s>>>(ids, R, E, rows, offs, inv, x, M, K, chunks, Xq, sx);
+    else mx_route_quant_kernel<W4A8_MX_FP8><<<grid, dim3(256), 0, s>>>(ids, R, E, rows, offs, inv, x, M, K, chunks, Xq, sx);
 }
 
 template <int FMT>
