@@ -316,6 +316,7 @@ static int check_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* g
     if (gather ? (k <= 0 || src_rows == 0) : src_rows < rows) return W4A8_EINVAL;
     if (E > 1 && stride < mx_layout(width, K).total) return W4A8_EINVAL;
     if (!aligned_to(Xq, 16) || !aligned_to(sx, 4) || !aligned_to(W, 16) || (stride & 15)) return W4A8_EINVAL;
+    if (!aligned_to(gather, 4) || !aligned_to(offsets, 4)) return W4A8_EINVAL;
     return W4A8_OK;
 }
 
@@ -439,7 +440,7 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
 }
 
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt) {
-    if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0 || H > MX_MAX_K || I > MX_MAX_N / 2 ||
+    if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0 || H > MX_MAX_K || I > MX_MAX_N / 2 || (long long)T * k > MX_MAX_ROWS ||
         (fmt != W4A8_MX_FP4 && fmt != W4A8_MX_FP8))
         return 0;
     return mx_layer_ws(T, k, H, I, E, fmt).total;
@@ -453,7 +454,8 @@ int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T
     int st = mx_check_weights(2 * I, H);
     if (st || (st = mx_check_weights(H, I))) return st;
     if (T == 0) return W4A8_OK;
-    if (!X || !ids || !w || !ws || !out || !aligned_to(X, 2) || !aligned_to(out, 2)) return W4A8_EINVAL;
+    if (!X || !ids || !w || !ws || !out || !aligned_to(X, 2) || !aligned_to(out, 2) || !aligned_to(ids, 4) || !aligned_to(w, 4))
+        return W4A8_EINVAL;
     const int chunks = (H + 1023) / 1024, ldy = (H + 3) & ~3;
     if ((long long)T * chunks >= (1ll << 24)) return W4A8_EUNSUPPORTED;     // less than 2^32 work-items
     const MxLayerWs L = mx_layer_ws(T, k, H, I, E, fmt);

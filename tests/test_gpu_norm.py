@@ -160,3 +160,29 @@ def test_zeros_and_nan_rows(H):
 def test_no_rows():
     X = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
     L.w4a8_norm_residual(X, X, L.norm_desc(), torch.ones(64, device=DEV), X, X)
+
+
+def test_rows_far_apart():
+    """Row strides whose product with the rows passes 2^32 bytes, and rows as wide as the calls take."""
+    for M, H, ld in ((300, 700, 1 << 23), (2, 65536, 1 << 30)):
+        c = inputs(8, M, H, "bf16", "bf16", True, "token")
+        want_r, want_h = run(c)
+        d = {n: torch.empty(M * ld, dtype=torch.bfloat16, device=DEV).view(M, ld)[:, 3:3 + H] for n in ("X", "r", "gate", "Y")}
+        for n in ("X", "r", "gate"):
+            d[n].copy_(c[n])
+        L.w4a8_norm_residual(d["X"], d["r"], L.norm_desc(1e-6, 1e-5, 0.5), c["w"].to(DEV), d["r"], d["Y"], post_w=c["p"].to(DEV),
+                             gate=d["gate"])
+        assert torch.equal(d["r"], want_r) and torch.equal(d["Y"], want_h)
+        check(c, got_r=want_r, got_h=want_h)
+
+
+@pytest.mark.parametrize("M", [4097, 70001])
+def test_many_rows(M):
+    """More rows than workgroups at a time: every row is the one that a call of it alone gives."""
+    c = inputs(M, M, 96, "bf16", "f32", True, "channel")
+    r, h = run(c)
+    pick = [0, 1, 255, 256, 4095, M - 2, M - 1]
+    part = dict(c, X=c["X"][pick], r=c["r"][pick])
+    r2, h2 = run(part)
+    assert torch.equal(r[pick], r2) and torch.equal(h[pick], h2)
+    check(c, got_r=r, got_h=h)
