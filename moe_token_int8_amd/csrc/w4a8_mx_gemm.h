@@ -173,8 +173,8 @@ __device__ __forceinline__ void mx_store_block(const MxArgs& a, const int row, c
     if (j == 0) a.sh[at] = uint8_t(byte);
 }
 
-// MFMA tiles (w4a8_mx_tile_kernels.hip): 128 x 512, 128 x 256, 64 x 256 or 32 x 256.
-enum MxTile { MX_TILE_WIDE, MX_TILE_128, MX_TILE_64, MX_TILE_32 };
+// MFMA tiles (w4a8_mx_tile_kernels.hip): 128 x 512, 128 x 256, 64 x 256, 32 x 256 or 32 x 128.
+enum MxTile { MX_TILE_WIDE, MX_TILE_128, MX_TILE_64, MX_TILE_32, MX_TILE_SMALL };
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s);
 
 // Routing (the results of w4a8_moe_align) and the codes of the M bfloat16 rows of X in one launch (w4a8_mx_quant_kernels.hip).

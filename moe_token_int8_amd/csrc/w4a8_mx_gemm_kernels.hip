@@ -210,24 +210,29 @@ static void launch_stream(const MxArgs& a, hipStream_t s) {
     mx_stream_kernel<FMT, PAIR><<<dim3(unsigned(std::min(slots, (1 << 22) / ncb) * ncb)), dim3(512), 0, s>>>(a, ncb, slots);
 }
 
-// Which kernel a call takes: the least of five estimates, in us.  The host knows rows and E, not the experts' rows: of E experts
-// about E (1 - exp(-rows / E)) have any, and each ends in a row tile that is half empty.  Streaming tiles: 512 workgroups at a time
-// take o and l a step.  MFMA tiles: `per` workgroups share a compute unit, a step takes l, or thr for each of them.  Either reads
-// the weights at bw TB/s.  Fitted to 352 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, K 300 .. 14336), of
-// which the choice loses 5 % in the mean against the best of all, 60 % at worst.  Measured, us, streaming / tiles of 32, 64, 128 x
-// 256 and 128 x 512: 16 x 4096 x 14336 fp8 9 / 19, 19, 26, 38; 128 x 14336 x 4096 fp4 26 / 39, 44, 54, 78; 512 x 4096 x 4096 fp4 - / 19, 16,
-// 20, 27; 2048 x 4096 x 14336 fp8 - / 150, 117, 103, 95; 2 rows for each of 256 experts, 2048 x 7168 fp8 393 / 276, 276, 298, 301; 64
-// rows for each of 64, gate/up 4096 x 1408 fp8 299 / 129, 123, 114, 103; 32 rows for each of 64, 1408 x 4096 fp4 114 / 53, 51, 52, 57.
-enum MxKernel { MXK_STREAM, MXK_TILE32, MXK_TILE64, MXK_TILE128, MXK_WIDE, MXK_KERNELS };
+// Which kernel a call takes: the least of six estimates, in us.  The host knows rows and E, not the experts' rows: of E experts
+// about E (1 - exp(-rows / E)) have any, and each ends in a row tile that is half empty.  n tiles meet c n / 256 times on a compute
+// unit (c > 1: a launch that fits does not spread evenly).  Streaming tiles, two of which share a unit, take o and l a step.  Of MFMA
+// tiles `per` share one, a step takes l, or thr for each of them.  Either reads the weights at bw TB/s, which adds up with the steps as
+// far as a norm of third powers says.  Fitted to 414 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, evenly or
+// skewed, K 300 .. 14336), of which the choice loses 2 % in the mean against the best of all, 27 % at worst.  Measured, us, streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x 256 and 128 x 512, fp8:
+//   16 x 4096 x 14336                      9 /  13,  19,  18,  26,  38       128 x 4096 x 14336            36 /  21,  22,  21,  29,  42
+//   256 x 14336 x 4096                     - /  41,  56,  54,  80, 120       2048 x 14336 x 4096            - / 146, 133,  96, 129, 122
+//   2048 x 4096 x 14336                    - / 151, 145, 111,  97,  92
+//   4 rows for each of 256, 2048 x 7168  401 / 321, 328, 331, 351, 348       64 rows for each, the same     - / 620, 566, 477, 474, 457
+enum MxKernel { MXK_STREAM, MXK_SMALL, MXK_TILE32, MXK_TILE64, MXK_TILE128, MXK_WIDE, MXK_KERNELS };
 
 static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
     struct Rate {
         int rows, cols, per;
-        double o, l, thr, bw;
+        double o, l, thr, bw, c;
     };
-    static const Rate rates[2][MXK_KERNELS] = {
-        {{16, 64, 2, 3.6, 0.132, 0, 3.5}, {32, 256, 4, 0.3, 0.48, 0.41, 5.1}, {64, 256, 3, 1.2, 0.47, 0.51, 5.2}, {128, 256, 2, 3.3, 0, 0.68, 4.8}, {128, 512, 1, 4.3, 0.09, 1.12, 4.4}},
-        {{16, 64, 2, 3.4, 0.102, 0, 3.8}, {32, 256, 4, 0.5, 0.11, 0.34, 5.3}, {64, 256, 3, 1.1, 0.40, 0.40, 5.0}, {128, 256, 2, 3.5, 0.38, 0.44, 4.5}, {128, 512, 1, 3.8, 0.65, 0.78, 4.7}}};
+    static const Rate rates[2][MXK_KERNELS] = {{{16, 64, 2, 1.73, 0.137, 0.000, 7.69, 1.91}, {32, 128, 4, 0.27, 0.248, 0.181, 5.27, 1.65},
+                                                {32, 256, 4, 0.00, 0.454, 0.404, 5.52, 1.05}, {64, 256, 2, 2.30, 0.086, 0.396, 5.51, 1.74},
+                                                {128, 256, 2, 3.53, 0.091, 0.672, 7.75, 1.71}, {128, 512, 1, 5.47, 0.004, 1.205, 7.26, 2.00}},
+                                               {{16, 64, 2, 1.55, 0.108, 0.000, 7.80, 2.00}, {32, 128, 4, 0.00, 0.196, 0.171, 5.43, 1.46},
+                                                {32, 256, 4, 0.00, 0.275, 0.301, 5.69, 1.33}, {64, 256, 2, 1.81, 0.106, 0.301, 5.40, 1.71},
+                                                {128, 256, 2, 3.40, 0.195, 0.446, 6.00, 1.73}, {128, 512, 1, 5.24, 0.351, 0.803, 6.04, 2.00}}};
     const double rows = a.rows, E = a.E, width = pair ? 2.0 * a.N : a.N, steps = a.K1;
     const double active = E > 1 ? std::min(rows, E * (1 - std::exp(-rows / E))) : 1;
     const double bytes = active * width * steps * 68;           // 128 k of a column
@@ -235,16 +240,18 @@ static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
     double least = 1e300;
     for (int v = 0; v < MXK_KERNELS; ++v) {
         const Rate& r = rates[fp4][v];
-        const double rt = E > 1 ? std::max(active, rows / r.rows + 0.5 * active) : std::ceil(rows / r.rows), n = rt * std::ceil(width / r.cols);
+        const double rt = E > 1 ? std::max(active, rows / r.rows + 0.5 * active) : std::ceil(rows / r.rows);
+        const double n = rt * std::ceil(width / r.cols);
         double us;
         if (v == MXK_STREAM) {
-            us = std::max(1.0, n / 512) * (r.o + r.l * steps);
+            us = std::max(1.0, r.c * n / 512) * (r.o + r.l * steps);
         } else {
             const double co = n / 256, full = co / r.per;
             const double rounds = full < 1 ? 1 : full < 4 ? std::ceil(full) : full + 0.5;
-            us = 4 + rounds * (r.o + steps * std::max(r.l, r.thr * std::min(std::max(co, 1.0), double(r.per))));
+            us = 4 + rounds * (r.o + steps * std::max(r.l, r.thr * std::min(std::max(r.c * co, 1.0), double(r.per))));
         }
-        us = std::max(us, 4 + bytes / (r.bw * 1e6));
+        const double read = 4 + bytes / (r.bw * 1e6);
+        us = std::cbrt(us * us * us + read * read * read);
         if (us < least) least = us, best = MxKernel(v);
     }
     return best;
@@ -255,6 +262,7 @@ static const char* launch_mx(const MxArgs& a, hipStream_t s) {
     // the tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
     const bool near = !a.gather || (long long)a.src_rows * a.rowb < 0xe0000000ll;
     switch (near ? choose_mx(a, FMT == W4A8_MX_FP4, PAIR) : MXK_STREAM) {
+        case MXK_SMALL: launch_mx_tile(a, FMT, PAIR, MX_TILE_SMALL, s); return "mx_tile_kernel (32 x 128)";
         case MXK_TILE32: launch_mx_tile(a, FMT, PAIR, MX_TILE_32, s); return "mx_tile_kernel (32 x 256)";
         case MXK_TILE64: launch_mx_tile(a, FMT, PAIR, MX_TILE_64, s); return "mx_tile_kernel (64 x 256)";
         case MXK_TILE128: launch_mx_tile(a, FMT, PAIR, MX_TILE_128, s); return "mx_tile_kernel (128 x 256)";

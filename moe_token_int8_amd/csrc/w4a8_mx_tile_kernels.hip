@@ -14,8 +14,10 @@ namespace w4a8 {
 // matching half up columns).  Each wave owns all rows and 64 columns: 4 MT accumulators of 4 a lane.
 //
 // The packed weights are in operand order, so they go from memory straight to registers, 4 KiB a wave and step of 128 k, two
-// steps ahead, each to one wave.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4, one of
-// fp8), copied without registers (buffer_load ... lds), three stages deep, with a stage's scale bytes behind its codes.
+// steps ahead (DEEP: five), each to one wave.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4,
+// one of fp8), copied without registers (buffer_load ... lds), three stages deep (DEEP, fp8: six), with a stage's scale bytes behind
+// its codes.  DEEP is for launches of few tiles, whose time is one chain of steps over K, each waiting for its loads: 2048 x 14336 x
+// 4096 in fp8, tiles of 64 x 256: 129 -> 96 us; 192 x 14336 x 4096, tiles of 32 x 256 two ahead 56, of 32 x 128 five ahead 34.
 //
 // What bounds it: the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
 // cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 104 us (4.6 PFLOP/s; MFMAs alone on
@@ -79,13 +81,16 @@ __device__ __forceinline__ uint32_t mx_max_rows(uint32_t m) {
     return max(uint32_t(b[0]), uint32_t(b[1]));
 }
 
-template <int FMT, bool PAIR, int WN, int MT>
-__global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != W4A8_MX_FP4) && FMT != MX_FP8_EXACT ? 4 : 3) void mx_tile_kernel(MxArgs a) {
+template <int FMT, bool PAIR, int WN, int MT, bool DEEP>
+__global__ __launch_bounds__(64 * WN, MT == 8 || DEEP ? 2 : (PAIR && FMT != W4A8_MX_FP4) || FMT == MX_FP8_EXACT ? 3 : 4)
+void mx_tile_kernel(MxArgs a) {
     constexpr bool FP4 = FMT == W4A8_MX_FP4;
     constexpr int THREADS = 64 * WN, BM = 16 * MT;
     constexpr int COLS = PAIR ? 32 * WN : 64 * WN;              // columns of Y
     constexpr int SPS = FP4 ? 2 : 1;                            // steps of a stage
     constexpr int CODES = BM * MXT_ROW, STAGE = CODES + THREADS * 4;
+    constexpr int SETS = DEEP ? 6 : 3, AHEAD = SETS - 1;        // register sets of weights, steps that they are requested ahead
+    constexpr int NST = DEEP && !FP4 ? 6 : 3;                   // stages of activations
     constexpr int SB = 4 * SPS;                                 // scale bytes of a row in a stage
     constexpr int COPIES = BM * 8 / THREADS;                    // 16-byte copies of a thread in a stage
     constexpr int G = FP4 ? MT / 2 : MT == 8 ? 2 : 1, NG = MT / G;      // row tiles of a group, groups of a step
@@ -95,6 +100,9 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
     __shared__ __align__(1024) uint8_t stage0[STAGE];
     __shared__ __align__(1024) uint8_t stage1[STAGE];
     __shared__ __align__(1024) uint8_t stage2[STAGE];
+    __shared__ __align__(1024) uint8_t stage3[NST > 3 ? STAGE : 16];
+    __shared__ __align__(1024) uint8_t stage4[NST > 3 ? STAGE : 16];
+    __shared__ __align__(1024) uint8_t stage5[NST > 3 ? STAGE : 16];
     __shared__ int4 list[LIST];                                 // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[MXT_MAX_E + 1];                        // row tiles before expert e
     __shared__ int entries[BM];                                 // gather entries of the next tile's rows
@@ -132,7 +140,7 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
         __syncthreads();
     }
     // Workgroups take the tiles in turn.  Within an expert, panels of MXT_PANEL row tiles go through all columns together.  (In 32
-    // bits: 2^24 rows in tiles of 32, and one more for each of 1024 experts, by 2^20 columns in blocks of 128 or more.)  Consecutive
+    // bits: 2^24 rows in tiles of 32, and one more for each of 1024 experts, by 2^20 columns in blocks of 64 or more.)  Consecutive
     // tiles for a workgroup, which keep its weights from one to the next, share less in L2: 4153 tokens x 6 of 64 experts, 4096 x
     // 2815 320 us in place of 270.
     const unsigned total = unsigned(first[a.E]) * unsigned(ncb);
@@ -154,7 +162,8 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
                 else hi = mid;
             }
             const unsigned in_e = t - unsigned(first[lo]) * unsigned(ncb), panel = in_e / (MXT_PANEL * unsigned(ncb));
-            const unsigned j = in_e - panel * (MXT_PANEL * unsigned(ncb)), rp = min(MXT_PANEL, unsigned(first[lo + 1] - first[lo]) - panel * MXT_PANEL);
+            const unsigned j = in_e - panel * (MXT_PANEL * unsigned(ncb));
+            const unsigned rp = min(MXT_PANEL, unsigned(first[lo + 1] - first[lo]) - panel * MXT_PANEL);
             const int cb = int(j / rp), r0 = mx_row_first(a, lo) + int(panel * MXT_PANEL + j - unsigned(cb) * rp) * BM;
             list[tid] = make_int4(lo, r0, min(BM, mx_row_last(a, lo) - r0), cb);
         }
@@ -168,8 +177,8 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
     unsigned xoff[COPIES], soff, woff[4], wsoff = NONE;
     MxPairScales ps{NONE, NONE, NONE, 0, 0};                    // paired form
     __amdgpu_buffer_rsrc_t xr, sr, wr, wsr;
-    v4i w[3][4];
-    uint32_t sw[3][PAIR ? 3 : 1];
+    v4i w[SETS][4];
+    uint32_t sw[SETS][PAIR ? 3 : 1];
 
     auto load_w_part = [&](const int set, const int step, const int part) __attribute__((always_inline)) {
         const int k = min(step, a.K1 - 1);
@@ -193,7 +202,7 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
 #pragma unroll
         for (int part = 0; part < FILL; ++part) copy_part(st, s, part);
     };
-    const lds_ptr st0 = (lds_ptr)stage0, st1 = (lds_ptr)stage1, st2 = (lds_ptr)stage2;
+    const lds_ptr sts[6] = {(lds_ptr)stage0, (lds_ptr)stage1, (lds_ptr)stage2, (lds_ptr)stage3, (lds_ptr)stage4, (lds_ptr)stage5};
 
     // gather entries of a tile's rows, copied to LDS a tile ahead
     auto request_rows = [&](const int4 g) __attribute__((always_inline)) {
@@ -248,24 +257,22 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
                 if (row < g.z && source(entries[row]) < 0) next_dead |= 1u << m;
             }
         }
-        // in this order, which the waits below count on
-        __builtin_amdgcn_sched_barrier(0);
-        if (!FP4) load_w(0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        copies(st0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (FP4) load_w(0, 0);
-        else load_w(1, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        copies(st1, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        if (FP4) load_w(1, 1);
+        // as the steps before the first one would: the waits below count on this order
+#pragma unroll
+        for (int t = -SPS * (NST - 1) < -AHEAD ? -SPS * (NST - 1) : -AHEAD; t < 0; ++t) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (t + AHEAD >= 0) load_w(t + AHEAD, t + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+            if ((t + SPS * NST) % SPS == 0 && t / SPS + NST - 1 >= 0) copies(sts[t / SPS + NST - 1], t / SPS + NST - 1);
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
-    constexpr int NEWER_FIRST = FP4 ? 2 * WL + FILL : WL + FILL;     // operations behind the copies of stage 0 at the start
+    // operations behind the copies of stage 0 at the start
+    constexpr int NEWER_FIRST = FP4 ? (AHEAD < 3 ? AHEAD : 3) * WL + FILL : (NST - 2) * (WL + FILL);
     // behind those of stage s + 1 at the barrier of stage s, which stands before the last group of its last step
     constexpr int OPS = FP4 ? WL : WL + FILL;                       // of that step, spread over its row tiles
-    constexpr int NEWER = (FP4 ? 2 * WL + FILL : 0) + (MT - G) * OPS / MT;
+    constexpr int NEWER = (FP4 ? 2 * WL + FILL : (NST - 3) * (WL + FILL)) + (MT - G) * OPS / MT;
+    static_assert((NST * SPS) % SETS == 0 && (FP4 ? NST == 3 : AHEAD == NST - 1), "what the counts are made for");
 
     // operands in LDS: byte offsets of this lane in a stage, for the halves of 64 bytes
     int xat[2];
@@ -318,18 +325,17 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
 #pragma unroll
                 for (int m = 0; m < MT; ++m) acc[n][m] = v4f{};
 #pragma unroll
-            for (int m = 0; m < G; ++m) read_tile(0, st0, 0, m);
-            for (int s3 = 0;; s3 += 3) {
+            for (int m = 0; m < G; ++m) read_tile(0, sts[0], 0, m);
+            for (int s0 = 0;; s0 += NST) {
 #pragma unroll
-                for (int u = 0; u < 3; ++u) {
-                    const lds_ptr st = u == 0 ? st0 : u == 1 ? st1 : st2, next = u == 0 ? st1 : u == 1 ? st2 : st0,
-                                  far = u == 0 ? st2 : u == 1 ? st0 : st1;
+                for (int u = 0; u < NST; ++u) {
+                    const lds_ptr st = sts[u], next = sts[(u + 1) % NST], far = sts[(u + NST - 1) % NST];
 #pragma unroll
                     for (int h = 0; h < SPS; ++h) {
                         // A step: for each row tile the operands of a row tile of the next group are read, a share of the step's memory
                         // operations is issued, and 4 MFMAs follow.  (Issued together at the start of the step, the memory operations
                         // of all waves meet: 4096 x 14336 x 4096 in fp4 113 us in place of 104.)
-                        const int step = (s3 + u) * SPS + h, set = (u * SPS + h) % 3;
+                        const int step = (s0 + u) * SPS + h, set = (u * SPS + h) % SETS;
                         const int ops = h == 0 ? WL + FILL : WL;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
@@ -341,8 +347,8 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
                             else read_tile(0, next, 0, i);
 #pragma unroll
                             for (int op = m * ops / MT; op < (m + 1) * ops / MT; ++op) {
-                                if (op < WL) load_w_part((set + 2) % 3, step + 2, op);
-                                else copy_part(far, s3 + u + 2, op - WL);
+                                if (op < WL) load_w_part((set + AHEAD) % SETS, step + AHEAD, op);
+                                else copy_part(far, s0 + u + NST - 1, op - WL);
                             }
                             __builtin_amdgcn_sched_barrier(0);
                             if constexpr (PAIR) {
@@ -404,8 +410,9 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
                     const uint32_t byte = fp4 ? mx_scale_byte<W4A8_MX_FP4>(top) : mx_scale_byte<W4A8_MX_FP8>(top);
                     const float up = byte == 255u ? 0.0f : mx_up(byte);
                     uint32_t c0, c1;
-                    if (fp4) c0 = mx_fp4x4(h0[0] * up, h0[1] * up, h0[2] * up, h0[3] * up), c1 = mx_fp4x4(h1[0] * up, h1[1] * up, h1[2] * up, h1[3] * up);
-                    else c0 = mx_fp8x4(h0[0] * up, h0[1] * up, h0[2] * up, h0[3] * up), c1 = mx_fp8x4(h1[0] * up, h1[1] * up, h1[2] * up, h1[3] * up);
+                    h0 *= up, h1 *= up;
+                    if (fp4) c0 = mx_fp4x4(h0[0], h0[1], h0[2], h0[3]), c1 = mx_fp4x4(h1[0], h1[1], h1[2], h1[3]);
+                    else c0 = mx_fp8x4(h0[0], h0[1], h0[2], h0[3]), c1 = mx_fp8x4(h1[0], h1[1], h1[2], h1[3]);
                     if (byte == 255u) c0 = 0u, c1 = 0u;
                     mx_swap16(c0, c1);                          // 8 neighbouring columns: tile q % 2, half q / 2
                     const unsigned at = unsigned(m * 16 + c16) * bpr + block, at8 = unsigned((q & 1) * 2 + (q >> 1));
@@ -473,19 +480,20 @@ __global__ __launch_bounds__(64 * WN, MT == 8 ? 2 : MT == 2 && !(PAIR && FMT != 
     }
 }
 
-template <int FMT, bool PAIR, int WN, int MT>
+template <int FMT, bool PAIR, int WN, int MT, bool DEEP>
 static void launch_tile_t(const MxArgs& a, int per_cu, hipStream_t s) {
     constexpr long long BM = 16 * MT, cols = PAIR ? 32 * WN : 64 * WN;
     const long long tiles = (a.rows / BM + std::min<long long>(a.E, a.rows)) * ((a.N + cols - 1) / cols);   // an upper bound
-    mx_tile_kernel<FMT, PAIR, WN, MT><<<dim3(unsigned(std::min<long long>(256 * per_cu, tiles))), dim3(64 * WN), 0, s>>>(a);
+    mx_tile_kernel<FMT, PAIR, WN, MT, DEEP><<<dim3(unsigned(std::min<long long>(256 * per_cu, tiles))), dim3(64 * WN), 0, s>>>(a);
 }
 
 template <int FMT, bool PAIR>
 static void launch_tile_v(const MxArgs& a, MxTile v, hipStream_t s) {
-    if (v == MX_TILE_WIDE) launch_tile_t<FMT, PAIR, 8, 8>(a, 1, s);
-    else if (v == MX_TILE_128) launch_tile_t<FMT, PAIR, 4, 8>(a, 2, s);
-    else if (v == MX_TILE_64) launch_tile_t<FMT, PAIR, 4, 4>(a, 3, s);
-    else launch_tile_t<FMT, PAIR, 4, 2>(a, 4, s);
+    if (v == MX_TILE_WIDE) launch_tile_t<FMT, PAIR, 8, 8, false>(a, 1, s);
+    else if (v == MX_TILE_128) launch_tile_t<FMT, PAIR, 4, 8, false>(a, 2, s);
+    else if (v == MX_TILE_64) launch_tile_t<FMT, PAIR, 4, 4, true>(a, 2, s);
+    else if (v == MX_TILE_32) launch_tile_t<FMT, PAIR, 4, 2, false>(a, 4, s);
+    else launch_tile_t<FMT, PAIR, 2, 2, true>(a, 4, s);
 }
 
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s) {

@@ -8,14 +8,15 @@ import moe_token_int8_amd as L
 from mx_cases import DEV, FP4, FP8, half_step, quant_bound, silu_bound, sum_bound
 
 SENTINEL = 7.0
-FEW, SOME, MANY, MORE = [9, 0, 1, 16, 0, 5, 9], [300, 0, 1, 17, 254, 0, 128], [0, 900, 31, 513, 1, 0, 55], [1300, 0, 129, 1100, 2, 0, 69]
+FEW, SOME, MANY = [9, 0, 1, 16, 0, 5, 9], [300, 0, 1, 17, 254, 0, 128], [0, 900, 31, 513, 1, 0, 55]
+LARGE = [2100, 0, 129, 1800, 2, 0, 78]
 # (rows of each expert, K, N): one size for each kernel at least, ragged in all three
 SIZES = {
-    "dense": [([5], 300, 523), ([1031], 400, 2575), ([2053], 399, 2573), ([2053], 1099, 4109), ([2053], 2100, 8207)],
-    "moe": [(FEW, 300, 523), (SOME, 400, 2575), (MANY, 399, 2573), (MANY, 2100, 4109), (MORE, 2099, 8205)],
-    "silu": [(FEW, 300, 528), (SOME, 400, 1552), (SOME, 1100, 4112), (MANY, 1099, 2576), (MORE, 1100, 4112)],
-    "quantized": [(FEW, 300, 528), (SOME, 400, 1552), (SOME, 1100, 4112), (MANY, 1099, 2576), (MORE, 1100, 4112)],
+    "dense": [([5], 300, 523), ([200], 1099, 4109), ([400], 1099, 4109), ([2053], 1099, 2573), ([2053], 399, 4109), ([4109], 4199, 2571)],
+    "moe": [(FEW, 300, 523), (SOME, 1099, 1037), (SOME, 400, 2575), (MANY, 1100, 4109), (MANY, 399, 8205), (LARGE, 4199, 2571)],
+    "silu": [(FEW, 300, 528), (SOME, 1100, 528), (SOME, 400, 2576), (SOME, 1100, 4112), (MANY, 1099, 4112), (LARGE, 4199, 4112)],
 }
+SIZES["quantized"] = SIZES["silu"]
 
 
 @pytest.fixture(scope="module", autouse=True)
