@@ -22,8 +22,10 @@ namespace w4a8 {
 // columns, then the 2 matching ones of up columns) over all of K.  The waves share the steps of 128 k: wave w takes w, w + 8, ...;
 // weights and activations go from memory to registers in the layout of the MFMA operands (a step of a weight tile is one
 // contiguous KiB), with no LDS and no barrier in the loop, two of a wave's steps in flight.  The 8 partial sums are added in wave
-// order through LDS, so a call repeats bit for bit.  (Two row tiles a workgroup read the weights once for 32 rows, but the tile
-// kernel does that faster: 32 rows for each of 64 experts, 1408 x 4096 fp4 73 against 51 us.)
+// order through LDS, so a call repeats bit for bit.  8 x 4096 x 14336 in fp8: 8.3 us (31 MB: 5 at the rate of a large read); one token's
+// 6 experts, 4096 x 1408 gate/up: 11.9 (37 MB: 6), of which the loads of activations take 1.4 us and 1.2 the half of the steps.
+// (Two row tiles a workgroup read the weights once for 32 rows, but the tile kernel does that faster: 32 rows for each of 64
+// experts, 1408 x 4096 fp4 73 against 51 us.  Three steps in flight: 9.7 in place of 8.4.)
 constexpr int MXS_WAVES = 8, MXS_ROWS = 16, MXS_TILES = 4;
 
 // The slot-th row tile over the experts, in their order; every wave finds it alone.  expert is -1 past the last one.
@@ -215,7 +217,8 @@ static void launch_stream(const MxArgs& a, hipStream_t s) {
 // unit (c > 1: a launch that fits does not spread evenly).  Streaming tiles, two of which share a unit, take o and l a step.  Of MFMA
 // tiles `per` share one, a step takes l, or thr for each of them.  Either reads the weights at bw TB/s, which adds up with the steps as
 // far as a norm of third powers says.  Fitted to 414 shapes (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 .. 1024 rows, evenly or
-// skewed, K 300 .. 14336), of which the choice loses 2 % in the mean against the best of all, 27 % at worst.  Measured, us, streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x 256 and 128 x 512, fp8:
+// skewed, K 300 .. 14336), of which the choice loses 2 % in the mean against the best of all, 27 % at worst.  Measured, us, fp8,
+// streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x 256 and 128 x 512:
 //   16 x 4096 x 14336                      9 /  13,  19,  18,  26,  38       128 x 4096 x 14336            36 /  21,  22,  21,  29,  42
 //   256 x 14336 x 4096                     - /  41,  56,  54,  80, 120       2048 x 14336 x 4096            - / 146, 133,  96, 129, 122
 //   2048 x 4096 x 14336                    - / 151, 145, 111,  97,  92

@@ -14,7 +14,8 @@
 namespace w4a8 {
 
 // Rows -> codes and scales.  A lane takes 8 neighbours along K (16 or 32 bytes in, 4 or 8 out), 4 lanes a block, a wave 512
-// of a row; the block's maximum is two quad permutes.  Bound by the copy: 2 bytes in and 17/32 or 33/32 out an element.
+// of a row; the block's maximum is two quad permutes.  Bound by the copy: 2 bytes in and 17/32 or 33/32 out an element (8192 x
+// 7168 bfloat16 -> fp4: 31 us, 4.8 TB/s).
 template <int DT, int FMT>
 __device__ __forceinline__ void quant_chunk(const uint8_t* X, const long long M, const int K, const long long ldx, const int chunks,
                                             uint8_t* Xq, uint8_t* sx, const long long w, const int lane) {

@@ -20,13 +20,13 @@ namespace w4a8 {
 // 4096 in fp8, tiles of 64 x 256: 129 -> 96 us; 192 x 14336 x 4096, tiles of 32 x 256 two ahead 56, of 32 x 128 five ahead 34.
 //
 // What bounds it: the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
-// cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 104 us (4.6 PFLOP/s; MFMAs alone on
+// cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 102 us (4.7 PFLOP/s; MFMAs alone on
 // registers reach 6.2), 83 without the memory operations in the loop, 99 without the copies, 94 without the weights, unchanged with
 // half the LDS reads.  256 x 256 tiles, where two waves load the same weights, took 108; touching the weights' lines 8 steps ahead,
 // one load of 64 lines, 115 to 130 (64 cycles of the same path); another order of steps for workgroups that share data, no change.
 //
-// vmcnt counts in the order of issue, so what is issued when is fixed: a step requests the weights of the step after the next;
-// the first step of a stage then requests the activations of the stage after the next.  One barrier a stage, before the last
+// vmcnt counts in the order of issue, so what is issued when is fixed: a step requests the weights of the step AHEAD steps on; the
+// first step of a stage then requests the activations of the stage NST - 1 stages on.  One barrier a stage, before the last
 // group of MFMAs, when the stage's last operands are in registers: behind it the next stage is whole and this one is free.
 constexpr int MXT_ROW = 128;                                    // bytes of a row in a stage
 constexpr int MXT_MAX_E = 1024;
@@ -105,7 +105,7 @@ void mx_tile_kernel(MxArgs a) {
     __shared__ __align__(1024) uint8_t stage5[NST > 3 ? STAGE : 16];
     __shared__ int4 list[LIST];                                 // tiles of this workgroup: expert, first row, rows, column block
     __shared__ int first[MXT_MAX_E + 1];                        // row tiles before expert e
-    __shared__ int entries[BM];                                 // gather entries of the next tile's rows
+    __shared__ int entries[(BM + 63) / 64 * 64];                // gather entries of the next tile's rows: a whole wave's copy at a time
     __shared__ int wsum[WN];
     const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int q = lane >> 4, c16 = lane & 15, wn = wave;
