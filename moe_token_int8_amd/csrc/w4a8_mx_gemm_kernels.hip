@@ -363,7 +363,7 @@ static MxArgs mx_args(const void* Xq, const uint8_t* sx, int fmt, const int32_t*
 // exact: float32 sums of fp8 products that drop nothing.
 static int run_mx(const char* call, MxArgs& a, int fmt, bool pair, bool exact, int K, hipStream_t s) {
     const char* names = fmt == W4A8_MX_FP4 ? (pair ? launch_mx<W4A8_MX_FP4, true>(a, s) : launch_mx<W4A8_MX_FP4, false>(a, s))
-                        : exact            ? launch_mx<MX_FP8_EXACT, false>(a, s)
+                        : exact            ? (pair ? launch_mx<MX_FP8_EXACT, true>(a, s) : launch_mx<MX_FP8_EXACT, false>(a, s))
                                            : (pair ? launch_mx<W4A8_MX_FP8, true>(a, s) : launch_mx<W4A8_MX_FP8, false>(a, s));
     if (log_on())
         std::fprintf(stderr, "w4a8: %s E=%d rows=%d K=%d N=%d %s -> %s\n", call, a.E, a.rows, K, a.N,
@@ -447,7 +447,13 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
     if (!offsets || !Hq || !sh || !aligned_to(Hq, 16) || !aligned_to(sh, 4)) return W4A8_EINVAL;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, 2 * I);
     a.N = I, a.Hq = static_cast<uint8_t*>(Hq), a.sh = sh, a.h_fmt = h_fmt;
-    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, fmt, true, false, K, static_cast<hipStream_t>(stream));
+    // A code of h that lies within the sums' error of a tie goes the other way, a step of up to 1/8 (E4M3): with fp8 products that drop
+    // their small parts this is 100 times as likely as with exact ones, and in a small layer one such code is seen (76 tokens, I 64: error
+    // against float64 4.1e-3 in place of 1.7e-3, the rounding of the output).  Exact products take twice the MFMAs: free where
+    // the read of the weights or the launch bounds the call, 122 us in place of 85 for 512 tokens x 6 of 64 experts, 4096 x 1408,
+    // whose error is 2.0e-3 without.
+    const bool exact = rows <= 32ll * E || double(rows) * (2.0 * I) * K <= 8.6e9;
+    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, fmt, true, exact, K, static_cast<hipStream_t>(stream));
 }
 
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt) {

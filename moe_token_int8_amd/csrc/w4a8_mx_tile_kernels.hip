@@ -498,7 +498,7 @@ static void launch_tile_v(const MxArgs& a, MxTile v, hipStream_t s) {
 
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s) {
     if (fmt == W4A8_MX_FP4) pair ? launch_tile_v<W4A8_MX_FP4, true>(a, v, s) : launch_tile_v<W4A8_MX_FP4, false>(a, v, s);
-    else if (fmt == MX_FP8_EXACT) launch_tile_v<MX_FP8_EXACT, false>(a, v, s);
+    else if (fmt == MX_FP8_EXACT) pair ? launch_tile_v<MX_FP8_EXACT, true>(a, v, s) : launch_tile_v<MX_FP8_EXACT, false>(a, v, s);
     else pair ? launch_tile_v<W4A8_MX_FP8, true>(a, v, s) : launch_tile_v<W4A8_MX_FP8, false>(a, v, s);
 }
 

@@ -120,6 +120,27 @@ def test_silu(counts, K, I, fmt, gathered):
         assert (q.view(p.rows, Ip // 32, -1)[:, -(-I // 32):] == 0).all() and (s[:, -(-I // 32):] == 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,I", [(5, 16), (300, 2064), (700, 528)])
+def test_small_parts_of_products_reach_quantized_h(rows, I):
+    """x = 448, -448, 2^-6: gate 448 (silu is itself), up 448 - 448 + 2^-6, 14 bits below the largest product: h = 7."""
+    x = torch.zeros(rows, 32, device=DEV)
+    x[:, 0], x[:, 1], x[:, 2] = 448.0, -448.0, 2.0 ** -6
+    q, s = L.mx_empty(FP8, rows, 32, DEV)
+    L.w4a8_mx_quant(x, FP8, q, s)
+    w = torch.zeros(2 * I, 32, device=DEV)
+    w[:I, 0], w[I:, :3] = 1.0, 1.0
+    W = torch.empty(L.w4a8_mx_packed_size(32, 2 * I), dtype=torch.uint8, device=DEV)
+    # E2M1 blocks scale their largest value, 1, to 4: the products are the same
+    L.w4a8_mx_pack(w, W)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    hq, hs = L.mx_empty(FP8, rows, I, DEV)
+    L.w4a8_moe_gemm_silu_mx_quant(q, s, FP8, None, 1, off, 1, W, W.numel(), 32, I, FP8, hq, hs)
+    h = torch.empty(rows, I, device=DEV)
+    L.w4a8_mx_dequant(hq, hs, FP8, h)
+    assert (h == 7).all()
+
+
 # ------------------------------------------------------------------------------------------- calls that repeat or meet others
 def launches(p, N):
     """The products of p as closures over their outputs."""
