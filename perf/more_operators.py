@@ -264,8 +264,8 @@ def prepare(case, seed):
     if c["op"] == "layer":
         s |= {"ids": ids, "w": w, "order": order, "X": _rows(g, T, K, "bf16"), "Wd": _experts(g, E, K, N),
               "Y": torch.empty(T, K, dtype=torch.bfloat16, device=DEV)}
-        # the workspace that a serving program keeps: both activations' codes, the routing and the experts' float32 outputs
-        s["ws"] = torch.empty(2 * T * _up(K, 128) + rows * (2 * _up(N, 128) + 4 * _up(K, 4) + 8) + 4 * E + 65536, dtype=torch.uint8, device=DEV)
+        # the workspace that a serving program keeps: both activations' codes, the routing and the experts' outputs
+        s["ws"] = torch.empty(2 * T * _up(K, 128) + rows * (2 * _up(N, 128) + 2 * K + 8) + 4 * E + 65536, dtype=torch.uint8, device=DEV)
         return s
     s["gather"] = order if c["gather"] else None
     s["Xq"], s["sx"] = _store(*_encode(_rows(g, T if c["gather"] else rows, K, "f32"), c["fmt"]), c["fmt"])
