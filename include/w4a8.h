@@ -665,7 +665,7 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
                                 const int32_t* expert_offsets, int E, int rows, int src_rows, const void* blobs,
                                 size_t expert_stride, int K, int I, int h_fmt, void* Hq, uint8_t* sh, void* stream);
 
-/* Workspace bytes needed by w4a8_moe_forward_mx (0 if invalid). */
+/* Workspace bytes with which w4a8_moe_forward_mx makes all columns at once (0 if invalid). */
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt);
 
 /* One MoE expert layer on MXFP4 experts with activations in fmt: w4a8_mx_quant(X) -> w4a8_moe_align ->
@@ -673,7 +673,9 @@ size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt);
  * in float32 and rounded once.
  *   X_bf16     device bfloat16 [T, H]; topk_ids / topk_w device [T, k] (ids outside [0, E) add nothing)
  *   gu_blobs   E packed [2I, H], gate channels first; d_blobs E packed [H, I]; strides in bytes
- *   workspace  device, >= w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt) bytes, 256-aligned
+ *   workspace  device, 256-aligned, w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt) bytes, or less: the last of it, 4 T k H, are
+ *              the experts' outputs, and where only a part of their columns fits, 64 at least (ESIZE), the down product
+ *              and the sum are made by slices of columns, at two launches a slice, with the same bits
  *   out_bf16   device bfloat16 [T, H]
  * I % 16 == 0 (EINVAL); T*k <= 2^24 and T ceil(H / 1024) < 2^24 (EUNSUPPORTED).  Every check of the chained
  * steps runs before the first launch. */

@@ -900,7 +900,7 @@ def w4a8_moe_mx_workspace_size(T: int, k: int, H: int, I: int, E: int, fmt: int)
 def w4a8_moe_forward_mx(X, topk_ids, topk_w, E: int, fmt: int, gu_blobs, gu_stride: int, d_blobs, d_stride: int, I: int, workspace,
                         out, stream=None) -> None:
     """One MoE layer on MXFP4 experts: gu_blobs E packed [2I, H], d_blobs E packed [H, I]; workspace of
-    w4a8_moe_mx_workspace_size bytes."""
+    w4a8_moe_mx_workspace_size bytes, or less (the experts' outputs are then made by slices of columns)."""
     t = _torch_of_calls or _torch()
     dev = X.get_device()
     (T, H), (rows, k) = X.shape, topk_ids.shape

@@ -225,7 +225,7 @@ static void launch_stream(const MxArgs& a, hipStream_t s) {
 //   4 rows for each of 256, 2048 x 7168  401 / 321, 328, 331, 351, 348       64 rows for each, the same     - / 620, 566, 477, 474, 457
 enum MxKernel { MXK_STREAM, MXK_SMALL, MXK_TILE32, MXK_TILE64, MXK_TILE128, MXK_WIDE, MXK_KERNELS };
 
-static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
+static MxKernel choose_mx(const MxArgs& a, int N, bool fp4, bool pair, MxKernel first) {
     struct Rate {
         int rows, cols, per;
         double o, l, thr, bw, c;
@@ -236,12 +236,12 @@ static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
                                                {{16, 64, 2, 1.55, 0.108, 0.000, 7.80, 2.00}, {32, 128, 4, 0.00, 0.196, 0.171, 5.43, 1.46},
                                                 {32, 256, 4, 0.00, 0.275, 0.301, 5.69, 1.33}, {64, 256, 2, 1.81, 0.106, 0.301, 5.40, 1.71},
                                                 {128, 256, 2, 3.40, 0.195, 0.446, 6.00, 1.73}, {128, 512, 1, 5.24, 0.351, 0.803, 6.04, 2.00}}};
-    const double rows = a.rows, E = a.E, width = pair ? 2.0 * a.N : a.N, steps = a.K1;
+    const double rows = a.rows, E = a.E, width = pair ? 2.0 * N : N, steps = a.K1;
     const double active = E > 1 ? std::min(rows, E * (1 - std::exp(-rows / E))) : 1;
     const double bytes = active * width * steps * 68;           // 128 k of a column
-    MxKernel best = MXK_STREAM;
+    MxKernel best = first;
     double least = 1e300;
-    for (int v = 0; v < MXK_KERNELS; ++v) {
+    for (int v = first; v < MXK_KERNELS; ++v) {
         const Rate& r = rates[fp4][v];
         const double rt = E > 1 ? std::max(active, rows / r.rows + 0.5 * active) : std::ceil(rows / r.rows);
         const double n = rt * std::ceil(width / r.cols);
@@ -260,11 +260,15 @@ static MxKernel choose_mx(const MxArgs& a, bool fp4, bool pair) {
     return best;
 }
 
+// N: columns of the whole product, of which a.N may be a slice.  A slice streams where the whole would, since that sums in another order
+// than tiles do (all of which sum alike): its bits are those of the whole.
 template <int FMT, bool PAIR>
-static const char* launch_mx(const MxArgs& a, hipStream_t s) {
+static const char* launch_mx(const MxArgs& a, int N, hipStream_t s) {
     // the tile kernel reaches activation rows through 32-bit offsets from X (gathered) or from its tile's first row
-    const bool near = !a.gather || (long long)a.src_rows * a.rowb < 0xe0000000ll;
-    switch (near ? choose_mx(a, FMT == W4A8_MX_FP4, PAIR) : MXK_STREAM) {
+    const bool near = !a.gather || (long long)a.src_rows * a.rowb < 0xe0000000ll, fp4 = FMT == W4A8_MX_FP4;
+    MxKernel kernel = near ? choose_mx(a, N, fp4, PAIR, MXK_STREAM) : MXK_STREAM;
+    if (kernel != MXK_STREAM && a.N != N) kernel = choose_mx(a, a.N, fp4, PAIR, MXK_SMALL);
+    switch (kernel) {
         case MXK_SMALL: launch_mx_tile(a, FMT, PAIR, MX_TILE_SMALL, s); return "mx_tile_kernel (32 x 128)";
         case MXK_TILE32: launch_mx_tile(a, FMT, PAIR, MX_TILE_32, s); return "mx_tile_kernel (32 x 256)";
         case MXK_TILE64: launch_mx_tile(a, FMT, PAIR, MX_TILE_64, s); return "mx_tile_kernel (64 x 256)";
@@ -276,11 +280,11 @@ static const char* launch_mx(const MxArgs& a, hipStream_t s) {
 
 // out[t] = sum_j w[t, j] Yd[inv[t, j]] in float32, j ascending, rounded once: the experts' outputs stay in float32 (rounded to
 // bfloat16 in between, a layer's error against float64 is 2.5e-3 normwise in place of 1.7e-3, that of the one rounding).
-// 4 columns a thread; the rows of 8 experts are requested together.
-__global__ __launch_bounds__(256) void mx_combine_kernel(const float* Yd, unsigned ldy, const int32_t* inv, const float* w, int k, int H,
-                                                         int chunks, uint16_t* out) {
+// 4 columns a thread; the rows of 8 experts are requested together.  N columns (a slice of out, whose rows have ldo).
+__global__ __launch_bounds__(256) void mx_combine_kernel(const float* Yd, unsigned ldy, const int32_t* inv, const float* w, int k, int N,
+                                                         int chunks, uint16_t* out, unsigned ldo) {
     const int t = int(blockIdx.x / unsigned(chunks)), c = (int(blockIdx.x % unsigned(chunks)) * 256 + int(threadIdx.x)) * 4;
-    if (c >= H) return;
+    if (c >= N) return;
     v4f s{};
     for (int j0 = 0; j0 < k; j0 += 8) {
         int row[8];
@@ -301,11 +305,11 @@ __global__ __launch_bounds__(256) void mx_combine_kernel(const float* Yd, unsign
             }
     }
     typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-    uint16_t* p = out + size_t(t) * size_t(H) + c;
-    if (c + 4 <= H) {
+    uint16_t* p = out + size_t(t) * ldo + c;
+    if (c + 4 <= N) {
         *reinterpret_cast<u2*>(p) = u2{f32_to_bf16_pair(s[0], s[1]), f32_to_bf16_pair(s[2], s[3])};
     } else {
-        for (int i = 0; i < H - c; ++i) p[i] = uint16_t(f32_to_bf16_rne(s[i]));
+        for (int i = 0; i < N - c; ++i) p[i] = uint16_t(f32_to_bf16_rne(s[i]));
     }
 }
 
@@ -360,11 +364,11 @@ static MxArgs mx_args(const void* Xq, const uint8_t* sx, int fmt, const int32_t*
     return a;
 }
 
-// exact: float32 sums of fp8 products that drop nothing.
-static int run_mx(const char* call, MxArgs& a, int fmt, bool pair, bool exact, int K, hipStream_t s) {
-    const char* names = fmt == W4A8_MX_FP4 ? (pair ? launch_mx<W4A8_MX_FP4, true>(a, s) : launch_mx<W4A8_MX_FP4, false>(a, s))
-                        : exact            ? (pair ? launch_mx<MX_FP8_EXACT, true>(a, s) : launch_mx<MX_FP8_EXACT, false>(a, s))
-                                           : (pair ? launch_mx<W4A8_MX_FP8, true>(a, s) : launch_mx<W4A8_MX_FP8, false>(a, s));
+// N: columns of the whole product (a.N: of this launch).  exact: float32 sums of fp8 products that drop nothing.
+static int run_mx(const char* call, MxArgs& a, int N, int fmt, bool pair, bool exact, int K, hipStream_t s) {
+    const char* names = fmt == W4A8_MX_FP4 ? (pair ? launch_mx<W4A8_MX_FP4, true>(a, N, s) : launch_mx<W4A8_MX_FP4, false>(a, N, s))
+                        : exact            ? (pair ? launch_mx<MX_FP8_EXACT, true>(a, N, s) : launch_mx<MX_FP8_EXACT, false>(a, N, s))
+                                           : (pair ? launch_mx<W4A8_MX_FP8, true>(a, N, s) : launch_mx<W4A8_MX_FP8, false>(a, N, s));
     if (log_on())
         std::fprintf(stderr, "w4a8: %s E=%d rows=%d K=%d N=%d %s -> %s\n", call, a.E, a.rows, K, a.N,
                      fmt == W4A8_MX_FP4 ? "mxfp4" : "mxfp8", names);
@@ -379,21 +383,34 @@ constexpr int MX_ROUTE_ROWS = 2048;
 
 struct MxLayerWs {
     size_t xq, sx, rows, offs, inv, hq, sh, yd, total;
+    int slice;                // columns of the experts' outputs that yd holds at a time
 };
-static MxLayerWs mx_layer_ws(int T, int k, int H, int I, int E, int fmt) {
+
+// The experts' float32 outputs come last and take what `bytes` leaves: all H columns where they fit, else equal slices of whole groups
+// of 64, whose down products and sums follow each other (slice 0: no room for 64).  The launches of a second slice cost 8 to 14 us (H
+// 4096, I 1408, 64 experts, k 6, fp4: 4 tokens 49 -> 57, 33 tokens 109 -> 124, 512 tokens 167 -> 176, skewed 161 -> 189), and prompts
+// nothing; more slices gain nothing there either (8192 tokens: whole 1042, two slices 1050, four 1024, eight 1036).
+static MxLayerWs mx_layer_ws(int T, int k, int H, int I, int E, int fmt, size_t bytes) {
     const size_t R = size_t(T) * size_t(k);
     MxLayerWs w;
     size_t o = 0;
-    auto piece = [&](size_t bytes) {
+    auto piece = [&](size_t size) {
         const size_t at = o;
-        o = (o + bytes + 255) & ~size_t(255);
+        o = (o + size + 255) & ~size_t(255);
         return at;
     };
     w.xq = piece(size_t(T) * mx_row_bytes(fmt, H)), w.sx = piece(size_t(T) * size_t(mx_kp(H) / 32));
     w.rows = piece(R * 4), w.offs = piece(size_t(E + 1) * 4), w.inv = piece(R * 4);
     w.hq = piece(R * mx_row_bytes(fmt, I)), w.sh = piece(R * size_t(mx_kp(I) / 32));
+    const size_t before = o;
     w.yd = piece(R * size_t((H + 3) & ~3) * 4);                 // float32, rows at whole 16 bytes
     w.total = o;
+    w.slice = H;
+    if (bytes < w.total) {
+        const size_t fit = bytes < before || R == 0 ? 0 : (bytes - before) / (R * 4) / 64 * 64;
+        const size_t slices = fit ? (size_t(H) + fit - 1) / fit : 0;
+        w.slice = slices ? int((size_t(H) + slices - 1) / slices + 63) / 64 * 64 : 0;
+    }
     return w;
 }
 
@@ -410,7 +427,7 @@ int w4a8_mx_gemm(const void* Xq, const uint8_t* sx, int fmt, int M, const void* 
     if ((st = check_out(Y, ldy, N, out_dtype, true))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, nullptr, 1, nullptr, 1, M, M, blob, 0, K, N);
     a.N = N, a.Y = Y, a.ldy = size_t(ldy), a.out = out_dtype;
-    return run_mx("w4a8_mx_gemm", a, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_mx_gemm", a, N, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E, int rows,
@@ -421,7 +438,7 @@ int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* 
     if ((st = check_out(Y, ldy, N, out_dtype, true))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, N);
     a.N = N, a.Y = Y, a.ldy = size_t(ldy), a.out = out_dtype;
-    return run_mx("w4a8_moe_gemm_mx", a, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_mx", a, N, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_silu_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E,
@@ -434,7 +451,7 @@ int w4a8_moe_gemm_silu_mx(const void* Xq, const uint8_t* sx, int fmt, const int3
     if ((st = check_out(H, ldh, I, out_dtype, false))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, 2 * I);
     a.N = I, a.Y = H, a.ldy = size_t(ldh), a.out = out_dtype;
-    return run_mx("w4a8_moe_gemm_silu_mx", a, fmt, true, false, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_silu_mx", a, I, fmt, true, false, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E,
@@ -453,14 +470,14 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
     // the read of the weights or the launch bounds the call, 122 us in place of 85 for 512 tokens x 6 of 64 experts, 4096 x 1408,
     // whose error is 2.0e-3 without.
     const bool exact = rows <= 32ll * E || double(rows) * (2.0 * I) * K <= 8.6e9;
-    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, fmt, true, exact, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, I, fmt, true, exact, K, static_cast<hipStream_t>(stream));
 }
 
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt) {
     if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0 || H > MX_MAX_K || I > MX_MAX_N / 2 || (long long)T * k > MX_MAX_ROWS ||
         (fmt != W4A8_MX_FP4 && fmt != W4A8_MX_FP8))
         return 0;
-    return mx_layer_ws(T, k, H, I, E, fmt).total;
+    return mx_layer_ws(T, k, H, I, E, fmt, ~size_t(0)).total;
 }
 
 int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T, int k, int E, int fmt, const void* gu, size_t gu_stride,
@@ -473,10 +490,9 @@ int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T
     if (T == 0) return W4A8_OK;
     if (!X || !ids || !w || !ws || !out || !aligned_to(X, 2) || !aligned_to(out, 2) || !aligned_to(ids, 4) || !aligned_to(w, 4))
         return W4A8_EINVAL;
-    const int chunks = (H + 1023) / 1024, ldy = (H + 3) & ~3;
-    if ((long long)T * chunks >= (1ll << 24)) return W4A8_EUNSUPPORTED;     // less than 2^32 work-items
-    const MxLayerWs L = mx_layer_ws(T, k, H, I, E, fmt);
-    if (ws_bytes < L.total) return W4A8_ESIZE;
+    if ((long long)T * ((H + 1023) / 1024) >= (1ll << 24)) return W4A8_EUNSUPPORTED;    // less than 2^32 work-items
+    const MxLayerWs L = mx_layer_ws(T, k, H, I, E, fmt, ws_bytes);
+    if (L.slice == 0) return W4A8_ESIZE;
     if (!aligned_to(ws, 256)) return W4A8_EINVAL;
     uint8_t* b = static_cast<uint8_t*>(ws);
     uint8_t *xq = b + L.xq, *sx = b + L.sx, *hq = b + L.hq, *sh = b + L.sh;
@@ -495,12 +511,20 @@ int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T
     }
     if ((st = w4a8_moe_gemm_silu_mx_quant(xq, sx, fmt, rows, k, offs, E, R, T, gu, gu_stride, H, I, fmt, hq, sh, stream))) return st;
     // the output is bfloat16: the expert's float32 sums need not be the exact ones
-    MxArgs a = mx_args(hq, sh, fmt, nullptr, k, offs, E, R, R, dn, d_stride, I, H);
-    a.N = H, a.Y = b + L.yd, a.ldy = size_t(ldy), a.out = W4A8_F32;
-    if ((st = run_mx("w4a8_moe_forward_mx (down)", a, fmt, false, false, I, static_cast<hipStream_t>(stream)))) return st;
-    mx_combine_kernel<<<dim3(unsigned(T * chunks)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(
-        reinterpret_cast<const float*>(b + L.yd), unsigned(ldy), inv, w, k, H, chunks, static_cast<uint16_t*>(out));
-    return launched();
+    const int slice = L.slice, ldy = (slice + 3) & ~3;
+    const MxArgs whole = mx_args(hq, sh, fmt, nullptr, k, offs, E, R, R, dn, d_stride, I, H);
+    for (int c = 0; c < H; c += slice) {
+        MxArgs a = whole;
+        a.N = std::min(slice, H - c), a.Y = b + L.yd, a.ldy = size_t(ldy), a.out = W4A8_F32;
+        a.W += size_t(c / 16) * size_t(a.K1) * 1024;            // codes by 16 columns, scales by 64
+        a.scales_off = whole.scales_off - size_t(c / 16) * size_t(a.K1) * 1024 + size_t(c / 64) * size_t(a.K1) * 256;
+        if ((st = run_mx("w4a8_moe_forward_mx (down)", a, H, fmt, false, false, I, static_cast<hipStream_t>(stream)))) return st;
+        const int chunks = (a.N + 1023) / 1024;
+        mx_combine_kernel<<<dim3(unsigned(T * chunks)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(
+            reinterpret_cast<const float*>(b + L.yd), unsigned(ldy), inv, w, k, a.N, chunks, static_cast<uint16_t*>(out) + c, unsigned(H));
+        if ((st = launched())) return st;
+    }
+    return W4A8_OK;
 }
 
 }  // extern "C"
