@@ -77,13 +77,6 @@ __device__ __forceinline__ int mx_src(const MxArgs& a, int r) {
     return mx_token(a, a.gather[r]);
 }
 
-// Activation operands of the kernels: fp4, fp8, and fp8 for float32 outputs (MX_FP8_EXACT).  Within 8 neighbouring k the MFMA
-// aligns the products of fp8 to the largest one and drops what lies 2^-13 and more below its power of two (measured: 2688
-// + 2^-3 is exact, 2^-4 is lost; 8 places further along K it is not).  On normal values that is 5e-6 normwise, 2e-5 with outliers:
-// nothing in 16 bits, but more than float32 should lose.  There each operand is multiplied in two parts, its elements of 2 and more
-// and the smaller ones: the products of a part then span no more than 14 bits, and nothing is dropped.
-enum { MX_FP8_EXACT = 2 };
-
 // Operand of one step of 128 k: 16 bytes of fp4 (a lane's block of 32), or two pieces of 16 fp8 values (k = 16 q and k = 64 + 16 q
 // of the step, where q = lane / 16).
 template <int FMT>
@@ -91,19 +84,25 @@ struct MxOperand {
     v4i p[FMT == W4A8_MX_FP4 ? 1 : 2];
 };
 
+// Within 8 neighbouring k the MFMA aligns the products of fp8 to the largest one and drops what lies 14 bits and more below its
+// operands' exponents (measured: 2688 + 2^-3 is exact, 2^-4 is lost; 8 places further along K it is not), 5e-6 of a sum of normal
+// values and 2e-5 with outliers: less than a 16-bit output rounds, but not a sum in 32 bits, and seen where an element of h lies near
+// a tie of its code (a layer's error against float64 2.0e-3 in place of 1.7e-3).  So an operand is multiplied in two parts, its elements
+// of 2 and more and the smaller ones: the products of a part span no more than 14 bits, and nothing is dropped.
+
 // The elements of magnitude 2 and more (bit 6 of their byte, the high bit of the exponent, is set); the others are zero.
 __device__ __forceinline__ v4i mx_large(const v4i x) {
     v4i r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t b = uint32_t(x[i]) & 0x40404040u;
-        r[i] = int(uint32_t(x[i]) & ((b << 2) - (b >> 6)));     // 255 times the bit, in every byte
+        // a byte of the permutation is 0 or 255 by the sign of byte 1 or 3 of either operand (selectors 8 to 11)
+        r[i] = x[i] & int(__builtin_amdgcn_perm(uint32_t(x[i]) << 1, uint32_t(x[i]) << 9, 0x0b090a08u));
     }
     return r;
 }
 
 // One step of a 16 x 16 tile: v_mfma_scale_f32_16x16x128_f8f6f4 multiplies blocks of 32 k with their scales and sums in float32
-// (fp4: exact where float32 holds the sum, else within 2^-23 of the sum of magnitudes).  The weights are the first operand, so
+// (exact where float32 holds the sum, else within 2^-23 of the sum of magnitudes).  The weights are the first operand, so
 // a lane's four sums are the columns 4 (lane / 16) .. + 3 of activation row lane % 16.  A lane's scale is that of block lane / 16:
 // byte WB of sw, byte 0 of sx.
 template <int FMT, int WB>
@@ -113,14 +112,10 @@ __device__ __forceinline__ v4f mx_mfma(const v4i w, const MxOperand<FMT>& x, v4f
         const v8i b = __builtin_shufflevector(x.p[0], x.p[0], 0, 1, 2, 3, -1, -1, -1, -1);
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, WB, int(sw), 0, int(sx));
     } else {
-        v4i p0 = x.p[0], p1 = x.p[1];
-        if constexpr (FMT == MX_FP8_EXACT) {
-            const v4i l0 = mx_large(p0), l1 = mx_large(p1);
-            const v8i l = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, l, c, 4, 0, WB, int(sw), 0, int(sx));
-            p0 ^= l0, p1 ^= l1;
-        }
-        const v8i b = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
+        const v4i l0 = mx_large(x.p[0]), l1 = mx_large(x.p[1]), s0 = x.p[0] ^ l0, s1 = x.p[1] ^ l1;
+        const v8i l = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, l, c, 4, 0, WB, int(sw), 0, int(sx));
+        const v8i b = __builtin_shufflevector(s0, s1, 0, 1, 2, 3, 4, 5, 6, 7);
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, WB, int(sw), 0, int(sx));
     }
 }

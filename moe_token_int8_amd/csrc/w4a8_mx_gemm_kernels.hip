@@ -154,11 +154,15 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb, in
                 acc[3] = mx_mfma<FMT, 3>(b.w[3], b.x, acc[3], b.sw[0], b.sx);
             }
         };
+        // (fp8: loads held back until the operands of the step before are free; moved ahead of them they spilled registers, 256 rows of 64
+        // experts, 4096 x 1408 gate/up, 86 us in place of 71)
         for (int s = wave; s < a.K1; s += 2 * MXS_WAVES) {
             multiply(s0);
+            if constexpr (FMT != W4A8_MX_FP4) __builtin_amdgcn_sched_barrier(0);
             load_w(s0, s + 2 * MXS_WAVES);
             load_x(s0, s + 2 * MXS_WAVES);
             multiply(s1);
+            if constexpr (FMT != W4A8_MX_FP4) __builtin_amdgcn_sched_barrier(0);
             load_w(s1, s + 3 * MXS_WAVES);
             load_x(s1, s + 3 * MXS_WAVES);
         }
@@ -364,10 +368,9 @@ static MxArgs mx_args(const void* Xq, const uint8_t* sx, int fmt, const int32_t*
     return a;
 }
 
-// N: columns of the whole product (a.N: of this launch).  exact: float32 sums of fp8 products that drop nothing.
-static int run_mx(const char* call, MxArgs& a, int N, int fmt, bool pair, bool exact, int K, hipStream_t s) {
+// N: columns of the whole product (a.N: of this launch).
+static int run_mx(const char* call, MxArgs& a, int N, int fmt, bool pair, int K, hipStream_t s) {
     const char* names = fmt == W4A8_MX_FP4 ? (pair ? launch_mx<W4A8_MX_FP4, true>(a, N, s) : launch_mx<W4A8_MX_FP4, false>(a, N, s))
-                        : exact            ? (pair ? launch_mx<MX_FP8_EXACT, true>(a, N, s) : launch_mx<MX_FP8_EXACT, false>(a, N, s))
                                            : (pair ? launch_mx<W4A8_MX_FP8, true>(a, N, s) : launch_mx<W4A8_MX_FP8, false>(a, N, s));
     if (log_on())
         std::fprintf(stderr, "w4a8: %s E=%d rows=%d K=%d N=%d %s -> %s\n", call, a.E, a.rows, K, a.N,
@@ -427,7 +430,7 @@ int w4a8_mx_gemm(const void* Xq, const uint8_t* sx, int fmt, int M, const void* 
     if ((st = check_out(Y, ldy, N, out_dtype, true))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, nullptr, 1, nullptr, 1, M, M, blob, 0, K, N);
     a.N = N, a.Y = Y, a.ldy = size_t(ldy), a.out = out_dtype;
-    return run_mx("w4a8_mx_gemm", a, N, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_mx_gemm", a, N, fmt, false, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E, int rows,
@@ -438,7 +441,7 @@ int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* 
     if ((st = check_out(Y, ldy, N, out_dtype, true))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, N);
     a.N = N, a.Y = Y, a.ldy = size_t(ldy), a.out = out_dtype;
-    return run_mx("w4a8_moe_gemm_mx", a, N, fmt, false, out_dtype == W4A8_F32, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_mx", a, N, fmt, false, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_silu_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E,
@@ -451,7 +454,7 @@ int w4a8_moe_gemm_silu_mx(const void* Xq, const uint8_t* sx, int fmt, const int3
     if ((st = check_out(H, ldh, I, out_dtype, false))) return st;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, 2 * I);
     a.N = I, a.Y = H, a.ldy = size_t(ldh), a.out = out_dtype;
-    return run_mx("w4a8_moe_gemm_silu_mx", a, I, fmt, true, false, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_silu_mx", a, I, fmt, true, K, static_cast<hipStream_t>(stream));
 }
 
 int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E,
@@ -464,13 +467,7 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
     if (!offsets || !Hq || !sh || !aligned_to(Hq, 16) || !aligned_to(sh, 4)) return W4A8_EINVAL;
     MxArgs a = mx_args(Xq, sx, fmt, gather, k, offsets, E, rows, src_rows, blobs, stride, K, 2 * I);
     a.N = I, a.Hq = static_cast<uint8_t*>(Hq), a.sh = sh, a.h_fmt = h_fmt;
-    // A code of h that lies within the sums' error of a tie goes the other way, a step of up to 1/8 (E4M3): with fp8 products that drop
-    // their small parts this is 100 times as likely as with exact ones, and in a small layer one such code is seen (76 tokens, I 64: error
-    // against float64 4.1e-3 in place of 1.7e-3, the rounding of the output).  Exact products take twice the MFMAs: free where
-    // the read of the weights or the launch bounds the call, 122 us in place of 85 for 512 tokens x 6 of 64 experts, 4096 x 1408,
-    // whose error is 2.0e-3 without.
-    const bool exact = rows <= 32ll * E || double(rows) * (2.0 * I) * K <= 8.6e9;
-    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, I, fmt, true, exact, K, static_cast<hipStream_t>(stream));
+    return run_mx("w4a8_moe_gemm_silu_mx_quant", a, I, fmt, true, K, static_cast<hipStream_t>(stream));
 }
 
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt) {
@@ -510,7 +507,6 @@ int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T
         if ((st = w4a8_moe_align(ids, T, k, E, rows, offs, inv, stream))) return st;
     }
     if ((st = w4a8_moe_gemm_silu_mx_quant(xq, sx, fmt, rows, k, offs, E, R, T, gu, gu_stride, H, I, fmt, hq, sh, stream))) return st;
-    // the output is bfloat16: the expert's float32 sums need not be the exact ones
     const int slice = L.slice, ldy = (slice + 3) & ~3;
     const MxArgs whole = mx_args(hq, sh, fmt, nullptr, k, offs, E, R, R, dn, d_stride, I, H);
     for (int c = 0; c < H; c += slice) {
@@ -518,7 +514,7 @@ int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T
         a.N = std::min(slice, H - c), a.Y = b + L.yd, a.ldy = size_t(ldy), a.out = W4A8_F32;
         a.W += size_t(c / 16) * size_t(a.K1) * 1024;            // codes by 16 columns, scales by 64
         a.scales_off = whole.scales_off - size_t(c / 16) * size_t(a.K1) * 1024 + size_t(c / 64) * size_t(a.K1) * 256;
-        if ((st = run_mx("w4a8_moe_forward_mx (down)", a, H, fmt, false, false, I, static_cast<hipStream_t>(stream)))) return st;
+        if ((st = run_mx("w4a8_moe_forward_mx (down)", a, H, fmt, false, I, static_cast<hipStream_t>(stream)))) return st;
         const int chunks = (a.N + 1023) / 1024;
         mx_combine_kernel<<<dim3(unsigned(T * chunks)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(
             reinterpret_cast<const float*>(b + L.yd), unsigned(ldy), inv, w, k, a.N, chunks, static_cast<uint16_t*>(out) + c, unsigned(H));

@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t mx_max_rows(uint32_t m) {
 }
 
 template <int FMT, bool PAIR, int WN, int MT, bool DEEP>
-__global__ __launch_bounds__(64 * WN, MT == 8 || DEEP ? 2 : (PAIR && FMT != W4A8_MX_FP4) || FMT == MX_FP8_EXACT ? 3 : 4)
+__global__ __launch_bounds__(64 * WN, MT == 8 || DEEP ? 2 : FMT != W4A8_MX_FP4 ? 3 : 4)
 void mx_tile_kernel(MxArgs a) {
     constexpr bool FP4 = FMT == W4A8_MX_FP4;
     constexpr int THREADS = 64 * WN, BM = 16 * MT;
@@ -498,7 +498,6 @@ static void launch_tile_v(const MxArgs& a, MxTile v, hipStream_t s) {
 
 void launch_mx_tile(const MxArgs& a, int fmt, bool pair, MxTile v, hipStream_t s) {
     if (fmt == W4A8_MX_FP4) pair ? launch_tile_v<W4A8_MX_FP4, true>(a, v, s) : launch_tile_v<W4A8_MX_FP4, false>(a, v, s);
-    else if (fmt == MX_FP8_EXACT) pair ? launch_tile_v<MX_FP8_EXACT, true>(a, v, s) : launch_tile_v<MX_FP8_EXACT, false>(a, v, s);
     else pair ? launch_tile_v<W4A8_MX_FP8, true>(a, v, s) : launch_tile_v<W4A8_MX_FP8, false>(a, v, s);
 }
 
