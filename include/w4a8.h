@@ -648,7 +648,7 @@ int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* 
                      size_t expert_stride, int K, int N, void* Y, int ldy, int out_dtype, void* stream);
 
 /* Grouped gate/up product with the gated activation in its epilogue, H[r, c] = silu(g) u from the float32
- * sums (silu(g) is good to 2^-22 + |g| 2^-24 of itself, and 0 for g < -88).
+ * sums (silu(g) is good to 2^-22 + |g| 2^-24 of itself, and 0 where exp(g) is below 2^-126: g < -87.3).
  *   blobs   packed [2I, K]: the I gate channels, then the I up channels; I % 16 == 0 (EINVAL)
  *   H       device [rows, I] bfloat16 or float16 (out_dtype), row stride ldh
  * Other arguments and errors as w4a8_moe_gemm_mx. */

@@ -121,10 +121,11 @@ __device__ __forceinline__ v4f mx_mfma(const v4i w, const MxOperand<FMT>& x, v4f
 }
 
 // silu(g) = g / (1 + exp(-g)) with v_exp_f32 and v_rcp_f32: the exponent's product is rounded once, which costs |g| 2^-24 of the
-// result (5e-6 at g = -80), well inside the half step of the 16-bit and the quantized outputs it goes to.  Past g = -88 the
-// exponential overflows and the result is 0.
+// result (5e-6 at g = -80), well inside the half step of the 16-bit and the quantized outputs it goes to.  Where exp(g) is below
+// 2^-126 (g < -87.3) the reciprocal is 0, and the result -0, also of g = -Inf.
 __device__ __forceinline__ float mx_silu(float g) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269502f));
+    const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269502f));
+    return r == 0.0f ? -0.0f : g * r;
 }
 
 // Four neighbouring outputs of one row, of which n (1..4) exist.
