@@ -702,7 +702,7 @@ typedef struct {
  *   post_w, w     device float32 [H]
  *   residual_out  row stride ldo, or NULL (not stored); may be residual itself
  *   Y             row stride ldy, or NULL (r' only; w is not read)
- * Any H up to 65536 (EUNSUPPORTED beyond, and for M > 2^22), rows aligned to their element.  M == 0 is a
+ * Any H up to 65536 (EUNSUPPORTED beyond, for M > 2^22, and for M = 2^22 with H > 8192), rows aligned to their element.  M == 0 is a
  * no-op.  EINVAL: types, strides below H, eps negative or not finite, alpha not finite, NULL X, no output. */
 int w4a8_norm_residual(const void* X, int dtype, int ldx, const void* residual, int res_dtype, int ldr,
                        const void* gate, int ldg, const float* post_w, const float* w, const w4a8_norm_desc* d,

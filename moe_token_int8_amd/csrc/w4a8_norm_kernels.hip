@@ -200,7 +200,7 @@ static bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintp
 static bool norm_type(int dt) { return dt == W4A8_BF16 || dt == W4A8_F16 || dt == W4A8_F32; }
 static size_t type_size(int dt) { return dt == W4A8_F32 ? 4 : 2; }
 
-constexpr int NORM_MAX_H = 65536, NORM_MAX_ROWS = 1 << 22;      // a row fits 1024 threads; less than 2^32 work-items
+constexpr int NORM_MAX_H = 65536, NORM_MAX_ROWS = 1 << 22;      // a row fits 1024 threads
 
 static int run_norm(const void* X, int dtype, int ldx, const void* res, int res_dtype, int ldr, const void* gate, int ldg,
                     const float* post_w, const float* w, const w4a8_norm_desc* d, int M, int H, void* res_out, int ldo, void* Y,
@@ -212,6 +212,7 @@ static int run_norm(const void* X, int dtype, int ldx, const void* res, int res_
         return W4A8_EINVAL;
     if (fmt == W4A8_QUANT_INT8 && H % 16) return W4A8_EINVAL;
     if (H > NORM_MAX_H || M > NORM_MAX_ROWS) return W4A8_EUNSUPPORTED;
+    if ((long long)M * (H > 8192 ? 1024 : 256) >= (1ll << 32)) return W4A8_EUNSUPPORTED;    // work-items of the launch (see launch_norm)
     if (M == 0) return W4A8_OK;
     if (!X || (fmt == NORM_NONE ? !res_out : !Y || !w) || (fmt >= 0 && !sx)) return W4A8_EINVAL;
     const size_t es = type_size(dtype), rs = type_size(res_dtype);
