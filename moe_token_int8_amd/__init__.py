@@ -931,6 +931,8 @@ def _norm_args(t, dev: int, X, residual, d: NormDesc, w, residual_out, post_w, g
     """Checked arguments of the norm calls, up to and including the row stride of residual_out."""
     shape = X.shape
     M, H = shape
+    if M | H > _INT_MAX:
+        _check_int32(M, H)
     if dev != (t.device() if dev >= 0 else t.current()) or not _norm_row(t, dev, w, H) or not _norm_row(t, dev, post_w, H):
         _refuse((X, w, post_w), what="w and post_w must be contiguous float32 [H]")
     res, ldr, out, ldo, kind = None, H, None, H, X
