@@ -346,6 +346,16 @@ static int check_out(const void* Y, int ldy, int N, int out, bool f32) {
     return W4A8_OK;
 }
 
+// Sizes of a layer.
+static int check_layer(int T, int k, int H, int I, int E, int fmt) {
+    if (T < 0 || k <= 0 || E <= 0 || E > 1024 || H <= 0 || I <= 0) return W4A8_EINVAL;
+    if (I % 16 || (fmt != W4A8_MX_FP4 && fmt != W4A8_MX_FP8)) return W4A8_EINVAL;
+    if (H > MX_MAX_K || I > MX_MAX_N / 2 || (long long)T * k > MX_MAX_ROWS) return W4A8_EUNSUPPORTED;
+    if ((long long)T * ((H + 1023) / 1024) >= (1ll << 24)) return W4A8_EUNSUPPORTED;    // work-items of the sum: less than 2^32
+    const int st = mx_check_weights(2 * I, H);
+    return st ? st : mx_check_weights(H, I);
+}
+
 static MxArgs mx_args(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k, const int32_t* offsets, int E,
                       int rows, int src_rows, const void* W, size_t stride, int K, int width) {
     MxArgs a;
@@ -472,23 +482,15 @@ int w4a8_moe_gemm_silu_mx_quant(const void* Xq, const uint8_t* sx, int fmt, cons
 }
 
 size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt) {
-    if (T < 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0 || H > MX_MAX_K || I > MX_MAX_N / 2 || (long long)T * k > MX_MAX_ROWS ||
-        (fmt != W4A8_MX_FP4 && fmt != W4A8_MX_FP8))
-        return 0;
-    return mx_layer_ws(T, k, H, I, E, fmt, ~size_t(0)).total;
+    return check_layer(T, k, H, I, E, fmt) ? 0 : mx_layer_ws(T, k, H, I, E, fmt, ~size_t(0)).total;
 }
 
 int w4a8_moe_forward_mx(const void* X, const int32_t* ids, const float* w, int T, int k, int E, int fmt, const void* gu, size_t gu_stride,
                         const void* dn, size_t d_stride, int H, int I, void* ws, size_t ws_bytes, void* out, void* stream) {
-    if (T < 0 || k <= 0 || E <= 0 || E > 1024 || H <= 0 || I <= 0) return W4A8_EINVAL;
-    if (I % 16 || (fmt != W4A8_MX_FP4 && fmt != W4A8_MX_FP8)) return W4A8_EINVAL;
-    if (H > MX_MAX_K || I > MX_MAX_N / 2 || (long long)T * k > MX_MAX_ROWS) return W4A8_EUNSUPPORTED;
-    int st = mx_check_weights(2 * I, H);
-    if (st || (st = mx_check_weights(H, I))) return st;
-    if (T == 0) return W4A8_OK;
+    int st = check_layer(T, k, H, I, E, fmt);
+    if (st || T == 0) return st;
     if (!X || !ids || !w || !ws || !out || !aligned_to(X, 2) || !aligned_to(out, 2) || !aligned_to(ids, 4) || !aligned_to(w, 4))
         return W4A8_EINVAL;
-    if ((long long)T * ((H + 1023) / 1024) >= (1ll << 24)) return W4A8_EUNSUPPORTED;    // less than 2^32 work-items
     const MxLayerWs L = mx_layer_ws(T, k, H, I, E, fmt, ws_bytes);
     if (L.slice == 0) return W4A8_ESIZE;
     if (!aligned_to(ws, 256)) return W4A8_EINVAL;
