@@ -634,7 +634,7 @@ int w4a8_mx_unpack_codes(const void* blob, int N, int K, uint8_t* codes, uint8_t
  *   Xq, sx, fmt  device activations [M, K], W4A8_MX_FP4 or W4A8_MX_FP8
  *   blob         device, packed [N, K]
  *   Y            device [M, N] bfloat16, float16 or float32 (out_dtype), row stride ldy; any N
- * M == 0 is a no-op.  EUNSUPPORTED: M > 2^24. */
+ * M == 0 is a no-op.  EUNSUPPORTED: M > 2^24, (M / 32 + 1) ceil(N / 64) >= 2^32. */
 int w4a8_mx_gemm(const void* Xq, const uint8_t* sx, int fmt, int M, const void* blob, int K, int N, void* Y,
                  int ldy, int out_dtype, void* stream);
 
@@ -642,7 +642,8 @@ int w4a8_mx_gemm(const void* Xq, const uint8_t* sx, int fmt, int M, const void* 
  *   gather, k, expert_offsets, E, rows, src_rows   as w4a8_moe_gemm_w8a8
  *   blobs, expert_stride   E packed [N, K], expert_stride bytes apart (a multiple of 16)
  * Rows at or past expert_offsets[E] are not written, nor is Y past column N.  A gather entry that names no
- * row gives a row of zeros.  E <= 1024 (EINVAL); EUNSUPPORTED: rows or src_rows > 2^24. */
+ * row gives a row of zeros.  E <= 1024 (EINVAL); EUNSUPPORTED: rows or src_rows > 2^24,
+ * (rows / 32 + E) ceil(columns of a blob / 64) >= 2^32. */
 int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* gather, int k,
                      const int32_t* expert_offsets, int E, int rows, int src_rows, const void* blobs,
                      size_t expert_stride, int K, int N, void* Y, int ldy, int out_dtype, void* stream);

@@ -331,6 +331,8 @@ static int check_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* g
     const int st = mx_check_weights(width, K);
     if (st) return st;
     if (rows > MX_MAX_ROWS || src_rows > MX_MAX_ROWS) return W4A8_EUNSUPPORTED;
+    // the tile kernel numbers its tiles, of 32 rows (and one more for each expert) by 64 columns of the weights or larger, in 32 bits
+    if ((long long)(rows / 32 + E) * ((width + 63) / 64) >= (1ll << 32)) return W4A8_EUNSUPPORTED;
     if (rows == 0) return W4A8_OK;
     if (!Xq || !sx || !W || (E > 1 && !offsets)) return W4A8_EINVAL;
     if (gather ? (k <= 0 || src_rows == 0) : src_rows < rows) return W4A8_EINVAL;

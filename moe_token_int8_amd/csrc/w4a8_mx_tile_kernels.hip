@@ -139,10 +139,9 @@ void mx_tile_kernel(MxArgs a) {
         if (a.E == MXT_MAX_E && tid == THREADS - 1) first[MXT_MAX_E] = incl;
         __syncthreads();
     }
-    // Workgroups take the tiles in turn.  Within an expert, panels of MXT_PANEL row tiles go through all columns together.  (In 32
-    // bits: 2^24 rows in tiles of 32, and one more for each of 1024 experts, by 2^20 columns in blocks of 64 or more.)  Consecutive
-    // tiles for a workgroup, which keep its weights from one to the next, share less in L2: 4153 tokens x 6 of 64 experts, 4096 x
-    // 2815 320 us in place of 270.
+    // Workgroups take the tiles in turn.  Within an expert, panels of MXT_PANEL row tiles go through all columns together.  (The calls
+    // refuse what has 2^32 tiles or more.)  Consecutive tiles for a workgroup, which keep its weights from one to the next, share less
+    // in L2: 4153 tokens x 6 of 64 experts, 4096 x 2815 320 us in place of 270.
     const unsigned total = unsigned(first[a.E]) * unsigned(ncb);
     // blocks go to the 8 XCDs in turn: the blocks of one XCD take neighbouring tiles, which share rows or columns in its L2
     const unsigned nblk = gridDim.x, per = nblk / 8;
