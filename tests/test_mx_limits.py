@@ -44,7 +44,7 @@ if lib.hipGetDeviceCount(ctypes.byref(n)) == 0 and n.value > 0:
     sys.exit(77)
 out = []
 for op, E, rows, N in json.loads(sys.argv[1]):
-    a = (f, f, 0, None, 1, f, E, rows, rows, f, L.w4a8_mx_packed_size(64, 2 * N if "silu" in op else N), 64, N)
+    a = (f, f, 0, None, 1, f, E, rows, rows, f, L.w4a8_mx_packed_size(64, 2 * N if op in ("silu", "quantized") else N), 64, N)
     out.append(lib.w4a8_mx_gemm(f, f, 0, rows, f, 64, N, f, N, 1, None) if op == "dense" else lib.w4a8_moe_gemm_mx(*a, f, N, 1, None) if op == "moe"
                else lib.w4a8_moe_gemm_silu_mx(*a, f, N, 0, None) if op == "silu" else lib.w4a8_moe_gemm_silu_mx_quant(*a, 0, f, f, None))
 print(json.dumps(out))
