@@ -695,7 +695,8 @@ typedef struct {
  *   u  = X rsqrt(mean(X^2) + eps_post) post_w, or X where post_w is NULL
  *   r' = residual + alpha gate u, rounded to res_dtype       -> residual_out
  *   h  = r' rsqrt(mean(r'^2) + eps) w, rounded to dtype      -> Y
- * in float32 (squares past its range make the mean infinite and h 0 or NaN).
+ * in float32 (squares past its range make the mean infinite and h 0 or NaN).  A call repeats bit for bit; the
+ * order of a row's sums depends on H and on whether M exceeds 512.
  *   X             device [M, H] of dtype (bfloat16, float16 or float32), row stride ldx
  *   residual      device [M, H] of res_dtype, row stride ldr, or NULL (zeros: with alpha = 1 and no gate the
  *                 call is the norm of X alone)
@@ -710,8 +711,8 @@ int w4a8_norm_residual(const void* X, int dtype, int ldx, const void* residual, 
                        int M, int H, void* residual_out, int ldo, void* Y, int ldy, void* stream);
 
 /* The same with h quantized in place of stored: the codes and scales that w4a8_mx_quant (fmt W4A8_MX_FP4 or
- * W4A8_MX_FP8) or w4a8_quant_act (W4A8_QUANT_INT8: int8 [M, H] and float32 [M], H % 16 == 0) give for h, bit
- * for bit.  Xq 16-byte, sx 4-byte aligned. */
+ * W4A8_MX_FP8) gives for h, or by the rule of w4a8_quant_act (W4A8_QUANT_INT8: int8 [M, H] and float32 [M],
+ * H % 16 == 0; h of any type), bit for bit.  Xq 16-byte, sx 4-byte aligned. */
 int w4a8_norm_residual_quant(const void* X, int dtype, int ldx, const void* residual, int res_dtype, int ldr,
                              const void* gate, int ldg, const float* post_w, const float* w,
                              const w4a8_norm_desc* d, int M, int H, void* residual_out, int ldo, int fmt, void* Xq,
