@@ -93,3 +93,37 @@ def test_layer_in_slices(T, k, E, H, I, fmt):
     for size in (of_16_bit_outputs(T, k, H, I, E), need, need + 128 * 4 * T * k, full - 256, need + (full - need) // 3):
         if size >= need:
             assert torch.equal(layer(size), out), size
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("T", [3, 130, 900])
+def test_layer_in_slices_captured(T, fmt):
+    """A layer in slices captured into a graph, replayed with its own eager work between on another stream with another workspace, on new
+    inputs each time."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    k, E, H, I = 4, 12, 700, 112
+    GU, DN, _, x, logits = layer_inputs(T, k, E, H, I, fmt, T)
+    ids, w = logits.topk(k, 1).indices.to(torch.int32).contiguous(), torch.rand(T, k, device=DEV)
+    size = least(T, k, H, I, E, fmt) + 192 * 4 * T * k                    # three slices of 256 columns
+    ws, full = (torch.empty(n, dtype=torch.uint8, device=DEV) for n in (size, L.w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt)))
+    out, eager = torch.empty_like(x), torch.empty_like(x)
+
+    def layer(work, o):
+        L.w4a8_moe_forward_mx(x, ids, w, E, fmt, GU, GU.shape[1], DN, DN.shape[1], I, work, o)
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        layer(ws, out)
+    for i in range(4):
+        x *= -1.25 if i % 2 else 0.7
+        ids.copy_(ids.flip(0))
+        out.fill_(SENTINEL), ws.fill_(0xff)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            layer(full, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
