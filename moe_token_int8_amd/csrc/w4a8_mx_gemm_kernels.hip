@@ -22,8 +22,8 @@ namespace w4a8 {
 // columns, then the 2 matching ones of up columns) over all of K.  The waves share the steps of 128 k: wave w takes w, w + 8, ...;
 // weights and activations go from memory to registers in the layout of the MFMA operands (a step of a weight tile is one
 // contiguous KiB), with no LDS and no barrier in the loop, two of a wave's steps in flight.  The 8 partial sums are added in wave
-// order through LDS, so a call repeats bit for bit.  8 x 4096 x 14336 in fp8: 8.3 us (31 MB: 5 at the rate of a large read); one token's
-// 6 experts, 4096 x 1408 gate/up: 11.9 (37 MB: 6), of which the loads of activations take 1.4 us and 1.2 the half of the steps.
+// order through LDS, so a call repeats bit for bit.  8 x 4096 x 14336 in fp8: 8.5 us (31 MB: 5 at the rate of a large read); one token's
+// 6 experts, 4096 x 1408 gate/up: 12.9 (37 MB: 6), of which the loads of activations take 1.4 us and the second MFMA of a step 1.
 // (Two row tiles a workgroup read the weights once for 32 rows, but the tile kernel does that faster: 32 rows for each of 64
 // experts, 1408 x 4096 fp4 73 against 51 us.  Three steps in flight: 9.7 in place of 8.4.)
 constexpr int MXS_WAVES = 8, MXS_ROWS = 16, MXS_TILES = 4;
@@ -391,12 +391,12 @@ static int run_mx(const char* call, MxArgs& a, int N, int fmt, bool pair, int K,
     return launched();
 }
 
-// Workspace of the layer: pieces in order, each 256-byte aligned.
 // Up to so many routed rows one launch makes the codes of the tokens and the order of the rows.  A whole layer of H 2048, I 1408,
-// k 8, fp8, two launches against one, us: 64 experts, 1 token 21.3 / 19.1, 256 tokens 88 / 85, 512 tokens 120 / 122; 8 experts, 256
-// tokens 51.5 / 51.3, 512 tokens 76 / 82; 256 experts, 256 tokens 248 / 239.
+// k 8, fp8, two launches against one, us: 64 experts, 1 token 22.8 / 21.2, 256 tokens 112 / 109, 512 tokens 148 / 150; 8 experts, 256
+// tokens 66.3 / 65.7, 512 tokens 113 / 120.
 constexpr int MX_ROUTE_ROWS = 2048;
 
+// Workspace of the layer: pieces in order, each 256-byte aligned.
 struct MxLayerWs {
     size_t xq, sx, rows, offs, inv, hq, sh, yd, total;
     int slice;                // columns of the experts' outputs that yd holds at a time

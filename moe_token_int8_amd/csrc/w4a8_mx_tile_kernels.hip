@@ -16,10 +16,11 @@ namespace w4a8 {
 // The packed weights are in operand order, so they go from memory straight to registers, 4 KiB a wave and step of 128 k, two
 // steps ahead (DEEP: five), each to one wave.  Only the activations pass through LDS: in stages of 128 bytes a row (two steps of fp4,
 // one of fp8), copied without registers (buffer_load ... lds), three stages deep (DEEP, fp8: six), with a stage's scale bytes behind
-// its codes.  DEEP is for launches of few tiles, whose time is one chain of steps over K, each waiting for its loads: 2048 x 14336 x
-// 4096 in fp8, tiles of 64 x 256: 129 -> 96 us; 192 x 14336 x 4096, tiles of 32 x 256 two ahead 56, of 32 x 128 five ahead 34.
+// its codes.  DEEP is for launches of few tiles, whose time is one chain of steps over K, each waiting for its loads: 192 x 14336 x 4096 in
+// fp4, tiles of 32 x 128: 31 -> 26 us (fp8, whose chain is one of MFMAs: 62 either way).
 //
-// What bounds it: the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
+// What bounds it: in fp8 the MFMAs, two for each step of 16 x 16 (see mx_mfma), whose rate alone is 2.2 PFLOP/s: 8192^3 takes 668 us (1.65
+// PFLOP/s), with one MFMA, which loses small parts, 332.  In fp4 the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
 // cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 102 us (4.7 PFLOP/s; MFMAs alone on
 // registers reach 6.2), 83 without the memory operations in the loop, 99 without the copies, 94 without the weights, unchanged with
 // half the LDS reads.  256 x 256 tiles, where two waves load the same weights, took 108; touching the weights' lines 8 steps ahead,
