@@ -95,8 +95,8 @@ __device__ __forceinline__ v4i mx_large(const v4i x) {
     v4i r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // a byte of the permutation is 0 or 255 by the sign of byte 1 or 3 of either operand (selectors 8 to 11)
-        r[i] = x[i] & int(__builtin_amdgcn_perm(uint32_t(x[i]) << 1, uint32_t(x[i]) << 9, 0x0b090a08u));
+        // v_perm_b32 makes 255 of a selector past 12 and takes byte 0 of its operand, which is 0, for 0
+        r[i] = x[i] & int(__builtin_amdgcn_perm(0u, 0u, uint32_t(x[i]) & 0x40404040u));
     }
     return r;
 }

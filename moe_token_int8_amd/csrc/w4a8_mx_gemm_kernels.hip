@@ -220,14 +220,14 @@ static void launch_stream(const MxArgs& a, hipStream_t s) {
 // about E (1 - exp(-rows / E)) have any, and each ends in a row tile that is half empty.  n tiles meet c n / 256 times on a compute
 // unit (c > 1: a launch that fits does not spread evenly).  Streaming tiles, two of which share a unit, take o and l a step.  Of MFMA
 // tiles `per` share one, a step takes l, or thr for each of them.  Either reads the weights at bw TB/s, which adds up with the steps as
-// far as a norm of third powers says.  Fitted to 414 shapes for fp4 and 207 for fp8 (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 ..
-// 1024 rows, evenly or skewed, K 300 .. 14336), of which the choice loses 2 % in the mean against the best of all, 27 % (fp8 22) at
-// worst; an fp8 step has twice the MFMAs of an fp4 one.  Measured, us, fp8, streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x
+// far as a norm of third powers says.  Fitted to 414 shapes for fp4 and 243 for fp8 (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 ..
+// 1024 rows, evenly or skewed, K 300 .. 14336), of which the choice loses 2 % (fp8 1.3) in the mean against the best of all, 27 %
+// (fp8 20) at worst; an fp8 step has twice the MFMAs of an fp4 one.  Measured, us, fp8, streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x
 // 256 and 128 x 512:
-//   16 x 4096 x 14336                     10 /  21,  23,  35,  60,  83       128 x 4096 x 14336            40 /  28,  27,  36,  61,  86
-//   256 x 14336 x 4096                     - /  72,  70, 105, 195, 272       2048 x 14336 x 4096            - / 189, 183, 164, 275, 280
-//   2048 x 4096 x 14336                    - / 204, 214, 193, 183, 181
-//   4 rows for each of 256, 2048 x 7168  426 / 327, 334, 388, 601, 606       64 rows for each, the same     - / 678, 636, 602, 744, 743
+//   16 x 4096 x 14336                      9 /  20,  23,  33,  57,  78       128 x 4096 x 14336            36 /  27,  26,  35,  58,  80
+//   256 x 14336 x 4096                     - /  65,  67, 101, 182, 253       2048 x 14336 x 4096            - / 186, 183, 162, 253, 258
+//   2048 x 4096 x 14336                    - / 201, 207, 185, 176, 173
+//   4 rows for each of 256, 2048 x 7168  405 / 326, 333, 379, 566, 573       64 rows for each, the same     - / 682, 633, 598, 730, 737
 enum MxKernel { MXK_STREAM, MXK_SMALL, MXK_TILE32, MXK_TILE64, MXK_TILE128, MXK_WIDE, MXK_KERNELS };
 
 static MxKernel choose_mx(const MxArgs& a, int N, bool fp4, bool pair, MxKernel first) {
@@ -235,9 +235,9 @@ static MxKernel choose_mx(const MxArgs& a, int N, bool fp4, bool pair, MxKernel 
         int rows, cols, per;
         double o, l, thr, bw, c;
     };
-    static const Rate rates[2][MXK_KERNELS] = {{{16, 64, 2, 2.30, 0.137, 0.000, 7.48, 1.85}, {32, 128, 4, 1.52, 0.498, 0.243, 5.77, 1.83},
-                                                {32, 256, 4, 1.06, 0.576, 0.536, 5.82, 1.19}, {64, 256, 2, 3.53, 0.006, 0.749, 6.59, 2.00},
-                                                {128, 256, 2, 3.52, 1.884, 1.278, 7.80, 1.39}, {128, 512, 1, 6.16, 0.034, 2.388, 7.37, 2.00}},
+    static const Rate rates[2][MXK_KERNELS] = {{{16, 64, 2, 2.30, 0.163, 0.000, 6.80, 1.67}, {32, 128, 4, 1.78, 0.449, 0.254, 6.35, 1.83},
+                                                {32, 256, 4, 0.93, 0.560, 0.513, 5.95, 1.22}, {64, 256, 2, 3.07, 0.006, 0.749, 6.14, 2.00},
+                                                {128, 256, 2, 3.57, 1.884, 1.278, 6.58, 1.44}, {128, 512, 1, 5.74, 0.032, 2.388, 7.57, 1.99}},
                                                {{16, 64, 2, 1.55, 0.108, 0.000, 7.80, 2.00}, {32, 128, 4, 0.00, 0.196, 0.171, 5.43, 1.46},
                                                 {32, 256, 4, 0.00, 0.275, 0.301, 5.69, 1.33}, {64, 256, 2, 1.81, 0.106, 0.301, 5.40, 1.71},
                                                 {128, 256, 2, 3.40, 0.195, 0.446, 6.00, 1.73}, {128, 512, 1, 5.24, 0.351, 0.803, 6.04, 2.00}}};

@@ -19,12 +19,14 @@ namespace w4a8 {
 // its codes.  DEEP is for launches of few tiles, whose time is one chain of steps over K, each waiting for its loads: 192 x 14336 x 4096 in
 // fp4, tiles of 32 x 128: 31 -> 26 us (fp8, whose chain is one of MFMAs: 62 either way).
 //
-// What bounds it: in fp8 the MFMAs, two for each step of 16 x 16 (see mx_mfma), whose rate alone is 2.2 PFLOP/s: 8192^3 takes 668 us (1.65
-// PFLOP/s), with one MFMA, which loses small parts, 332.  In fp4 the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640
-// cycles of the MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 102 us (4.7 PFLOP/s; MFMAs alone on
-// registers reach 6.2), 83 without the memory operations in the loop, 99 without the copies, 94 without the weights, unchanged with
-// half the LDS reads.  256 x 256 tiles, where two waves load the same weights, took 108; touching the weights' lines 8 steps ahead,
-// one load of 64 lines, 115 to 130 (64 cycles of the same path); another order of steps for workgroups that share data, no change.
+// What bounds it: in fp8 the MFMAs, two for each step of 16 x 16 (see mx_mfma; 2.2 PFLOP/s by themselves), and the split of the operands
+// between them, which every wave does for all rows: MFMAs are busy for 59 % of a prompt's cycles.  8192^3 takes 653 us (1.68 PFLOP/s),
+// with one MFMA, which loses small parts, 332.
+// In fp4 the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640 cycles of the
+// MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 102 us (4.7 PFLOP/s; MFMAs alone on registers reach
+// 6.2), 83 without the memory operations in the loop, 99 without the copies, 94 without the weights, unchanged with half the LDS
+// reads.  256 x 256 tiles, where two waves load the same weights, took 108; touching the weights' lines 8 steps ahead, one load of
+// 64 lines, 115 to 130 (64 cycles of the same path); another order of steps for workgroups that share data, no change.
 //
 // vmcnt counts in the order of issue, so what is issued when is fixed: a step requests the weights of the step AHEAD steps on; the
 // first step of a stage then requests the activations of the stage NST - 1 stages on.  One barrier a stage, before the last
