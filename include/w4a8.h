@@ -649,7 +649,7 @@ int w4a8_moe_gemm_mx(const void* Xq, const uint8_t* sx, int fmt, const int32_t* 
                      size_t expert_stride, int K, int N, void* Y, int ldy, int out_dtype, void* stream);
 
 /* Grouped gate/up product with the gated activation in its epilogue, H[r, c] = silu(g) u from the float32
- * sums (silu(g) is good to 2^-22 + |g| 2^-24 of itself, and 0 where exp(g) is below 2^-126: g < -87.3).
+ * sums (silu(g) is good to 2^-22 + |g| 2^-24 of itself, and 0 where exp(g) is below 2^-126, g < -87.3).
  *   blobs   packed [2I, K]: the I gate channels, then the I up channels; I % 16 == 0 (EINVAL)
  *   H       device [rows, I] bfloat16 or float16 (out_dtype), row stride ldh
  * Other arguments and errors as w4a8_moe_gemm_mx. */
@@ -671,9 +671,10 @@ size_t w4a8_moe_mx_workspace_size(int T, int k, int H, int I, int E, int fmt);
  * in float32 and rounded once.
  *   X_bf16     device bfloat16 [T, H]; topk_ids / topk_w device [T, k] (ids outside [0, E) add nothing)
  *   gu_blobs   E packed [2I, H], gate channels first; d_blobs E packed [H, I]; strides in bytes
- *   workspace  device, 256-aligned, w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt) bytes, or less: the last of it, 4 T k H, are
- *              the experts' outputs, and where only a part of their columns fits, 64 at least (ESIZE), the down product
- *              and the sum are made by slices of columns, at two launches a slice, with the same bits
+ *   workspace  device, 256-aligned, w4a8_moe_mx_workspace_size(T, k, H, I, E, fmt) bytes, or less: its last
+ *              4 T k H bytes are the experts' outputs, and where only a part of their columns fits (64 at
+ *              least, ESIZE), the down product and the sum are made by slices of columns, at two launches a
+ *              slice, with the same bits
  *   out_bf16   device bfloat16 [T, H]
  * I % 16 == 0 (EINVAL); T*k <= 2^24 and T ceil(H / 1024) < 2^24 (EUNSUPPORTED).  Every check of the chained
  * steps runs before the first launch. */
@@ -704,8 +705,8 @@ typedef struct {
  *   post_w, w     device float32 [H]
  *   residual_out  row stride ldo, or NULL (not stored); may be residual itself
  *   Y             row stride ldy, or NULL (r' only; w is not read)
- * Any H up to 65536 (EUNSUPPORTED beyond, for M > 2^22, and for M = 2^22 with H > 8192), rows aligned to their element.  M == 0 is a
- * no-op.  EINVAL: types, strides below H, eps negative or not finite, alpha not finite, NULL X, no output. */
+ * Any H up to 65536 (EUNSUPPORTED beyond, for M > 2^22, and for M = 2^22 with H > 8192), rows aligned to
+ * their element.  M == 0 is a no-op.  EINVAL: types, strides below H, eps negative or not finite, alpha not finite, NULL X, no output. */
 int w4a8_norm_residual(const void* X, int dtype, int ldx, const void* residual, int res_dtype, int ldr,
                        const void* gate, int ldg, const float* post_w, const float* w, const w4a8_norm_desc* d,
                        int M, int H, void* residual_out, int ldo, void* Y, int ldy, void* stream);

@@ -20,7 +20,7 @@ namespace w4a8 {
 // fp4, tiles of 32 x 128: 31 -> 26 us (fp8, whose chain is one of MFMAs: 62 either way).
 //
 // What bounds it: in fp8 the MFMAs, two for each step of 16 x 16 (see mx_mfma; 2.2 PFLOP/s by themselves), and the split of the operands
-// between them, which every wave does for all rows: MFMAs are busy for 59 % of a prompt's cycles.  8192^3 takes 653 us (1.68 PFLOP/s),
+// between them, which every wave does for all rows: MFMAs are busy for 63 % of a prompt's cycles.  8192^3 takes 653 us (1.68 PFLOP/s),
 // with one MFMA, which loses small parts, 332.
 // In fp4 the path of the vector memory, 64 bytes a cycle and compute unit.  A 128 x 512 step of fp4 moves 40 KiB, 640 cycles of the
 // MFMAs' 1024, and each scale of a row costs a cycle.  4096 x 14336 x 4096 in fp4: 102 us (4.7 PFLOP/s; MFMAs alone on registers reach
