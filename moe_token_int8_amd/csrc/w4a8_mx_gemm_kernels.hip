@@ -155,7 +155,8 @@ __global__ __launch_bounds__(512, 4) void mx_stream_kernel(MxArgs a, int ncb, in
             }
         };
         // (fp8 pairs: loads held back until the operands of the step before are free; moved ahead of them they spilled registers, 256 rows
-        // of 64 experts, 4096 x 1408 gate/up, 86 us in place of 71.  Unpaired, held back, 3072 rows 141 in place of 117)
+        // of 64 experts, 4096 x 1408 gate/up, 86 us in place of 71.  Unpaired, held back, 512 tokens x 6 of 64, 1408 x 4096,
+        // 141 in place of 117)
         for (int s = wave; s < a.K1; s += 2 * MXS_WAVES) {
             multiply(s0);
             if constexpr (PAIR && FMT != W4A8_MX_FP4) __builtin_amdgcn_sched_barrier(0);
@@ -222,8 +223,8 @@ static void launch_stream(const MxArgs& a, hipStream_t s) {
 // tiles `per` share one, a step takes l, or thr for each of them.  Either reads the weights at bw TB/s, which adds up with the steps as
 // far as a norm of third powers says.  Fitted to 414 shapes for fp4 and 243 for fp8 (dense 1 .. 8192 rows, 8 .. 256 experts of 0.1 ..
 // 1024 rows, evenly or skewed, K 300 .. 14336), of which the choice loses 2 % (fp8 1.3) in the mean against the best of all, 27 %
-// (fp8 20) at worst; an fp8 step has twice the MFMAs of an fp4 one.  Measured, us, fp8, streaming / tiles of 32 x 128, 32 x 256, 64 x 256, 128 x
-// 256 and 128 x 512:
+// (fp8 20) at worst; an fp8 step has twice the MFMAs of an fp4 one.  Measured, us, fp8, streaming / tiles of 32 x 128, 32 x 256, 64 x
+// 256, 128 x 256 and 128 x 512:
 //   16 x 4096 x 14336                      9 /  20,  23,  33,  57,  78       128 x 4096 x 14336            36 /  27,  26,  35,  58,  80
 //   256 x 14336 x 4096                     - /  65,  67, 101, 182, 253       2048 x 14336 x 4096            - / 186, 183, 162, 253, 258
 //   2048 x 4096 x 14336                    - / 201, 207, 185, 176, 173
